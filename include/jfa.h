@@ -59,7 +59,9 @@ typedef enum {
   JFA_ERR_WORKSPACE = 3,   /* workspace missing, too small or misaligned */
   JFA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (launch, tensor-map encode) */
   JFA_ERR_BAD_OFFSETS = 5, /* device: offsets not 0-based, not monotone, or last != total (also kind-2 bias block offsets) */
-  JFA_ERR_TIMEOUT = 6      /* device: a bounded pipeline wait ran out; outputs unspecified */
+  JFA_ERR_TIMEOUT = 6,     /* device: a bounded pipeline wait ran out; outputs unspecified */
+  JFA_ERR_BAD_PAGES = 7    /* device: a page table entry that a call needs is not a page of the cache, or a
+                              token lies past the table's last page */
 } jfa_status;
 
 /* Additive attention bias (the user-defined biases of "Jagged Flash Attention
@@ -144,9 +146,69 @@ jfa_status jfa_forward_noalloc(const void* q, const void* k, const void* v, cons
                                const jfa_bias* bias, float scale, int causal, void* out, float* lse,
                                jfa_stream_t stream);
 
+/* ---- Paged key/value cache: serving one new token at a time.
+ *
+ * k, v: bf16 [num_pages][H_kv][page_size][d], the caller's, 16-byte aligned; token p of
+ * sequence b lives in row p % page_size of page page_table[b * max_pages + p / page_size].
+ * page_size in {16, 32, 64, 128}; d in {64, 128}; num_pages * H_kv * page_size < 2^31 and
+ * max_pages * page_size < 2^31.  page_table: device int32 [B][max_pages]; entries that a
+ * call does not need may hold anything.  lengths: device int32 [B], tokens of each
+ * sequence.  Pages may be shared by sequences for reading. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t num_pages;
+  int H_kv, page_size, d;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* lengths;
+  int B;
+} jfa_cache;
+
+/* Bytes of workspace the two calls below need (256-byte aligned, zero before its first use;
+ * every call leaves what it needs zero, zero again).  Returns 0 on invalid sizes. */
+size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
+
+/* Append new tokens, keys rotated by their position on the way.  Sequence b's new tokens are
+ * rows [offsets[b], offsets[b+1]) of k and v (device int64 [B+1], offsets[0] = 0,
+ * non-decreasing, offsets[B] <= total: rows behind the last sequence are neither read nor
+ * written), and take positions lengths[b], lengths[b] + 1, ...  Rows of a token are H_kv
+ * (q: H) heads of d contiguous bf16; tokens k_stride (v_stride, q_stride) elements apart, so
+ * that slices of one fused projection can be given; 16-byte aligned, strides multiples of 8.
+ *
+ * Rotation: the first rot_dim (0 .. d, a multiple of 16) elements of each head of k (and q)
+ * form rot_dim / 2 pairs, pair i = (x_i, x_{i + rot_dim/2}), or (x_2i, x_2i+1) when
+ * `interleaved`, and (a, b) becomes (a cos t - b sin t, b cos t + a sin t) with
+ * t = position * frequencies[i]; `frequencies` is a HOST array of rot_dim / 2 doubles
+ * (radians per position), read during the call.  Angles are exact to 2^-32 of a turn at any
+ * position when the frequencies are.  Results are rounded to bf16 once.
+ *
+ * q (may be NULL) is rotated into q_out, contiguous [total][H][d]; with k_out non-NULL the
+ * rotated keys are also written there, contiguous [total][H_kv][d] (for the prompt's own
+ * attention).  q_out may be q and k_out may be k when those are contiguous.  lengths_out (may
+ * be NULL): device int32 [B], overwritten with lengths[b] + the number of appended tokens; it
+ * may be `lengths` itself.  Each cache row must be written by one token only.
+ *
+ * Errors on the device: malformed offsets or a negative length (JFA_ERR_BAD_OFFSETS); a token
+ * whose page is missing (JFA_ERR_BAD_PAGES; that token is not stored). */
+jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const void* q, int64_t q_stride, int H, const int64_t* offsets, int64_t total,
+                            const double* frequencies, int rot_dim, int interleaved, void* q_out, void* k_out,
+                            int32_t* lengths_out, void* workspace, size_t workspace_bytes, jfa_stream_t stream);
+
+/* Attention of each sequence's newest token over the cache: q, out bf16 [B][H][d], lse fp32
+ * [H][B]; H a multiple of H_kv, query head h reading key/value head h / (H / H_kv).  With
+ * L = lengths[b] (the newest token, at position L - 1, already appended), key j is visible iff
+ * j < L and (j >= L - window or j < sinks); window >= 1, sinks >= 0.  L = 0 gives out = 0 and
+ * lse = -inf.  Only pages that hold a visible key are looked up, and what rows hold that show
+ * no key does not matter (NaN included).  A length below 0 or above max_pages * page_size is
+ * JFA_ERR_BAD_OFFSETS, a visible key on a page outside the cache JFA_ERR_BAD_PAGES. */
+jfa_status jfa_cache_attention(const jfa_cache* cache, const void* q, int H, int window, int sinks, float scale,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, jfa_stream_t stream);
+
 /* Synchronises `stream`, then returns the first device-side error recorded in
  * `workspace` since the previous jfa_check_status (JFA_OK if none; else
- * JFA_ERR_BAD_OFFSETS, JFA_ERR_TIMEOUT or JFA_ERR_WORKSPACE) and clears it. */
+ * JFA_ERR_BAD_OFFSETS, JFA_ERR_TIMEOUT, JFA_ERR_WORKSPACE or JFA_ERR_BAD_PAGES) and clears it. */
 jfa_status jfa_check_status(void* workspace, jfa_stream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
@@ -162,7 +224,8 @@ const char* jfa_last_error(void);
 
 /* Kernel kinds for per-kernel timing. */
 enum { JFA_KERNEL_PLAN = 0, JFA_KERNEL_FORWARD = 1, JFA_KERNEL_BWD_PREPROCESS = 2, JFA_KERNEL_BWD_DKDV = 3,
-       JFA_KERNEL_BWD_DQ = 4, JFA_KERNEL_BWD_FUSED = 5, JFA_KERNEL_BWD_NSP = 6, JFA_NUM_KERNEL_KINDS = 7 };
+       JFA_KERNEL_BWD_DQ = 4, JFA_KERNEL_BWD_FUSED = 5, JFA_KERNEL_BWD_NSP = 6, JFA_KERNEL_BWD_JOIN = 7,
+       JFA_KERNEL_CACHE_APPEND = 8, JFA_KERNEL_CACHE_ATTENTION = 9, JFA_NUM_KERNEL_KINDS = 10 };
 
 /* Benchmark support (not part of the attention itself).  While enabled (process-wide),
  * every kernel launch is bracketed by two CUDA events recorded on the launch stream.

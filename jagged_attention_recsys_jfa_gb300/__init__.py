@@ -7,6 +7,8 @@ from .jfa import (  # noqa: F401
     JfaError,
     jagged_attention,
     jfa_backward,
+    jfa_cache_append,
+    jfa_cache_attention,
     jfa_check_status,
     jfa_forward,
     jfa_last_launch_count,
@@ -19,6 +21,9 @@ from .jfa import (  # noqa: F401
     KERNEL_KINDS,
     library_path,
     load_library,
+    cache_workspace_size,
+    new_cache_workspace,
+    rotary_frequencies,
     status_string,
     workspace_size,
 )

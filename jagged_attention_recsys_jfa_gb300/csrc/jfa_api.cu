@@ -5,6 +5,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <atomic>
@@ -177,6 +178,46 @@ Problem make_problem(int B, int H, int d, int64_t total_q, int64_t total_kv, con
   return p;
 }
 
+// The whole cache as [rows of one (page, head), d]: boxes of 64 columns (the 128-byte swizzle
+// span) by a page's rows, 64 at most.
+jfa_status encode_cache_map(CUtensorMap* m, const void* base, const jfa_cache& c) {
+  auto fn = encode_fn();
+  if (!fn) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled entry point not available");
+    return JFA_ERR_CUDA;
+  }
+  const cuuint64_t dims[2] = {cuuint64_t(c.d), cuuint64_t(c.num_pages) * cuuint64_t(c.H_kv) * cuuint64_t(c.page_size)};
+  const cuuint64_t strides[1] = {cuuint64_t(c.d) * 2};
+  const cuuint32_t box[2] = {64, cuuint32_t(c.page_size < 64 ? c.page_size : 64)};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled: CUresult %d", int(r));
+    return JFA_ERR_CUDA;
+  }
+  return JFA_OK;
+}
+
+jfa_status check_cache(const jfa_cache* c) {
+  if (!c || c->B < 1 || c->H_kv < 1 || c->H_kv > 4096 || c->num_pages < 1 || c->max_pages < 1) return JFA_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return JFA_ERR_UNSUPPORTED;
+  if (c->page_size != 16 && c->page_size != 32 && c->page_size != 64 && c->page_size != 128) return JFA_ERR_UNSUPPORTED;
+  if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !c->page_table || !c->lengths) return JFA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(c->lengths) & 3u) != 0)
+    return JFA_ERR_INVALID_ARG;
+  const int64_t limit = int64_t(1) << 31;
+  if (c->num_pages >= limit || c->num_pages * c->H_kv >= limit || c->num_pages * c->H_kv * c->page_size >= limit ||
+      int64_t(c->max_pages) * c->page_size >= limit)
+    return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
+
+jfa_status check_workspace_bytes(void* ws, size_t bytes, size_t need) {
+  return !ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < need ? JFA_ERR_WORKSPACE : JFA_OK;
+}
+
 jfa_status check_workspace(void* ws, size_t bytes, const WsLayout& L) {
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < L.total) return JFA_ERR_WORKSPACE;
   return JFA_OK;
@@ -311,6 +352,80 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
   return JFA_OK;
 }
 
+size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d) {
+  if (B < 1 || H_kv < 1 || H < H_kv || H > 4096 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+  return cache_workspace_bytes(B, H, H_kv, d);
+}
+
+jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                            const void* q, int64_t q_stride, int H, const int64_t* offsets, int64_t total,
+                            const double* frequencies, int rot_dim, int interleaved, void* q_out, void* k_out,
+                            int32_t* lengths_out, void* workspace, size_t workspace_bytes, jfa_stream_t stream) {
+  g_last_launches = 0;
+  jfa_status st = check_cache(cache);
+  if (st != JFA_OK) return st;
+  const int d = cache->d;
+  if (total < 0 || total >= (int64_t(1) << 31) || !offsets || (reinterpret_cast<uintptr_t>(offsets) & 7u) != 0 ||
+      (reinterpret_cast<uintptr_t>(lengths_out) & 3u) != 0)
+    return JFA_ERR_INVALID_ARG;
+  if (total > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return JFA_ERR_INVALID_ARG;
+  const int64_t kv_row = int64_t(cache->H_kv) * d;
+  if (total > 1 && (k_stride < kv_row || v_stride < kv_row || k_stride % 8 != 0 || v_stride % 8 != 0))
+    return JFA_ERR_INVALID_ARG;
+  if (q && (H < 1 || H > 4096 || !q_out || !aligned16(q) || !aligned16(q_out) ||
+            (total > 1 && (q_stride < int64_t(H) * d || q_stride % 8 != 0))))
+    return JFA_ERR_INVALID_ARG;
+  if (k_out && !aligned16(k_out)) return JFA_ERR_INVALID_ARG;
+  if ((q && q_out == q && total > 1 && q_stride != int64_t(H) * d) || (k_out && k_out == k && total > 1 && k_stride != kv_row))
+    return JFA_ERR_INVALID_ARG;
+  if (rot_dim < 0 || rot_dim > d || (rot_dim > 0 && !frequencies)) return JFA_ERR_INVALID_ARG;
+  if (rot_dim % 16 != 0) return JFA_ERR_UNSUPPORTED;
+  if ((st = check_workspace_bytes(workspace, workspace_bytes, sizeof(WsHeader))) != JFA_OK) return st;
+  CacheAppend a = {k, v, q, k_stride, v_stride, q_stride, offsets, total, q ? H : 0, q_out, k_out, lengths_out, rot_dim,
+                   interleaved ? 1 : 0, {}};
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    if (!std::isfinite(frequencies[i])) return JFA_ERR_INVALID_ARG;
+    const double turns = frequencies[i] / 6.283185307179586476925;
+    const double frac = std::ldexp(turns - std::floor(turns), 64);  // of one turn per position, in 2^-64
+    a.turn[i] = frac < 18446744073709551616.0 ? uint64_t(frac) : 0;
+  }
+  const int nsm = sm_count();
+  if (nsm <= 0) return JFA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  {
+    KernelTimer t(JFA_KERNEL_CACHE_APPEND, s);
+    JFA_CHECK_LAUNCH(launch_cache_append(*cache, a, workspace, nsm, s), "cache append launch");
+  }
+  g_last_launches = 1;
+  return JFA_OK;
+}
+
+jfa_status jfa_cache_attention(const jfa_cache* cache, const void* q, int H, int window, int sinks, float scale,
+                               void* out, float* lse, void* workspace, size_t workspace_bytes, jfa_stream_t stream) {
+  g_last_launches = 0;
+  jfa_status st = check_cache(cache);
+  if (st != JFA_OK) return st;
+  if (H < cache->H_kv || H > 4096 || H % cache->H_kv != 0 || window < 1 || sinks < 0) return JFA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !(scale < 3.0e38f)) return JFA_ERR_INVALID_ARG;
+  if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse)) return JFA_ERR_INVALID_ARG;
+  if ((st = check_workspace_bytes(workspace, workspace_bytes, cache_workspace_bytes(cache->B, H, cache->H_kv, cache->d))) !=
+      JFA_OK)
+    return st;
+  const int nsm = sm_count();
+  if (nsm <= 0) return JFA_ERR_CUDA;
+  CUtensorMap km, vm;
+  if ((st = encode_cache_map(&km, cache->k, *cache)) != JFA_OK) return st;
+  if ((st = encode_cache_map(&vm, cache->v, *cache)) != JFA_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  {
+    KernelTimer t(JFA_KERNEL_CACHE_ATTENTION, s);
+    JFA_CHECK_LAUNCH(launch_cache_attention(*cache, km, vm, q, H, window, sinks, scale, out, lse, workspace, nsm, s),
+                     "cache attention launch");
+  }
+  g_last_launches = 1;
+  return JFA_OK;
+}
+
 jfa_status jfa_check_status(void* workspace, jfa_stream_t stream) {
   if (!workspace) return JFA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -330,6 +445,7 @@ const char* jfa_status_string(jfa_status s) {
     case JFA_ERR_CUDA: return "CUDA runtime or driver call failed";
     case JFA_ERR_BAD_OFFSETS: return "offsets must start at 0, be non-decreasing and end at the row count";
     case JFA_ERR_TIMEOUT: return "a bounded pipeline wait ran out on the device; outputs are unspecified";
+    case JFA_ERR_BAD_PAGES: return "a page table entry that the call needs is not a page of the cache";
   }
   return "unknown status";
 }

@@ -96,4 +96,22 @@ cudaError_t launch_bwd_nsp(const Problem& p, const float* lse, void* ws, const W
 cudaError_t launch_bwd_fused(const Problem& p, const float* lse, void* ws, const WsLayout& L, void* dq, void* dk,
                              void* dv, int num_sms, cudaStream_t stream);
 
+// ---- paged key/value cache (jfa_cache.cu)
+struct CacheAppend {
+  const void *k, *v, *q;
+  int64_t k_stride, v_stride, q_stride;  // elements between tokens
+  const int64_t* offsets;
+  int64_t total;
+  int H;
+  void *q_out, *k_out;
+  int32_t* lengths_out;
+  int rot, interleaved;
+  uint64_t turn[64];  // angle per position of each rotated pair, in 2^-64 turns
+};
+size_t cache_workspace_bytes(int B, int H, int Hkv, int d);
+cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* ws, int num_sms, cudaStream_t stream);
+cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& k_map, const CUtensorMap& v_map, const void* q,
+                                   int H, int window, int sinks, float scale, void* out, float* lse, void* ws,
+                                   int num_sms, cudaStream_t stream);
+
 }  // namespace jfa

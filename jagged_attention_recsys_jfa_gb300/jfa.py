@@ -7,6 +7,7 @@ without the built library, or with CPU tensors, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -18,14 +19,15 @@ from . import build as _build
 
 JFA_OK = 0
 STATUS_NAMES = {0: "JFA_OK", 1: "JFA_ERR_INVALID_ARG", 2: "JFA_ERR_UNSUPPORTED", 3: "JFA_ERR_WORKSPACE",
-                4: "JFA_ERR_CUDA", 5: "JFA_ERR_BAD_OFFSETS", 6: "JFA_ERR_TIMEOUT"}
+                4: "JFA_ERR_CUDA", 5: "JFA_ERR_BAD_OFFSETS", 6: "JFA_ERR_TIMEOUT", 7: "JFA_ERR_BAD_PAGES"}
 
 # Every symbol include/jfa.h declares.
 EXPORTED_SYMBOLS = ("jfa_workspace_size", "jfa_forward", "jfa_forward_noalloc", "jfa_backward", "jfa_check_status",
                     "jfa_status_string", "jfa_last_launch_count", "jfa_last_error", "jfa_timing_enable",
                     "jfa_timing_read", "jfa_trace_configure", "jfa_selftest_wait_timeout", "jfa_wait_limit_ns",
-                    "jfa_set_nsp_max_tiles")
-KERNEL_KINDS = ("plan", "forward", "bwd_preprocess", "bwd_dkdv", "bwd_dq", "bwd_fused", "bwd_nsp")
+                    "jfa_set_nsp_max_tiles", "jfa_cache_workspace_size", "jfa_cache_append", "jfa_cache_attention")
+KERNEL_KINDS = ("plan", "forward", "bwd_preprocess", "bwd_dkdv", "bwd_dq", "bwd_fused", "bwd_nsp", "bwd_join",
+                "cache_append", "cache_attention")
 
 
 class JfaError(RuntimeError):
@@ -44,6 +46,12 @@ class _Bias(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int), ("table", ctypes.c_void_p), ("num_buckets", ctypes.c_int),
                 ("center", ctypes.c_int), ("grad", ctypes.c_void_p), ("values", ctypes.c_void_p),
                 ("block_offsets", ctypes.c_void_p), ("plane", ctypes.c_int64), ("values_grad", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64), ("H_kv", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("d", ctypes.c_int), ("page_table", ctypes.c_void_p),
+                ("max_pages", ctypes.c_int), ("lengths", ctypes.c_void_p), ("B", ctypes.c_int)]
 
 
 _LIB = None
@@ -96,6 +104,13 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.jfa_wait_limit_ns.restype = ctypes.c_uint64
     lib.jfa_trace_configure.argtypes = [vp, sz, i32]
     lib.jfa_trace_configure.restype = i32
+    cache = ctypes.POINTER(_Cache)
+    lib.jfa_cache_workspace_size.argtypes = [i32, i32, i32, i32]
+    lib.jfa_cache_workspace_size.restype = sz
+    lib.jfa_cache_append.argtypes = [cache, vp, i64, vp, i64, vp, i64, i32, vp, i64, vp, i32, i32, vp, vp, vp, vp, sz, vp]
+    lib.jfa_cache_append.restype = i32
+    lib.jfa_cache_attention.argtypes = [cache, vp, i32, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.jfa_cache_attention.restype = i32
     _LIB = lib
     return lib
 
@@ -142,6 +157,13 @@ def _check_workspace(ws, nbytes, device):
     if ws.data_ptr() % 256:
         raise ValueError("workspace must start on a 256-byte boundary")
     return have
+
+
+def _check_window(window, sinks):
+    """`window` as the library's int (None: every key; longer than any sequence is the same)."""
+    if int(sinks) < 0 or (window is not None and int(window) < 1):
+        raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")
+    return (1 << 31) - 1 if window is None else min(int(window), (1 << 31) - 1)
 
 
 def _check_offsets(name, off):
@@ -293,6 +315,172 @@ def jfa_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, bias=None, bias
         raise JfaError(st, "jfa_backward")
     del bias_keep
     return dq, dk, dv, workspace
+
+
+# ---------------------------------------------------------------- paged key/value cache
+def _on(device, stream):
+    """Context of a call: `stream` current (so that what the call allocates and clears is
+    ordered with its kernels), else `device` current (no-op when it already is)."""
+    if stream is not None:
+        return torch.cuda.stream(stream)
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _check_int32(name, t, shape, device):
+    if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or tuple(t.shape) != shape
+            or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor {list(shape)} on {device}")
+
+
+def _check_tokens(name, t, rows, heads, d, device):
+    """Token rows [T, heads, d], each row contiguous; tokens may be strided."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device} (the library has no CPU path)")
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or (rows is not None and t.shape[0] != rows) or t.shape[2] != d or \
+            (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{rows}, {heads}, {d}]")
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or
+                      (t.shape[0] > 1 and (t.stride(0) % 8 or t.stride(0) < t.shape[1] * d)) or t.data_ptr() % 16):
+        raise ValueError(f"{name} needs contiguous 16-byte aligned rows, tokens a multiple of 8 elements apart")
+
+
+def _cache_struct(k_cache, v_cache, page_table, lengths):
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or not t.is_contiguous() or t.shape != k_cache.shape or \
+                t.device != k_cache.device:
+            raise ValueError(f"{name} must be a contiguous bfloat16 tensor [num_pages, H_kv, page_size, d] "
+                             "(both of one shape, on one device)")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] < 1:
+        raise ValueError("page_table must be an int32 CUDA tensor [B, max_pages]")
+    device, B = k_cache.device, page_table.shape[0]
+    _check_int32("page_table", page_table, (B, page_table.shape[1]), device)
+    _check_int32("lengths", lengths, (B,), device)
+    P, G, page, d = k_cache.shape
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), P, G, page, d, page_table.data_ptr(), page_table.shape[1],
+                  lengths.data_ptr(), B)
+
+
+def cache_workspace_size(B, H, H_kv, d) -> int:
+    return int(load_library().jfa_cache_workspace_size(B, H, H_kv, d))
+
+
+def new_cache_workspace(B, H, H_kv, d, device) -> torch.Tensor:
+    """A zero-initialised workspace for jfa_cache_append and jfa_cache_attention."""
+    nbytes = cache_workspace_size(B, H, H_kv, d)
+    if nbytes == 0:
+        raise ValueError(f"no cache workspace for B={B}, H={H}, H_kv={H_kv}, d={d}")
+    return _workspace(nbytes, device)
+
+
+def rotary_frequencies(dim, base=10000.0) -> torch.Tensor:
+    """The usual angles per position, base^(-2i/dim) for pairs i = 0 .. dim/2 - 1, as the
+    float64 CPU tensor that jfa_cache_append takes."""
+    return float(base) ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+
+
+def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=None, frequencies=None, interleaved=False,
+                     q_out=None, k_out=None, lengths_out=None, workspace=None, stream=None):
+    """q_out, k_out, lengths_out, workspace = jfa_cache_append(...): append new tokens to the
+    paged cache, keys (and q) rotated by their positions on the way.
+
+    k, v: bf16 [T, H_kv, d], q: bf16 [T, H, d] or None; tokens may be strided (slices of one
+    projection).  offsets: int64 [B+1] on the device, sequence b's new tokens being rows
+    offsets[b] .. offsets[b+1] - 1 (rows behind the last sequence are left alone).  k_cache,
+    v_cache: bf16 [num_pages, H_kv, page_size, d]; page_table: int32 [B, max_pages]; lengths:
+    int32 [B], tokens cached so far.  frequencies: float64 CPU tensor [rot_dim / 2], radians per
+    position (rotary_frequencies), or None for no rotation.  Writes the caches; returns the
+    rotated q (None without q), k_out (the rotated keys where a tensor was given for them) and
+    the lengths after the call (lengths_out may be `lengths` itself).  Asynchronous; device-side
+    errors are reported by jfa_check_status(workspace).
+    """
+    lib = load_library()
+    cache = _cache_struct(k_cache, v_cache, page_table, lengths)
+    device, G, d = k_cache.device, cache.H_kv, cache.d
+    _check_tokens("k", k, None, G, d, device)
+    T = k.shape[0]
+    _check_tokens("v", v, T, G, d, device)
+    _check_offsets("offsets", offsets)
+    if offsets.device != device or offsets.numel() != cache.B + 1:
+        raise ValueError(f"offsets must have {cache.B + 1} entries on {device}")
+    H = 0
+    if q is not None:
+        _check_tokens("q", q, T, None, d, device)
+        H = q.shape[1]
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    rot, freq_ptr = 0, None
+    if frequencies is not None:
+        if (not isinstance(frequencies, torch.Tensor) or frequencies.is_cuda or frequencies.dtype != torch.float64
+                or frequencies.dim() != 1 or not frequencies.is_contiguous()):
+            raise ValueError("frequencies must be a contiguous float64 CPU tensor [rot_dim / 2]")
+        rot, freq_ptr = 2 * frequencies.numel(), frequencies.data_ptr()
+    with _on(device, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
+        if lengths_out is None:
+            lengths_out = torch.empty_like(lengths)
+        if workspace is None:
+            workspace = _workspace(256, device)
+        _check_int32("lengths_out", lengths_out, (cache.B,), device)
+        for name, t, heads in (("q_out", q_out, H), ("k_out", k_out, G)):
+            if t is not None:
+                _check_values(name, t, rows=T, H=heads, d=d)
+                if t.device != device:
+                    raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+        ws_bytes = _check_workspace(workspace, 256, device)
+        st = lib.jfa_cache_append(ctypes.byref(cache), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
+                                  q.data_ptr() if q is not None else None, q.stride(0) if q is not None else 0, H,
+                                  offsets.data_ptr(), T, freq_ptr, rot, 1 if interleaved else 0,
+                                  q_out.data_ptr() if q is not None else None,
+                                  k_out.data_ptr() if k_out is not None else None, lengths_out.data_ptr(),
+                                  workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    if st != JFA_OK:
+        raise JfaError(st, "jfa_cache_append")
+    return q_out, k_out, lengths_out, workspace
+
+
+def jfa_cache_attention(q, k_cache, v_cache, page_table, lengths, window=None, sinks=0, scale=None, out=None, lse=None,
+                        workspace=None, stream=None):
+    """out, lse, workspace = jfa_cache_attention(...): attention of each sequence's newest token
+    over the paged cache.
+
+    q: bf16 [B, H, d], H a multiple of H_kv; lengths: int32 [B], the newest token included.  Key j
+    is visible iff j < L and (j >= L - window or j < sinks); window None: every key.  Returns out
+    bf16 [B, H, d] and lse fp32 [H, B] (0 and -inf for an empty sequence).  Asynchronous;
+    device-side errors are reported by jfa_check_status(workspace).
+    """
+    lib = load_library()
+    cache = _cache_struct(k_cache, v_cache, page_table, lengths)
+    device, G, d, B = k_cache.device, cache.H_kv, cache.d, cache.B
+    _check_values("q", q)
+    if q.device != device or q.shape[0] != B or q.shape[2] != d or q.shape[1] % G:
+        raise ValueError(f"q has shape {tuple(q.shape)} on {q.device}, expected [{B}, a multiple of {G}, {d}] on {device}")
+    H = q.shape[1]
+    window = _check_window(window, sinks)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = int(lib.jfa_cache_workspace_size(B, H, G, d))
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((H, B), dtype=torch.float32, device=device)
+        if workspace is None:
+            workspace = _workspace(nbytes, device)
+        _check_values("out", out, rows=B, H=H, d=d)
+        _check_lse(lse, H, B)
+        for name, t in (("out", out), ("lse", lse)):
+            if t.device != device:
+                raise ValueError(f"{name} is on {t.device}, the cache on {device}")
+        ws_bytes = _check_workspace(workspace, nbytes, device)
+        st = lib.jfa_cache_attention(ctypes.byref(cache), q.data_ptr(), H, window, int(sinks), scale, out.data_ptr(),
+                                     lse.data_ptr(), workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    if st != JFA_OK:
+        raise JfaError(st, "jfa_cache_attention")
+    return out, lse, workspace
 
 
 def jfa_check_status(workspace, stream=None) -> int:
