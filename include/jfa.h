@@ -124,6 +124,33 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
                         int causal, void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
                         jfa_stream_t stream);
 
+/* ---- Sliding window with sinks, key/value heads shared by groups of query heads.
+ *
+ * The same attention, causal, with query i of a sequence (at position p = i + Lk_b - Lq_b)
+ * seeing key j iff  j <= p  and  (j > p - window  or  j < sinks):  the last `window` keys up to
+ * its own position, and the sequence's first `sinks` keys always.  A window of at least Lk_b is
+ * plain causal attention.  Query head h reads key/value head h / (H / H_kv).  A row that sees no
+ * key (p < 0) gets out = 0, lse = -inf and no gradient.
+ *
+ * q, out, dout, dq: bf16 [total_q, H, d]; k, v, dk, dv: bf16 [total_kv, H_kv, d]; the rest as for
+ * jfa_forward / jfa_backward.  H a multiple of H_kv; window >= 1; sinks in 0 .. 128.  Cost goes
+ * with the visible key tiles, not with the sequence length squared.  Keys that no query of their
+ * sequence sees (when queries follow a longer history) are not read: they may hold anything,
+ * NaN included, and get zero gradients.  A non-finite value in a key or value that some query
+ * sees may reach every row of that sequence and head.  dk and dv sum over the group's query heads
+ * in fp32, in a fixed order (results are bit-reproducible). */
+size_t jfa_window_workspace_size(int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv, int sinks,
+                                 int is_backward);
+jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                              const int64_t* kv_offsets, int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv,
+                              int window, int sinks, float scale, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, jfa_stream_t stream);
+jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                               const float* lse, const int64_t* q_offsets, const int64_t* kv_offsets, int B, int H,
+                               int H_kv, int d, int64_t total_q, int64_t total_kv, int window, int sinks, float scale,
+                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                               jfa_stream_t stream);
+
 /* Forward without a workspace, for callers that cannot allocate device memory.  The
  * pages have no counterpart to this entry point.  Hosts such as inference-runtime
  * plugins and services on a fixed, pre-planned memory arena give a kernel library

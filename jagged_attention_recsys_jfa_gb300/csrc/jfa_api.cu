@@ -107,8 +107,8 @@ int sm_count() {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Whole-tensor template for a bf16 [rows, H*d] row-major tensor: boxes of 64 columns
-// (128 bytes, the 128-byte swizzle span) by 128 rows; out-of-bounds elements read as 0.
-jfa_status encode_template(CUtensorMap* m, const void* base, int64_t rows, int H, int d) {
+// (128 bytes, the 128-byte swizzle span) by 128 rows (or `box_rows`); out-of-bounds elements read as 0.
+jfa_status encode_template(CUtensorMap* m, const void* base, int64_t rows, int H, int d, int box_rows = kBM) {
   auto fn = encode_fn();
   if (!fn) {
     std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled entry point not available");
@@ -116,7 +116,7 @@ jfa_status encode_template(CUtensorMap* m, const void* base, int64_t rows, int H
   }
   const cuuint64_t dims[2] = {cuuint64_t(H) * cuuint64_t(d), cuuint64_t(rows > 0 ? rows : 1)};
   const cuuint64_t strides[1] = {cuuint64_t(H) * cuuint64_t(d) * 2};
-  const cuuint32_t box[2] = {64, 128};
+  const cuuint32_t box[2] = {64, cuuint32_t(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -211,6 +211,36 @@ jfa_status check_cache(const jfa_cache* c) {
   if (c->num_pages >= limit || c->num_pages * c->H_kv >= limit || c->num_pages * c->H_kv * c->page_size >= limit ||
       int64_t(c->max_pages) * c->page_size >= limit)
     return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
+
+jfa_status check_window(int H, int H_kv, int d, int64_t total_kv, int window, int sinks) {
+  if (H_kv < 1 || H % H_kv != 0 || window < 1 || sinks < 0) return JFA_ERR_INVALID_ARG;
+  if (sinks > kMaxSinks) return JFA_ERR_UNSUPPORTED;
+  if ((total_kv + 1) * int64_t(H_kv) * d > (int64_t(1) << 40)) return JFA_ERR_INVALID_ARG;
+  return JFA_OK;
+}
+
+// The templates of a windowed call: K and V have H_kv heads, and maps of their own for the sinks.
+jfa_status window_maps(PlanMaps* maps, const Problem& pr, const void* q, const void* k, const void* v, const void* dout) {
+  std::memset(maps, 0, sizeof(*maps));
+  const int G = pr.win.H_kv;
+  const void* kbase = pr.total_kv > 0 ? k : q;  // maps of a side without rows are never read
+  const void* vbase = pr.total_kv > 0 ? v : kbase;
+  const void* qbase = pr.total_q > 0 ? q : kbase;
+  const void* base[kNumMapSlots] = {qbase, kbase, vbase, pr.total_q > 0 ? dout : kbase};
+  for (int i = 0; i < kNumMapSlots; ++i) {
+    if (i == kMapDO && !dout && pr.total_q > 0) continue;  // forward
+    const bool kv = i == kMapK || i == kMapV;
+    const int heads = kv ? G : pr.H;
+    const int64_t rows = kv ? pr.total_kv : pr.total_q;
+    jfa_status st = encode_template(&maps->tmpl[i], base[i], rows, heads, pr.d);
+    if (st == JFA_OK && kv) st = encode_template(&maps->sink_tmpl[i - kMapK], base[i], rows, heads, pr.d, sink_rows(pr.win.sinks));
+    if (st != JFA_OK) return st;
+    maps->base[i] = base[i];
+    maps->row_bytes[i] = uint32_t(heads) * uint32_t(pr.d) * 2;
+    maps->used[i] = 1;
+  }
   return JFA_OK;
 }
 
@@ -349,6 +379,96 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
     JFA_CHECK_LAUNCH(launch_bwd_nsp(pr, lse, workspace, L, dq, dk, dv, nsm, s), "non-sequence-parallel launch");
   }
   g_last_launches = nsp ? 6 : 5;
+  return JFA_OK;
+}
+
+size_t jfa_window_workspace_size(int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv, int sinks,
+                                 int is_backward) {
+  if (B < 1 || H_kv < 1 || H < H_kv || H % H_kv != 0 || (d != 64 && d != 128) || total_q < 0 || total_kv < 0 || sinks < 0 ||
+      sinks > kMaxSinks)
+    return 0;
+  return make_layout(B, H, d, total_q, total_kv, is_backward != 0, false, WindowSpec{1, sinks, H_kv}).total;
+}
+
+jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const int64_t* q_offsets,
+                              const int64_t* kv_offsets, int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv,
+                              int window, int sinks, float scale, void* out, float* lse, void* workspace,
+                              size_t workspace_bytes, jfa_stream_t stream) {
+  g_last_launches = 0;
+  jfa_status st = check_common(B, H, d, total_q, total_kv, nullptr, scale, q_offsets, kv_offsets);
+  if (st != JFA_OK) return st;
+  if ((st = check_window(H, H_kv, d, total_kv, window, sinks)) != JFA_OK) return st;
+  if (total_q > 0 && (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse)))
+    return JFA_ERR_INVALID_ARG;
+  if (total_kv > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return JFA_ERR_INVALID_ARG;
+  if (total_q == 0) return JFA_OK;  // no rows: nothing to enqueue
+  Problem pr = make_problem(B, H, d, total_q, total_kv, q_offsets, kv_offsets, nullptr, scale, 1);
+  pr.win = WindowSpec{window < kMaxWindow ? window : kMaxWindow, sinks, H_kv};
+  const WsLayout L = make_layout(B, H, d, total_q, total_kv, false, false, pr.win);
+  if ((st = check_workspace(workspace, workspace_bytes, L)) != JFA_OK) return st;
+  const int nsm = sm_count();
+  if (nsm <= 0) return JFA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  PlanMaps maps;
+  if ((st = window_maps(&maps, pr, q, k, v, nullptr)) != JFA_OK) return st;
+  {
+    KernelTimer t(JFA_KERNEL_PLAN, s);
+    JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, false, nsm, s), "planner launch");
+  }
+  {
+    KernelTimer t(JFA_KERNEL_FORWARD, s);
+    JFA_CHECK_LAUNCH(launch_forward(pr, workspace, L, out, lse, nsm, s), "forward launch");
+  }
+  g_last_launches = 2;
+  return JFA_OK;
+}
+
+jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, const void* v, const void* out,
+                               const float* lse, const int64_t* q_offsets, const int64_t* kv_offsets, int B, int H,
+                               int H_kv, int d, int64_t total_q, int64_t total_kv, int window, int sinks, float scale,
+                               void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                               jfa_stream_t stream) {
+  g_last_launches = 0;
+  jfa_status st = check_common(B, H, d, total_q, total_kv, nullptr, scale, q_offsets, kv_offsets);
+  if (st != JFA_OK) return st;
+  if ((st = check_window(H, H_kv, d, total_kv, window, sinks)) != JFA_OK) return st;
+  if (total_q > 0 && (!dout || !q || !out || !lse || !dq || !aligned16(dout) || !aligned16(q) || !aligned16(out) ||
+                      !aligned16(lse) || !aligned16(dq)))
+    return JFA_ERR_INVALID_ARG;
+  if (total_kv > 0 && (!k || !v || !dk || !dv || !aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv)))
+    return JFA_ERR_INVALID_ARG;
+  if (total_q == 0 && total_kv == 0) return JFA_OK;  // no rows: nothing to enqueue
+  Problem pr = make_problem(B, H, d, total_q, total_kv, q_offsets, kv_offsets, nullptr, scale, 1);
+  pr.win = WindowSpec{window < kMaxWindow ? window : kMaxWindow, sinks, H_kv};
+  pr.nsp_max_tiles = 0;
+  const WsLayout L = make_layout(B, H, d, total_q, total_kv, true, false, pr.win);
+  if ((st = check_workspace(workspace, workspace_bytes, L)) != JFA_OK) return st;
+  const int nsm = sm_count();
+  if (nsm <= 0) return JFA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  PlanMaps maps;
+  if ((st = window_maps(&maps, pr, q, k, v, dout)) != JFA_OK) return st;
+  {
+    KernelTimer t(JFA_KERNEL_PLAN, s);
+    JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, true, nsm, s), "planner launch");
+  }
+  {
+    KernelTimer t(JFA_KERNEL_BWD_PREPROCESS, s);
+    JFA_CHECK_LAUNCH(launch_bwd_preprocess(pr, dout, out, lse, workspace, L, nsm, s), "backward preprocess launch");
+  }
+  {
+    KernelTimer t(JFA_KERNEL_BWD_DKDV, s);
+    JFA_CHECK_LAUNCH(launch_bwd_dkdv(pr, lse, workspace, L, dk, dv, nsm, s), "dK/dV launch");
+  }
+  {
+    KernelTimer t(JFA_KERNEL_BWD_DQ, s);
+    JFA_CHECK_LAUNCH(launch_bwd_dq(pr, lse, workspace, L, dq, nsm, s), "dQ launch");
+  }
+  {
+    KernelTimer t(JFA_KERNEL_BWD_JOIN, s);
+    JFA_CHECK_LAUNCH(launch_bwd_join(pr, workspace, L, dk, dv, nsm, s), "sink gradient launch");
+  }
+  g_last_launches = 5;
   return JFA_OK;
 }
 

@@ -79,6 +79,11 @@ struct BwdParams {
   __nv_bfloat16* g2;   // dQ (fused and non-sequence-parallel passes)
   float* dqacc;        // non-sequence-parallel pass: fp32 dQ sums [total_q][H][D]
   TraceBuf trace;
+  WindowSpec win;            // sliding window with sinks (the kWin kernels)
+  int group;                 // query heads per key/value head
+  const CUtensorMap* smaps;  // the sinks' K / V maps
+  int sink_rows;             // rows of their boxes
+  float* spart;              // partial dK, dV of the sinks (dK/dV pass): [slot][2][sinks][D]
 };
 
 __device__ __forceinline__ void raise_status(int* status, int code) { atomicCAS(status, 0, code); }
@@ -392,6 +397,27 @@ __device__ __forceinline__ void drain_row_own(uint32_t taddr, float mul, __nv_bf
   }
 }
 
+// The D accumulator columns of this thread's TMEM lane as fp32 to its own row (16-byte
+// aligned); arrives on `empty` as soon as the last columns are in registers.
+template <int D>
+__device__ __forceinline__ void drain_row_f32(uint32_t taddr, float* dst, bool valid, uint64_t* empty) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 32) {
+    uint32_t r[32];
+    tmem_ld32(taddr + c0, r);
+    tmem_ld_wait();
+    if (c0 + 32 == D) {
+      tc_fence_before();
+      mbar_arrive(empty);
+    }
+    if (valid) {
+#pragma unroll
+      for (int c = 0; c < 32; c += 4)
+        *reinterpret_cast<uint4*>(dst + c0 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
+    }
+  }
+}
+
 // Write NC (32 or 64) accumulator columns of this thread's TMEM lane, times `mul`, as bf16
 // to global (or zeros when `zero`).  All 32 lanes of the warp call it together: the rows'
 // stores are shared across lanes so that each store instruction writes whole row segments.
@@ -451,7 +477,30 @@ __device__ __forceinline__ void drain_acc_rows(uint32_t taddr, float mul, __nv_b
 // tile: dO_i is released after dV(i) and Q_i after dK(i), i.e. in fill order.  Each Q_i
 // brings its tile's lse2 and D vectors (vector slot = query tile count mod kVecSlots; a
 // slot is refilled only after dK of its previous tile completed).
-template <int D, bool kBias, bool kJBias = false>
+//
+// kWin (sliding window with sinks, shared key/value heads): an item's head is a key/value head,
+// whose tile sums over the query tiles that its keys' windows reach, of every query head of the
+// group.  The units behind the key tiles are chunks of the sinks' pairs (win_key_unit): K and V
+// are then the sinks, and the epilogue writes fp32 partial sums for join_kernel.
+struct KeyUnit {
+  int first, n, r0, count, chunk;  // see WinKeyUnit
+};
+template <bool kWin>
+__device__ __forceinline__ KeyUnit key_unit(const BwdParams& p, const ItemMeta& m, int kt) {
+  KeyUnit u;
+  if (kWin) {
+    const WinKeyUnit w = win_key_unit(kt, m.Lq, meta_win(m), p.win.window, p.group);
+    u = KeyUnit{w.first, w.n, w.r0, w.r1 - w.r0, w.chunk};
+  } else {
+    u.r0 = 0;
+    u.chunk = -1;
+    q_tiles_for_kv_tile(kt, m.Lq, m.Lk, p.causal != 0, &u.first, &u.count);
+    u.n = u.count;
+  }
+  return u;
+}
+
+template <int D, bool kBias, bool kJBias = false, bool kWin = false>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p) {
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDkdv;
@@ -518,35 +567,41 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
     // dP^T MMA frees the buffers, whatever the ring producer is waiting on.
     if (lane == 0) {
       uint32_t item_n = 0, tn = 0;
-      int acq_b = -1;  // sequence whose maps this thread has acquired
+      int acq_b = -1, acq_s = -1;  // sequences whose maps (sink maps) this thread has acquired
       bool ok = true;
       uint32_t item_k = 0;
       for (; ok; ++item_k) {
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
-        const int Lq = wi.Lq, Lk = wi.Lk;
         const int64_t k0 = wi.ko;
         acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
+        if (kWin && p.win.sinks > 0 && acq_s != wi.b) {
+          tmap_acquire(p.smaps + size_t(wi.b) * kNumMapSlots + kMapK);
+          tmap_acquire(p.smaps + size_t(wi.b) * kNumMapSlots + kMapV);
+          acq_s = wi.b;
+        }
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-          int first, count;
-          q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
-          if (count == 0) continue;
-          const TileMap mk = tile_map(p.maps, p.B, kMapK, wi.b, k0, kt, p.total_kv);
-          const TileMap mv = tile_map(p.maps, p.B, kMapV, wi.b, k0, kt, p.total_kv);
+          const KeyUnit ku = key_unit<kWin>(p, wi, kt);
+          if (ku.count == 0) continue;
+          const bool sink = kWin && ku.chunk >= 0;
+          const CUtensorMap* maps = sink ? p.smaps : p.maps;
+          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv);
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv);
           if (mk.tail) {
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
           }
           if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
-          mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
+          mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
           load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
           load_tile<D>(sV, mv.map, &kv_full, wi.h * D, mv.y);
           ++item_n;
           // pull the next key tile into L2 meanwhile: the next of this range, else the first
           // of this CTA's next item
-          {
+          if (!kWin) {
             int nb = -1, nh = 0, nt = 0;
             if (kt + 1 < wi.u1) {
               nb = wi.b, nh = wi.h, nt = kt + 1;
@@ -594,14 +649,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
-        const int Lq = wi.Lq, Lk = wi.Lk;
         const int64_t q0 = wi.qo;
         acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
-        const int64_t vec0 = int64_t(wi.h) * p.qpad_cap + wi.qp;
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-          int first, count;
-          q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
-          if (const ItemMeta* wnp = kt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
+          const KeyUnit ku = key_unit<kWin>(p, wi, kt);
+          if (const ItemMeta* wnp = !kWin && kt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
             // pull the first query tiles of this CTA's next item into L2 meanwhile
             const ItemMeta& wn = *wnp;
             int nLq, nLk, nfirst, ncount;
@@ -614,12 +666,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
               prefetch_tile<D / 64>(p.maps, p.B, kMapQ, wn.b, nqo, t, p.total_q, wn.h * D);
             }
           }
-          for (int i = 0; i < count && ok; ++i) {
-            const int qt = first + i;
+          for (int i = 0; i < ku.count && ok; ++i) {
+            const int qt = kWin ? ku.first + (ku.r0 + i) % ku.n : ku.first + i;
+            const int qh = kWin ? wi.h * p.group + (ku.r0 + i) / ku.n : wi.h;  // query head
+            const int64_t vec0 = int64_t(qh) * p.qpad_cap + wi.qp;
             const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
             const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
-            if (!fill(mdo, wi.h * D, nullptr, nullptr)) { ok = false; break; }
-            if (!fill(mq, wi.h * D, p.lse2 + vec0 + qt * kBM, p.delta + vec0 + qt * kBM)) {
+            if (!fill(mdo, qh * D, nullptr, nullptr)) { ok = false; break; }
+            if (!fill(mq, qh * D, p.lse2 + vec0 + qt * kBM, p.delta + vec0 + qt * kBM)) {
               ok = false;
               break;
             }
@@ -669,10 +723,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int Lq = wi.Lq, Lk = wi.Lk;
        for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-        int first, count;
-        q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
+        const int count = key_unit<kWin>(p, wi, kt).count;
         if (count == 0) continue;
         if (!wait(&kv_full, item_n & 1)) { ok = false; break; }
         ++item_n;
@@ -730,7 +782,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
     }
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag))
+    if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
+                                         p.win.window, p.win.sinks))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -755,14 +808,15 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
      if (it.b < 0) break;  // end of this CTA's items
      const int Lq = it.Lq, Lk = it.Lk;
      for (int kt = it.u0; kt < it.u1 && ok; ++kt) {
-      int first, count;
-      q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
-      const int j = kt * kBN + row;  // local key index
+      const KeyUnit ku = key_unit<kWin>(p, it, kt);
+      const int count = ku.count;
+      const bool sink = kWin && ku.chunk >= 0;
+      const int j = sink ? row - meta_win(it).org : kt * kBN + row;  // local key index (sinks: behind org)
       if (count == 0) continue;  // rows of zeros: written by the epilogue warpgroup
       const int diag = Lk - Lq;  // key j visible to query i iff i >= j - diag
       const float* brow = kBias ? p.bias2 + size_t(it.h) * p.num_buckets : nullptr;
       for (int i = 0; i < count && ok; ++i) {
-        const int qt = first + i;
+        const int qt = kWin ? ku.first + (ku.r0 + i) % ku.n : ku.first + i;
         uint4 jbw[8];  // general bias for this tile (row order), loaded before the waits
         if (kJBias) {
           const int64_t pitch = (Lk + 7) / 8 * 8;  // rows of the sequence's block: bias[i][j] at i * pitch + j
@@ -829,6 +883,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c < lim) x[c] = -INFINITY;
+          }
+          if (kWin && !sink) {
+            const int hi = lim + p.win.window - 1;  // columns c > hi have moved past the key
+            if (hi < 63) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (c > hi) x[c] = -INFINITY;
+            }
           }
         }
 #pragma unroll
@@ -900,12 +962,27 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
      const int64_t ko = it.ko;
      const int Lq = it.Lq, Lk = it.Lk;
      for (int kt = it.u0; kt < it.u1 && ok; ++kt) {
-      int first, count;
-      q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
+      const KeyUnit ku = key_unit<kWin>(p, it, kt);
+      const int count = ku.count;
       const int j = kt * kBN + row;  // local key index
       const bool valid = j < Lk;
-      __nv_bfloat16* dk_row = p.g0 + ((ko + j) * p.H + it.h) * int64_t(D);
-      __nv_bfloat16* dv_row = p.g1 + ((ko + j) * p.H + it.h) * int64_t(D);
+      const int heads = kWin ? p.win.H_kv : p.H;
+      __nv_bfloat16* dk_row = p.g0 + ((ko + j) * heads + it.h) * int64_t(D);
+      __nv_bfloat16* dv_row = p.g1 + ((ko + j) * heads + it.h) * int64_t(D);
+      if (kWin && ku.chunk >= 0) {  // a chunk of the sinks: fp32 partial sums
+        const WinSeq ws = meta_win(it);
+        const int64_t slot = sink_slot0(it.qp / kBM, it.b, p.group) * p.win.H_kv +
+                             int64_t(it.h) * win_sink_chunks(Lq, ws, p.group) + ku.chunk;
+        float* part = p.spart + (slot * 2 * p.win.sinks + row) * int64_t(D);
+        if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        tc_fence_after();
+        drain_row_f32<D>(tmem + lane_addr + C::kColA1, part + p.win.sinks * int64_t(D), row < ws.ns, &dv_empty);
+        if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        ++acc_n;
+        tc_fence_after();
+        drain_row_f32<D>(tmem + lane_addr + C::kColA0, part, row < ws.ns, &dk_empty);
+        continue;
+      }
       if (count == 0) {  // no query sees these keys
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -937,7 +1014,27 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
 // Ring of single tiles, filled V_j, K_j per key tile: V_j is released after dP(j), K_j
 // after dQ(j), i.e. in fill order.  S and dP of the next key tile are issued as soon as
 // the warpgroups hold S in registers, so the dP/dS buffer alternates by tile parity.
-template <int D, bool kBias, bool kJBias = false>
+//
+// kWin: a query tile's steps are the sinks (nz = 1 if any of its rows sees them), then the
+// window-part key tiles from a on.  The sinks' products have sink_rows keys.
+struct QueryUnit {
+  int a, nz, nkv;
+};
+template <bool kWin>
+__device__ __forceinline__ QueryUnit query_unit(const BwdParams& p, const ItemMeta& m, int qt) {
+  QueryUnit u = {0, 0, 0};
+  if (kWin) {
+    int e;
+    win_kv_tiles(qt, m.Lq, m.Lk, p.win.window, &u.a, &e);
+    u.nz = win_sees_sinks(qt, m.Lq, meta_win(m)) ? 1 : 0;
+    u.nkv = e - u.a + u.nz;
+  } else {
+    u.nkv = kv_tiles_for_q_tile(qt, m.Lq, m.Lk, p.causal != 0);
+  }
+  return u;
+}
+
+template <int D, bool kBias, bool kJBias = false, bool kWin = false>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) {
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDq;
@@ -1012,11 +1109,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int Lq = wi.Lq, Lk = wi.Lk;
        const int64_t q0 = wi.qo;
        acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        if (kv_tiles_for_q_tile(qt, Lq, Lk, causal) == 0) continue;
+        if (query_unit<kWin>(p, wi, qt).nkv == 0) continue;
         const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
         const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
         if (mq.tail) {
@@ -1057,14 +1153,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
     // ------------------------------------------------------------ V / K ring producer
     if (lane == 0) {
       uint32_t ring_n = 0, tn = 0;
-      int acq_b = -1;  // sequence whose maps this thread has acquired
+      int acq_b = -1, acq_s = -1;  // sequences whose maps (sink maps) this thread has acquired
       bool ok = true;
-      auto fill = [&](const TileMap& m, int col) {
+      auto fill = [&](const TileMap& m, int col, uint32_t bytes) {
         const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
         if (m.tail) tmap_acquire(m.map);
         if (!mbar_wait(&ring_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
         trace_event(p.trace, kTraceProducer, tn, 2);
-        mbar_arrive_expect_tx(&ring_full[e], C::kTileBytes);
+        mbar_arrive_expect_tx(&ring_full[e], bytes);
         load_tile<D>(sRing + e * C::kTileBytes, m.map, &ring_full[e], col, m.y);
         ++ring_n;
         return true;
@@ -1074,12 +1170,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int Lq = wi.Lq, Lk = wi.Lk;
        const int64_t k0 = wi.ko;
+       const int col = (kWin ? wi.h / p.group : wi.h) * D;  // first column of the key/value head
        acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
+       if (kWin && p.win.sinks > 0) acquire_seq_maps(p.smaps, wi.b, kMapK, kMapV, acq_s, false);
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
-        if (const ItemMeta* wnp = qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
+        const QueryUnit qu = query_unit<kWin>(p, wi, qt);
+        const int nkv = qu.nkv;
+        if (const ItemMeta* wnp = !kWin && qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
           // pull the first key tiles of this CTA's next item into L2 meanwhile
           const ItemMeta& wn = *wnp;
           const int64_t nko = p.kv_off[wn.b];
@@ -1091,9 +1189,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           }
         }
         for (int jt = 0; jt < nkv && ok; ++jt) {
-          const TileMap mv = tile_map(p.maps, p.B, kMapV, wi.b, k0, jt, p.total_kv);
-          const TileMap mk = tile_map(p.maps, p.B, kMapK, wi.b, k0, jt, p.total_kv);
-          if (!fill(mv, wi.h * D) || !fill(mk, wi.h * D)) { ok = false; break; }
+          const bool sink = kWin && jt < qu.nz;
+          const CUtensorMap* maps = sink ? p.smaps : p.maps;
+          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
+          const int kt = kWin ? (sink ? 0 : qu.a + jt - qu.nz) : jt;
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv);
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv);
+          const uint32_t bytes = sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes);
+          if (!fill(mv, col, bytes) || !fill(mk, col, bytes)) { ok = false; break; }
         }
        }
        if (ok) meta_release(meta, item_k);
@@ -1117,15 +1220,15 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
       auto wait_ring = [&](uint32_t n) { return wait(&ring_full[n % R], (n / R) & 1); };
       auto ra = [&](uint32_t n) { return aR + (n % R) * C::kTileBytes; };
       // S (dp = false: Q K^T) or dP (dp = true: dO V^T) of a query tile and the key tile at b
-      auto mma_nt = [&](uint32_t dcol, bool dp, uint32_t b) {
+      auto mma_nt = [&](uint32_t dcol, bool dp, uint32_t b, uint32_t id) {
         const uint64_t ad = sdesc_sw128(dp ? aDO : aQ, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
           if (C::kDqQTmem)
-            umma_ts(tmem + dcol, tmem + (dp ? C::kColDqDO : C::kColDqQ) + kk * 8, bd + o, kIdS, kk > 0);
+            umma_ts(tmem + dcol, tmem + (dp ? C::kColDqDO : C::kColDqQ) + kk * 8, bd + o, id, kk > 0);
           else
-            umma_ss(tmem + dcol, ad + o, bd + o, kIdS, kk > 0);
+            umma_ss(tmem + dcol, ad + o, bd + o, id, kk > 0);
         }
       };
       uint32_t item_k = 0;
@@ -1133,19 +1236,20 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int Lq = wi.Lq, Lk = wi.Lk;
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
+        const QueryUnit qu = query_unit<kWin>(p, wi, qt);
+        const int nkv = qu.nkv;
         if (nkv == 0) continue;
+        const uint32_t id0 = kWin && qu.nz ? idesc_bf16_f32(128, p.sink_rows, false, false) : kIdS;  // the first step's
         if (!wait(C::kDqQTmem ? &qt_full : &qdo_full, item_n & 1)) { ok = false; break; }
         ++item_n;
         trace_event(p.trace, kTraceMma, tn, 10);
         const uint32_t n0 = ring_n;  // V_j at n0 + 2j, K_j at n0 + 2j + 1
         if (!wait_ring(n0 + 1)) { ok = false; break; }
-        mma_nt(C::kColS, false, ra(n0 + 1));
+        mma_nt(C::kColS, false, ra(n0 + 1), id0);
         umma_commit(&s_full);
         if (!wait_ring(n0)) { ok = false; break; }
-        mma_nt(colP(tile_n), true, ra(n0));
+        mma_nt(colP(tile_n), true, ra(n0), id0);
         umma_commit(&dp_full[tile_n & 1]);
         umma_commit(&ring_empty[n0 % R]);
         // Q and dO are read only by S and dP: once the last dP is issued the loader may
@@ -1161,11 +1265,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
             if (!wait(&s_free, g & 1)) { ok = false; break; }
             trace_event(p.trace, kTraceMma, tn, 11);
             if (!wait_ring(nk + 2)) { ok = false; break; }
-            mma_nt(C::kColS, false, ra(nk + 2));
+            mma_nt(C::kColS, false, ra(nk + 2), kIdS);
             umma_commit(&s_full);
             trace_event(p.trace, kTraceMma, tn, 12);
             if (!wait_ring(nv + 2)) { ok = false; break; }
-            mma_nt(colP(g + 1), true, ra(nv + 2));
+            mma_nt(colP(g + 1), true, ra(nv + 2), kIdS);
             umma_commit(&dp_full[(g + 1) & 1]);
             umma_commit(&ring_empty[(nv + 2) % R]);
             if (jt + 2 == nkv && !C::kDqQTmem) umma_commit(&qdo_empty);
@@ -1177,6 +1281,12 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           if (jt == 0 && !wait(&acc_empty, (acc_n & 1) ^ 1)) { ok = false; break; }
           // dQ += dS (TMEM, queries x keys) * K (keys x D, MN-major)
           const uint64_t kd = sdesc_sw128(ra(nk), 16384, 1024);
+          if (kWin && jt < qu.nz) {
+#pragma unroll 1
+            for (int kk = 0; kk < p.sink_rows / 16; ++kk)
+              umma_ts(tmem + C::kColDQ, tmem + colP(g) + (kk >> 2) * 64 + (kk & 3) * 8, kd + uint32_t(kk * 2048 >> 4),
+                      kIdAcc, kk > 0 ? 1u : 0u);
+          } else
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
             umma_ts(tmem + C::kColDQ, tmem + colP(g) + (kk >> 2) * 64 + (kk & 3) * 8, kd + uint32_t(kk * 2048 >> 4),
@@ -1199,7 +1309,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
     }
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag))
+    if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
+                                         p.win.window, p.win.sinks))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -1221,7 +1332,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
      const int Lq = it.Lq, Lk = it.Lk;
      const int64_t vec0 = int64_t(it.h) * p.qpad_cap + it.qp;
      for (int qt = it.u0; qt < it.u1 && ok; ++qt) {
-      const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
+      const QueryUnit qu = query_unit<kWin>(p, it, qt);
+      const int nkv = qu.nkv;
       const int i = qt * kBM + row;
       const bool valid = i < Lq;
       if (nkv == 0) continue;  // rows of zeros: written by the epilogue warpgroup
@@ -1299,8 +1411,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
         tc_fence_before();
         mbar_arrive(&s_free);
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 21);
-        const int j0 = jt * kBN + 64 * w;  // local key index of column 0 of this half
-        const int n_real = Lk - j0;        // columns >= n_real are past the sequence end
+        const bool sink = kWin && jt < qu.nz;
+        // local key index of column 0 of this half (sinks: behind org)
+        const int j0 = (kWin ? (sink ? -meta_win(it).org : (qu.a + jt - qu.nz) * kBN) : jt * kBN) + 64 * w;
+        const int n_real = sink ? meta_win(it).ns - 64 * w : Lk - j0;  // columns >= n_real hold no key
         if (kJBias) {
           jbias_apply<64>(x, jbk, sl2, kLog2e);
 #pragma unroll
@@ -1325,6 +1439,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c > lim) x[c] = -INFINITY;
+          }
+          if (kWin && !sink) {
+            const int clo = lim - p.win.window + 1;  // columns c < clo are behind the window
+            if (clo > 0) {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (c < clo) x[c] = -INFINITY;
+            }
           }
         }
         if (n_real < 64) {
@@ -1379,7 +1501,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
       const int i = qt * kBM + row;
       const bool valid = i < Lq;
       __nv_bfloat16* dq_row = p.g0 + ((it.qo + i) * p.H + it.h) * int64_t(D);
-      if (kv_tiles_for_q_tile(qt, Lq, Lk, causal) == 0) {  // the query tile sees no key
+      if (query_unit<kWin>(p, it, qt).nkv == 0) {  // the query tile sees no key
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) store_acc_row<32>(0, 0.f, dq_row + c0, valid, true);
         continue;
@@ -2480,9 +2602,79 @@ BwdParams make_params(const Problem& pr, const float* lse, void* ws, const WsLay
   bp.g0 = nullptr;
   bp.g1 = nullptr;
   bp.g2 = nullptr;
+  bp.win = pr.win;
+  bp.group = pr.win.window > 0 ? pr.H / pr.win.H_kv : 1;
+  bp.smaps = reinterpret_cast<const CUtensorMap*>(static_cast<uint8_t*>(ws) + L.smaps);
+  bp.sink_rows = sink_rows(pr.win.sinks);
+  bp.spart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.spart);
   bp.trace = pr.trace[pass == kPassDq ? JFA_KERNEL_BWD_DQ : pass == kPassFused ? JFA_KERNEL_BWD_FUSED
                      : pass == kPassNsp ? JFA_KERNEL_BWD_NSP : JFA_KERNEL_BWD_DKDV];
   return bp;
+}
+
+// ================================================================== the sinks' gradients (window)
+// dK and dV of each sequence's sinks from the dK/dV pass's partial sums, added in chunk order,
+// and zero rows for the keys between the sinks and the window part, which no query sees.
+// Memory bound and small: the partials are sinks x d x 2 floats per 16 query tiles.  Every
+// sequence gets the same number of warps.
+struct JoinParams {
+  const int64_t *q_off, *kv_off, *qpad;
+  const int* planned;  // 0 with malformed offsets: nothing to do
+  const float* spart;
+  int B, group;
+  WindowSpec win;
+  float scale;
+  __nv_bfloat16 *dk, *dv;
+};
+
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (*p.planned == 0) return;
+  const int lane = threadIdx.x & 31;
+  const int warps = int(gridDim.x * blockDim.x) >> 5, warp = int(blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int per_seq = warps / p.B > 0 ? warps / p.B : 1;
+  const int Hkv = p.win.H_kv;
+  for (int b = warp / per_seq; b < p.B; b += warps / per_seq) {
+    const int Lq = int(p.q_off[b + 1] - p.q_off[b]);
+    const int64_t ko = p.kv_off[b];
+    const WinSeq ws = win_seq(Lq, int(p.kv_off[b + 1] - ko), p.win.window, p.win.sinks);
+    const int chunks = win_sink_chunks(Lq, ws, p.group);
+    const int64_t slot0 = sink_slot0(p.qpad[b] / kBM, b, p.group) * Hkv;
+    const int64_t row_vecs = int64_t(Hkv) * D / 8;  // 16-byte pieces of a key row, all heads
+    const int64_t first = int64_t(warp % per_seq) * 32 + lane, step = int64_t(per_seq) * 32;
+    uint4* dk = reinterpret_cast<uint4*>(p.dk + ko * Hkv * D);
+    uint4* dv = reinterpret_cast<uint4*>(p.dv + ko * Hkv * D);
+    for (int64_t i = first; i < ws.ns * row_vecs; i += step) {
+      const int j = int(i / row_vecs), h = int(i % row_vecs) / (D / 8), c = int(i % (D / 8)) * 8;
+      const float* part = p.spart + ((slot0 + int64_t(h) * chunks) * 2 * p.win.sinks + j) * D + c;
+      float sk[8] = {}, sv[8] = {};
+      for (int k = 0; k < chunks; ++k, part += int64_t(2) * p.win.sinks * D) {
+        const float* pv = part + int64_t(p.win.sinks) * D;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(part) + q), v = __ldg(reinterpret_cast<const float4*>(pv) + q);
+          sk[4 * q] += a.x;
+          sk[4 * q + 1] += a.y;
+          sk[4 * q + 2] += a.z;
+          sk[4 * q + 3] += a.w;
+          sv[4 * q] += v.x;
+          sv[4 * q + 1] += v.y;
+          sv[4 * q + 2] += v.z;
+          sv[4 * q + 3] += v.w;
+        }
+      }
+      dk[i] = make_uint4(pack_bf16x2(sk[0] * p.scale, sk[1] * p.scale), pack_bf16x2(sk[2] * p.scale, sk[3] * p.scale),
+                         pack_bf16x2(sk[4] * p.scale, sk[5] * p.scale), pack_bf16x2(sk[6] * p.scale, sk[7] * p.scale));
+      dv[i] = make_uint4(pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]), pack_bf16x2(sv[4], sv[5]),
+                         pack_bf16x2(sv[6], sv[7]));
+    }
+    for (int64_t i = ws.ns * row_vecs + first; i < ws.org * row_vecs; i += step) {
+      dk[i] = make_uint4(0, 0, 0, 0);
+      dv[i] = make_uint4(0, 0, 0, 0);
+    }
+  }
 }
 
 }  // namespace
@@ -2533,6 +2725,10 @@ cudaError_t launch_bwd_dkdv(const Problem& pr, const float* lse, void* ws, const
   BwdParams bp = make_params(pr, lse, ws, L, kPassDkdv);
   bp.g0 = static_cast<__nv_bfloat16*>(dk);
   bp.g1 = static_cast<__nv_bfloat16*>(dv);
+  if (pr.win.window > 0)
+    return pr.d == 128
+               ? launch_dkdv_k(dkdv_kernel<128, false, false, true>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream)
+               : launch_dkdv_k(dkdv_kernel<64, false, false, true>, BwdCfg<64>::kSmemDkdv, num_sms, bp, stream);
   const bool bias = pr.bias_table != nullptr, jb = pr.jbias != nullptr;
   if (pr.d == 128)
     return bias ? launch_dkdv_k(dkdv_kernel<128, true>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream)
@@ -2563,6 +2759,9 @@ cudaError_t launch_bwd_dq(const Problem& pr, const float* lse, void* ws, const W
                           cudaStream_t stream) {
   BwdParams bp = make_params(pr, lse, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
+  if (pr.win.window > 0)
+    return pr.d == 128 ? launch_dkdv_k(dq_kernel<128, false, false, true>, BwdCfg<128>::kSmemDq, num_sms, bp, stream)
+                       : launch_dkdv_k(dq_kernel<64, false, false, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream);
   const bool bias = pr.bias_table != nullptr, jb = pr.jbias != nullptr;
   if (pr.d == 128)
     return bias ? launch_dkdv_k(dq_kernel<128, true>, BwdCfg<128>::kSmemDq, num_sms, bp, stream)
@@ -2571,6 +2770,25 @@ cudaError_t launch_bwd_dq(const Problem& pr, const float* lse, void* ws, const W
   return bias ? launch_dkdv_k(dq_kernel<64, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream)
               : jb ? launch_dkdv_k(dq_kernel<64, false, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream)
                    : launch_dkdv_k(dq_kernel<64, false>, BwdCfg<64>::kSmemDq, num_sms, bp, stream);
+}
+
+cudaError_t launch_bwd_join(const Problem& pr, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+                            cudaStream_t stream) {
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  JoinParams jp;
+  jp.q_off = pr.q_off;
+  jp.kv_off = pr.kv_off;
+  jp.qpad = reinterpret_cast<const int64_t*>(w + L.qpad);
+  jp.planned = &reinterpret_cast<const WsHeader*>(w)->planned;
+  jp.spart = reinterpret_cast<const float*>(w + L.spart);
+  jp.B = pr.B;
+  jp.group = pr.H / pr.win.H_kv;
+  jp.win = pr.win;
+  jp.scale = pr.scale;
+  jp.dk = static_cast<__nv_bfloat16*>(dk);
+  jp.dv = static_cast<__nv_bfloat16*>(dv);
+  return pr.d == 128 ? launch_pdl(join_kernel<128>, dim3(2 * num_sms), dim3(256), 0, stream, jp)
+                     : launch_pdl(join_kernel<64>, dim3(2 * num_sms), dim3(256), 0, stream, jp);
 }
 
 cudaError_t launch_bwd_nsp(const Problem& pr, const float* lse, void* ws, const WsLayout& L, void* dq, void* dk,

@@ -136,7 +136,8 @@ struct WsHeader {
   // (written by the planner)
   uint64_t wait_ns[5];
   int n_nsp;       // number of non-sequence-parallel backward items
-  int pad[41];
+  int planned;     // 1: the last plan found the offsets well formed
+  int pad[40];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
@@ -151,6 +152,8 @@ struct WsLayout {
   size_t nsp = 0;      // WorkItem[cap_nsp]    backward: sequences of 2 .. kNspMaxTiles query tiles
   size_t dqacc = 0;    // float[total_q][H][d] backward: their dQ sums over key tiles
   size_t bias2 = 0;    // float[H][num_buckets]  bias table pre-multiplied by log2(e)
+  size_t smaps = 0;    // window: the sinks' K and V maps, laid out like `maps`
+  size_t spart = 0;    // window, backward: float[sink chunk][2][sinks][d] partial dK, dV of the sinks
   size_t qpad = 0;     // int64[B+1]  backward: offsets of each sequence in the padded vectors
   size_t lse2 = 0;     // float[H][qpad_cap]  backward: lse * log2(e) (+inf if -inf), 0 on padding
   size_t delta = 0;    // float[H][qpad_cap]  backward: D_i = rowsum(dO * O), 0 on padding
@@ -160,13 +163,41 @@ struct WsLayout {
 
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// A sliding window with sinks and shared key/value heads (window = 0: none).
+struct WindowSpec {
+  int window = 0;  // keys a query sees up to its own position, 1 .. kMaxWindow
+  int sinks = 0;   // first keys that stay visible, 0 .. kMaxSinks
+  int H_kv = 0;    // key/value heads; query head h reads head h / (H / H_kv)
+};
+constexpr int kMaxWindow = 1 << 30;  // at least any sequence length
+constexpr int kMaxSinks = 128;       // one key tile
+// Rows of the boxes that load the sinks: whole MMA steps of 16 keys (rows past them arrive as zeros).
+__host__ __device__ inline int sink_rows(int sinks) { return sinks < 1 ? 16 : (sinks + 15) / 16 * 16; }
+// Query tiles of one chunk of the sinks' gradient.  Every query tile of a sequence sees its
+// sinks, so their dK / dV are summed chunk by chunk in fp32 partials, which join_kernel adds up
+// in order.
+constexpr int kSinkChunk = 16;
+
+// Slots for the sinks' partial gradients: sequence b's chunks of kv head g start at
+// sink_slot0(tiles of 128 queries before b, b) * H_kv + g * chunks_b.  floor(G n / kSinkChunk) + b,
+// with n the query tiles before b, is at least the chunks of the sequences before b, since
+// ceil(x) <= floor(x) + 1.
+__host__ __device__ inline int64_t sink_slot0(int64_t q_tiles_before, int b, int group) {
+  return q_tiles_before * group / kSinkChunk + b;
+}
+__host__ __device__ inline int64_t sink_slots(int B, int H, int H_kv, int64_t total_q) {
+  return (sink_slot0(total_q / kBM + B, B, H / H_kv) + 1) * H_kv;
+}
+
 // Capacities are upper bounds on the item counts for any offsets with these totals:
 //   sum_b ceil(ceil(L_b/128)/2) <= total/256 + B,  sum_b ceil(L_b/128) <= total/128 + B.
 // `nsp`: the backward may route sequences to the non-sequence-parallel pass, which needs its
 // fp32 dQ sum buffer (4 * total_q * H * d bytes); without it the buffer is left out.
 __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t total_q, int64_t total_kv,
-                                                bool backward, bool nsp = false) {
+                                                bool backward, bool nsp = false,
+                                                const WindowSpec& win = WindowSpec()) {
   WsLayout L;
+  const bool windowed = win.window > 0;
   size_t off = sizeof(WsHeader);
   L.maps = align_up(off, 128);
   off = L.maps + (size_t(B) + kTailMaps) * kNumMapSlots * 128;
@@ -177,12 +208,18 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
   L.fwd = align_up(off, 16);
   off = L.fwd + size_t(L.cap_fwd) * sizeof(WorkItem);
   L.bias2 = align_up(off, 256);
-  off = L.bias2 + size_t(H) * size_t(kMaxBuckets) * sizeof(float);
+  off = L.bias2 + (windowed ? 0 : size_t(H) * size_t(kMaxBuckets) * sizeof(float));
+  if (windowed) {
+    L.smaps = align_up(off, 128);
+    off = L.smaps + (win.sinks > 0 ? (size_t(B) + kTailMaps) * kNumMapSlots * 128 : 0);
+  }
   if (backward) {
     L.cap_dq = int64_t(H) * (total_q / 128 + B + 1);
     L.dq = align_up(off, 16);
     off = L.dq + size_t(L.cap_dq) * sizeof(WorkItem);
     L.cap_dkv = int64_t(H) * (total_kv / 128 + B + 1);
+    const int64_t chunks = windowed && win.sinks > 0 ? sink_slots(B, H, win.H_kv, total_q) : 0;
+    if (windowed) L.cap_dkv = int64_t(win.H_kv) * (total_kv / 128 + B + 1) + chunks;
     L.dkv = align_up(off, 16);
     off = L.dkv + size_t(L.cap_dkv) * sizeof(WorkItem);
     L.cap_fused = int64_t(H) * (B + 1);
@@ -200,6 +237,8 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
     off = L.lse2 + size_t(H) * size_t(L.qpad_cap) * sizeof(float);
     L.delta = align_up(off, 256);
     off = L.delta + size_t(H) * size_t(L.qpad_cap) * sizeof(float);
+    L.spart = align_up(off, 256);
+    off = L.spart + size_t(chunks) * 2 * size_t(win.sinks) * size_t(d) * sizeof(float);
   }
   L.total = align_up(off, 256);
   return L;
@@ -237,6 +276,74 @@ __host__ __device__ inline void q_tiles_for_kv_tile(int t, int Lq, int Lk, bool 
   }
   *first = i_min / kBM;
   *count = nq - *first;
+}
+
+// ---- Sliding window with sinks.  Query i stands at p = i + Lk - Lq and sees key j iff j <= p and
+// (j > p - W or j < S).  A sequence's keys fall into two parts that no key is in both of: the
+// sinks, keys [0, ns), and the window part, keys from org = max(first query's window, ns) on,
+// which is bottom-right aligned again with Lk' = Lk - org keys: i + Lk' - Lq = p - org.  Keys in
+// between are seen by no query and never read.
+struct WinSeq {
+  int ns, org, Lk;  // sinks; first key and key count of the window part
+};
+__host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S) {
+  WinSeq r;
+  r.ns = S < Lk ? S : Lk;
+  const int lo = Lk - Lq - W + 1;
+  r.org = lo > r.ns ? lo : r.ns;
+  r.Lk = Lk - r.org;
+  return r;
+}
+// Window-part key tiles [*a, *e) that query tile t visits.
+__host__ __device__ inline void win_kv_tiles(int t, int Lq, int Lk, int W, int* a, int* e) {
+  *a = *e = 0;
+  if (t * kBM >= Lq || Lk <= 0) return;
+  const int i0 = t * kBM, i1 = i0 + kBM - 1 < Lq - 1 ? i0 + kBM - 1 : Lq - 1, diag = Lk - Lq;
+  if (i1 + diag < 0) return;
+  const int lo = i0 + diag - W + 1;
+  *a = lo > 0 ? lo / kBN : 0;
+  *e = (i1 + diag) / kBN + 1;
+}
+// Whether a row of query tile t sees a sink (i.e. stands at a position >= 0).
+__host__ __device__ inline bool win_sees_sinks(int t, int Lq, const WinSeq& s) {
+  const int i1 = t * kBM + kBM - 1 < Lq - 1 ? t * kBM + kBM - 1 : Lq - 1;
+  return s.ns > 0 && t * kBM < Lq && i1 + s.org + s.Lk - Lq >= 0;
+}
+// The (query head of the group, query tile) pairs that one dK/dV unit sums over: pair r in
+// [r0, r1) is head r / n, query tile first + r % n.  Units kt < tiles of the window part are key
+// tiles; the ones behind are chunks of the sinks' pairs.
+struct WinKeyUnit {
+  int first, n, r0, r1;
+  int chunk;  // -1: a key tile
+};
+__host__ __device__ inline int win_sink_chunks(int Lq, const WinSeq& s, int group) {
+  if (s.ns <= 0 || Lq <= 0) return 0;
+  const int nq = (Lq + kBM - 1) / kBM;
+  const int i_min = Lq - s.org - s.Lk > 0 ? Lq - s.org - s.Lk : 0;  // first row at a position >= 0
+  return (group * (nq - i_min / kBM) + kSinkChunk - 1) / kSinkChunk;
+}
+__host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq& s, int W, int group) {
+  WinKeyUnit u = {0, 1, 0, 0, -1};
+  const int nk = (s.Lk + kBN - 1) / kBN, nq = (Lq + kBM - 1) / kBM;
+  if (kt >= nk) {
+    u.chunk = kt - nk;
+    const int i_min = Lq - s.org - s.Lk > 0 ? Lq - s.org - s.Lk : 0;
+    u.first = i_min / kBM;
+    u.n = nq - u.first;
+    u.r0 = u.chunk * kSinkChunk;
+    u.r1 = u.r0 + kSinkChunk < group * u.n ? u.r0 + kSinkChunk : group * u.n;
+    return u;
+  }
+  if (Lq <= 0) return u;
+  // key j' is seen by queries j' - diag .. j' - diag + W - 1
+  const int diag = s.Lk - Lq, j0 = kt * kBN, j1 = j0 + kBN - 1 < s.Lk - 1 ? j0 + kBN - 1 : s.Lk - 1;
+  const int lo = j0 - diag > 0 ? j0 - diag : 0;
+  const int hi = j1 - diag > Lq - W ? Lq - 1 : j1 - diag + W - 1;  // min(Lq - 1, j1 - diag + W - 1)
+  if (hi < lo) return u;
+  u.first = lo / kBM;
+  u.n = hi / kBM - u.first + 1;
+  u.r1 = group * u.n;
+  return u;
 }
 
 #ifdef __CUDACC__

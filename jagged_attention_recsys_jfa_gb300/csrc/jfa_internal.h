@@ -22,11 +22,13 @@ struct Problem {
   int64_t jb_plane;
   void* jb_grad;            // its gradient (backward), bf16 [H][jb_plane], or nullptr
   TraceBuf trace[JFA_NUM_KERNEL_KINDS];  // per kernel kind (JFA_KERNEL_*): developer tracing, buf == nullptr when off
+  WindowSpec win;           // sliding window with sinks (window = 0: none; causal then set, no bias)
   int nsp_max_tiles;        // backward: query tiles up to which a sequence takes the non-sequence-parallel pass
 };
 
 struct PlanMaps {
   CUtensorMap tmpl[kNumMapSlots];  // whole-tensor templates; the planner patches per-sequence copies
+  CUtensorMap sink_tmpl[2];        // window: K and V again, with boxes of sink_rows(sinks) rows
   const void* base[kNumMapSlots];  // tensor base pointers (row 0)
   uint32_t row_bytes[kNumMapSlots];
   int used[kNumMapSlots];
@@ -88,6 +90,9 @@ cudaError_t launch_bwd_dkdv(const Problem& p, const float* lse, void* ws, const 
                             void* dv, int num_sms, cudaStream_t stream);
 cudaError_t launch_bwd_dq(const Problem& p, const float* lse, void* ws, const WsLayout& L, void* dq,
                           int num_sms, cudaStream_t stream);
+// Window: the sinks' dK and dV from their partial sums, and zeros for keys that no query sees.
+cudaError_t launch_bwd_join(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+                            cudaStream_t stream);
 // Sequences of 2 .. kNspMaxTiles query tiles: one CTA per sequence and head, every tile
 // pair once, dQ summed over key tiles in the workspace.
 cudaError_t launch_bwd_nsp(const Problem& p, const float* lse, void* ws, const WsLayout& L, void* dq, void* dk,

@@ -28,6 +28,7 @@ struct PlanParams {
   int nb;
   const int64_t* jb_off;  // general jagged bias block offsets [B+1], or nullptr
   int64_t jb_plane;
+  WindowSpec win;         // sliding window with sinks (window = 0: none)
 };
 
 enum ListKind { kListFwd = 0, kListDq = 1, kListDkv = 2, kListFused = 3, kListNsp = 4 };
@@ -38,9 +39,18 @@ enum ListKind { kListFwd = 0, kListDq = 1, kListDkv = 2, kListFused = 3, kListNs
 // once); the others by the split dK/dV and dQ passes.  Units: key tiles, except for the
 // forward (query-tile pairs) and the dQ pass (query tiles); a sequence without keys still
 // gets one unit in the fused and non-sequence-parallel lists (its dq rows are zeroed there).
-__device__ __forceinline__ int list_units(int kind, int Lq, int Lk, int nsp_max) {
+// With a sliding window every sequence goes through the forward, dQ and dK/dV lists; the dK/dV
+// units are the key tiles of the window part, then the chunks of the sinks.
+__device__ __forceinline__ int list_units(const PlanParams& p, int kind, int Lq, int Lk) {
+  const int nsp_max = p.nsp_max_tiles;
   const int nq = (Lq + kBM - 1) / kBM;
   const int nk = (Lk + kBN - 1) / kBN;
+  if (p.win.window > 0) {
+    if (kind == kListFwd) return (nq + 1) / 2;
+    if (kind == kListDq) return nq;
+    const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
+    return (s.Lk + kBN - 1) / kBN + win_sink_chunks(Lq, s, p.H / p.win.H_kv);
+  }
   if (kind == kListFwd) return (nq + 1) / 2;
   if (kind == kListFused) return Lq <= kBM ? (nk > 0 ? nk : (Lq > 0 ? 1 : 0)) : 0;
   if (kind == kListNsp) return nsp_path(Lq, nsp_max) ? (nk > 0 ? nk : 1) : 0;
@@ -48,7 +58,21 @@ __device__ __forceinline__ int list_units(int kind, int Lq, int Lk, int nsp_max)
   return kind == kListDq ? nq : nk;
 }
 
-__device__ __forceinline__ int unit_cost(int kind, int u, int Lq, int Lk, bool causal) {
+__device__ __forceinline__ int win_tile_cost(int t, int Lq, const WinSeq& s, int W) {
+  int a, e;
+  win_kv_tiles(t, Lq, s.Lk, W, &a, &e);
+  return e - a + (win_sees_sinks(t, Lq, s) ? 1 : 0);
+}
+
+__device__ __forceinline__ int unit_cost(const PlanParams& p, int kind, int u, int Lq, int Lk) {
+  const bool causal = p.causal != 0;
+  if (p.win.window > 0) {
+    const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
+    if (kind == kListFwd) return win_tile_cost(2 * u, Lq, s, p.win.window) + win_tile_cost(2 * u + 1, Lq, s, p.win.window);
+    if (kind == kListDq) return win_tile_cost(u, Lq, s, p.win.window);
+    const WinKeyUnit k = win_key_unit(u, Lq, s, p.win.window, p.H / p.win.H_kv);
+    return k.r1 - k.r0;
+  }
   if (kind == kListFused) return 1;  // a key tile (its dK / dV rows are stored even when unseen)
   if (kind == kListNsp) {            // the query tiles that see key tile u (at least 1)
     int first, count;
@@ -111,12 +135,12 @@ __device__ int scan_desc(const int* hist, int* base) {
 // Walk the units of one sequence, cutting them into consecutive ranges whose summed
 // cost stays <= cap (a unit costlier than cap forms its own range); calls f(u0, u1, cost).
 template <typename F>
-__device__ void for_each_range(int kind, int Lq, int Lk, bool causal, int nsp_max, long long cap, F&& f) {
-  const int n = list_units(kind, Lq, Lk, nsp_max);
+__device__ void for_each_range(const PlanParams& p, int kind, int Lq, int Lk, long long cap, F&& f) {
+  const int n = list_units(p, kind, Lq, Lk);
   int start = 0;
   long long acc = 0;
   for (int u = 0; u < n; ++u) {
-    const int c = unit_cost(kind, u, Lq, Lk, causal);
+    const int c = unit_cost(p, kind, u, Lq, Lk);
     if (u > start && acc + c > cap) {
       f(start, u, acc);
       start = u;
@@ -131,17 +155,17 @@ __device__ void emit_list(const PlanParams& p, int kind, WorkItem* items, int64_
                           int* hist, int* base) {
   __shared__ long long total_cost;
   const int tid = threadIdx.x;
-  const bool causal = p.causal != 0;
+  const int heads = p.win.window > 0 && kind == kListDkv ? p.win.H_kv : p.H;
   // total work, to cap range cost at about 1/kItemsPerCta of a CTA's share
   long long local = 0;
   for (int b = tid; b < p.B; b += blockDim.x) {
     const int Lq = int(p.q_off[b + 1] - p.q_off[b]);
     const int Lk = int(p.kv_off[b + 1] - p.kv_off[b]);
-    const int n = list_units(kind, Lq, Lk, p.nsp_max_tiles);
-    for (int u = 0; u < n; ++u) local += unit_cost(kind, u, Lq, Lk, causal);
+    const int n = list_units(p, kind, Lq, Lk);
+    for (int u = 0; u < n; ++u) local += unit_cost(p, kind, u, Lq, Lk);
   }
   block_scan_incl(local, &total_cost);
-  const long long share = (total_cost * p.H + (long long)kItemsPerCta * p.grid - 1) /
+  const long long share = (total_cost * heads + (long long)kItemsPerCta * p.grid - 1) /
                           ((long long)kItemsPerCta * p.grid);
   // the fused and non-sequence-parallel passes own each sequence's dQ: their items are
   // never cut into ranges.  At d = 128 the dK/dV and dQ passes take one tile per item, and
@@ -165,14 +189,14 @@ __device__ void emit_list(const PlanParams& p, int kind, WorkItem* items, int64_
     if (grouped) {
       long long gcost = 0;
       int nr = 0;
-      for_each_range(kind, Lq, Lk, causal, p.nsp_max_tiles, range_cap, [&](int, int, long long cost) {
+      for_each_range(p, kind, Lq, Lk, range_cap, [&](int, int, long long cost) {
         gcost += cost;
         ++nr;
       });
-      if (nr) atomicAdd(&hist[bucket(gcost)], p.H * nr);
+      if (nr) atomicAdd(&hist[bucket(gcost)], heads * nr);
     } else {
-      for_each_range(kind, Lq, Lk, causal, p.nsp_max_tiles, range_cap,
-                     [&](int, int, long long cost) { atomicAdd(&hist[bucket(cost)], p.H); });
+      for_each_range(p, kind, Lq, Lk, range_cap,
+                     [&](int, int, long long cost) { atomicAdd(&hist[bucket(cost)], heads); });
     }
   }
   __syncthreads();
@@ -194,24 +218,24 @@ __device__ void emit_list(const PlanParams& p, int kind, WorkItem* items, int64_
     if (grouped) {
       long long gcost = 0;
       int nr = 0;
-      for_each_range(kind, Lq, Lk, causal, p.nsp_max_tiles, range_cap, [&](int, int, long long cost) {
+      for_each_range(p, kind, Lq, Lk, range_cap, [&](int, int, long long cost) {
         gcost += cost;
         ++nr;
       });
       if (nr) {
         // head h's tiles at pos + h * nr + r, in tile order
-        const int pos = atomicAdd(&base[bucket(gcost)], p.H * nr);
+        const int pos = atomicAdd(&base[bucket(gcost)], heads * nr);
         int r = 0;
-        for_each_range(kind, Lq, Lk, causal, p.nsp_max_tiles, range_cap, [&](int u0, int u1, long long cost) {
-          for (int h = 0; h < p.H; ++h) items[pos + h * nr + r] = WorkItem{b, h, u0, u1};
+        for_each_range(p, kind, Lq, Lk, range_cap, [&](int u0, int u1, long long cost) {
+          for (int h = 0; h < heads; ++h) items[pos + h * nr + r] = WorkItem{b, h, u0, u1};
           ++r;
           if ((unsigned long long)cost > mx) mx = (unsigned long long)cost;
         });
       }
     } else {
-      for_each_range(kind, Lq, Lk, causal, p.nsp_max_tiles, range_cap, [&](int u0, int u1, long long cost) {
-        const int pos = atomicAdd(&base[bucket(cost)], p.H);
-        for (int h = 0; h < p.H; ++h) items[pos + h] = WorkItem{b, h, u0, u1};
+      for_each_range(p, kind, Lq, Lk, range_cap, [&](int u0, int u1, long long cost) {
+        const int pos = atomicAdd(&base[bucket(cost)], heads);
+        for (int h = 0; h < heads; ++h) items[pos + h] = WorkItem{b, h, u0, u1};
         if ((unsigned long long)cost > mx) mx = (unsigned long long)cost;
       });
     }
@@ -222,7 +246,7 @@ __device__ void emit_list(const PlanParams& p, int kind, WorkItem* items, int64_
     *count_out = total;
     // the bounded waits of the kernel that walks this list scale with the planned work
     reinterpret_cast<WsHeader*>(p.ws)->wait_ns[kind] =
-        wait_limit_ns(total_cost * p.H, p.grid, (long long)max_item);
+        wait_limit_ns(total_cost * heads, p.grid, (long long)max_item);
   }
   __syncthreads();
 }
@@ -257,7 +281,7 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
   grid_dependency_wait();    // the offsets and the workspace may come from earlier work
   grid_launch_dependents();  // the next kernel may start its prologue; it waits for this one
 
-  const int list_ctas = p.backward ? 4 : 1;
+  const int list_ctas = !p.backward ? 1 : p.win.window > 0 ? 2 : 4;
   if (int(blockIdx.x) >= list_ctas) {
     const size_t gt = size_t(blockIdx.x - list_ctas) * blockDim.x + tid;
     const size_t gstride = size_t(gridDim.x - list_ctas) * blockDim.x;
@@ -270,15 +294,15 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       for (size_t i = gt; i < size_t(p.H) * p.nb; i += gstride) p.bias_grad[i] = 0.f;
     // ---- tail copies: the last min(128, total) rows of each tensor, which the boxes that
     //      would otherwise read past the tensor's last row load from instead
-    const size_t rb = p.L.row_bytes;
     for (int slot = 0; slot < kNumMapSlots; ++slot) {
       if (!maps.used[slot]) continue;
       const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
       if (total <= 0) continue;
       const int64_t n = total < kBM ? total : kBM;
+      const size_t rb = maps.row_bytes[slot];
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(maps.base[slot]) +
                                                         size_t(total - n) * rb);
-      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * kTailRows * rb);
+      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes);
       const size_t nvec = size_t(n) * rb / 16;
       for (size_t i = gt; i < nvec; i += gstride) dst[i] = src[i];
     }
@@ -289,32 +313,46 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
     //      offsets CTA 0 leaves every list empty, so no map is used; a tail map is only
     //      written for a sequence inside its tensor, which keeps its index in range.)
     CUtensorMap* out_maps = reinterpret_cast<CUtensorMap*>(p.ws + p.L.maps);
-    for (size_t idx = gt; idx < size_t(p.B) * kNumMapSlots; idx += gstride) {
-      const int b = int(idx / kNumMapSlots), slot = int(idx % kNumMapSlots);
-      if (!maps.used[slot]) continue;
-      const bool is_q_side = (slot == kMapQ || slot == kMapDO);
-      const int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
-      const int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
-      const uint4* src = reinterpret_cast<const uint4*>(&maps.tmpl[slot]);
-      CUtensorMap* dst = out_maps + idx;
+    auto write_map = [&](CUtensorMap* set, const CUtensorMap& tmpl, int b, int slot, int64_t row0, int64_t len) {
+      const size_t rb = maps.row_bytes[slot];
+      const uint4* src = reinterpret_cast<const uint4*>(&tmpl);
+      CUtensorMap* dst = set + size_t(b) * kNumMapSlots + slot;
       uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll
       for (int i = 0; i < 8; ++i) d4[i] = src[i];
       tmap_replace_address(dst, static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb));
       tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
-      const int64_t total = is_q_side ? p.total_q : p.total_kv;
-      if (len <= 0 || row0 < 0 || row0 + len > total) continue;
+      const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
+      if (len <= 0 || row0 < 0 || row0 + len > total) return;
       const int64_t g0 = row0 + (len - 1) / kBM * kBM;  // first row of the sequence's last tile
       if (g0 + kBM > total) {
         const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
-        CUtensorMap* tdst =
-            out_maps + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total);
+        CUtensorMap* tdst = set + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total);
         uint4* t4 = reinterpret_cast<uint4*>(tdst);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t4[i] = src[i];
-        tmap_replace_address(tdst, p.ws + p.L.tail + size_t(slot) * kTailRows * rb + size_t(g0 - (total - n)) * rb);
+        tmap_replace_address(
+            tdst, p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(g0 - (total - n)) * rb);
         tmap_replace_dim1(tdst, uint32_t(row0 + len - g0));
       }
+    };
+    for (size_t idx = gt; idx < size_t(p.B) * kNumMapSlots; idx += gstride) {
+      const int b = int(idx / kNumMapSlots), slot = int(idx % kNumMapSlots);
+      if (!maps.used[slot]) continue;
+      const bool is_q_side = (slot == kMapQ || slot == kMapDO);
+      int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
+      int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
+      if (p.win.window > 0 && !is_q_side) {
+        // the window part, and the sinks' own map (with malformed lengths neither is used)
+        const int64_t lq = p.q_off[b + 1] - p.q_off[b];
+        if (lq < 0 || len < 0 || lq > (int64_t(1) << 30) || len > (int64_t(1) << 30)) continue;
+        const WinSeq ws = win_seq(int(lq), int(len), p.win.window, p.win.sinks);
+        if (p.win.sinks > 0)
+          write_map(reinterpret_cast<CUtensorMap*>(p.ws + p.L.smaps), maps.sink_tmpl[slot - kMapK], b, slot, row0, ws.ns);
+        row0 += ws.org;
+        len = ws.Lk;
+      }
+      write_map(out_maps, maps.tmpl[slot], b, slot, row0, len);
     }
     tmap_release();
     return;
@@ -341,17 +379,20 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       atomicCAS(&hdr->status, 0, int(JFA_ERR_BAD_OFFSETS));
       hdr->n_fwd = hdr->n_dq = hdr->n_dkv = hdr->n_fused = hdr->n_nsp = 0;
       hdr->total_qpad = 0;  // the preprocess walks no rows
+      if (blockIdx.x == 0) hdr->planned = 0;
     }
     return;
   }
 
   // ---- work lists
+  if (blockIdx.x == 0 && tid == 0) hdr->planned = 1;
   if (!p.backward) {
     emit_list(p, kListFwd, reinterpret_cast<WorkItem*>(p.ws + p.L.fwd), p.L.cap_fwd, &hdr->n_fwd, hist, base);
   } else if (blockIdx.x == 0) {
     write_qpad(p);
     emit_list(p, kListDkv, reinterpret_cast<WorkItem*>(p.ws + p.L.dkv), p.L.cap_dkv, &hdr->n_dkv, hist,
               base);
+    if (tid == 0 && p.win.window > 0) hdr->n_fused = hdr->n_nsp = 0;  // no such lists
   } else if (blockIdx.x == 1) {
     emit_list(p, kListDq, reinterpret_cast<WorkItem*>(p.ws + p.L.dq), p.L.cap_dq, &hdr->n_dq, hist, base);
   } else if (blockIdx.x == 2) {
@@ -404,10 +445,11 @@ cudaError_t launch_plan(const Problem& pr, const PlanMaps& maps, void* ws, const
   p.jb_off = pr.jb_off;
   p.jb_plane = pr.jb_plane;
   p.nb = pr.num_buckets;
+  p.win = pr.win;
   // one CTA per list; helpers for the maps (one thread each), tail copies and bias table
   const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots + 1023) / 1024;
   const int helpers = int(map_ctas < 1 ? 1 : (map_ctas > 32 ? 32 : map_ctas)) + 4;
-  return launch_pdl(plan_kernel, dim3((backward ? 4 : 1) + helpers), dim3(1024), 0, stream, maps, p);
+  return launch_pdl(plan_kernel, dim3((!backward ? 1 : pr.win.window > 0 ? 2 : 4) + helpers), dim3(1024), 0, stream, maps, p);
 }
 
 }  // namespace jfa

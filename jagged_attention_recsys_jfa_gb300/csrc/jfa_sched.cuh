@@ -24,6 +24,10 @@ struct ItemMeta {
   int64_t jb;         // general jagged bias: the sequence's block offset in each head's plane
 };
 
+// With a sliding window, ko and Lk are those of the sequence's window part, and jb holds its
+// (org, sinks) instead.
+__device__ __forceinline__ WinSeq meta_win(const ItemMeta& m) { return {int(m.jb), int(m.jb >> 32), m.Lk}; }
+
 struct MetaRing {
   ItemMeta e[kMetaSlots];
   uint64_t full[kMetaSlots], empty[kMetaSlots];
@@ -47,9 +51,11 @@ __device__ __forceinline__ void meta_init(MetaRing& r, const uint64_t* wait_ns, 
 // end marker (b = -1) that ends every role's loop.  Slot k % kMetaSlots was last used by
 // item k - 4, which every role released before item k - 2.  False when a bounded wait ran
 // out (the CTA is aborting).
+template <bool kWin = false>
 __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items, int n_items, int* claim,
                                              const int64_t* q_off, const int64_t* kv_off, const int64_t* qpad,
-                                             const int64_t* jb_off, volatile int* abort) {
+                                             const int64_t* jb_off, volatile int* abort, int window = 0,
+                                             int sinks = 0) {
   for (uint32_t k = 0;; ++k) {
     if (k >= 2) {
       const uint32_t kp = k - 2;
@@ -69,6 +75,12 @@ __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items,
       m.Lk = int(kv_off[wi.b + 1] - m.ko);
       m.qp = qpad ? qpad[wi.b] : 0;
       m.jb = jb_off ? jb_off[wi.b] : 0;
+      if (kWin) {
+        const WinSeq ws = win_seq(m.Lq, m.Lk, window, sinks);
+        m.ko += ws.org;
+        m.Lk = ws.Lk;
+        m.jb = (int64_t(ws.org) << 32) | int64_t(ws.ns);
+      }
     } else {
       m = ItemMeta{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     }

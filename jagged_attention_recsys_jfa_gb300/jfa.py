@@ -25,7 +25,8 @@ STATUS_NAMES = {0: "JFA_OK", 1: "JFA_ERR_INVALID_ARG", 2: "JFA_ERR_UNSUPPORTED",
 EXPORTED_SYMBOLS = ("jfa_workspace_size", "jfa_forward", "jfa_forward_noalloc", "jfa_backward", "jfa_check_status",
                     "jfa_status_string", "jfa_last_launch_count", "jfa_last_error", "jfa_timing_enable",
                     "jfa_timing_read", "jfa_trace_configure", "jfa_selftest_wait_timeout", "jfa_wait_limit_ns",
-                    "jfa_set_nsp_max_tiles", "jfa_cache_workspace_size", "jfa_cache_append", "jfa_cache_attention")
+                    "jfa_set_nsp_max_tiles", "jfa_window_workspace_size", "jfa_window_forward", "jfa_window_backward",
+                    "jfa_cache_workspace_size", "jfa_cache_append", "jfa_cache_attention")
 KERNEL_KINDS = ("plan", "forward", "bwd_preprocess", "bwd_dkdv", "bwd_dq", "bwd_fused", "bwd_nsp", "bwd_join",
                 "cache_append", "cache_attention")
 
@@ -104,6 +105,13 @@ def load_library(build_if_missing: bool = True) -> ctypes.CDLL:
     lib.jfa_wait_limit_ns.restype = ctypes.c_uint64
     lib.jfa_trace_configure.argtypes = [vp, sz, i32]
     lib.jfa_trace_configure.restype = i32
+    lib.jfa_window_workspace_size.argtypes = [i32, i32, i32, i32, i64, i64, i32, i32]
+    lib.jfa_window_workspace_size.restype = sz
+    lib.jfa_window_forward.argtypes = [vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i32, i32, f32, vp, vp, vp, sz, vp]
+    lib.jfa_window_forward.restype = i32
+    lib.jfa_window_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i64, i32, i32, f32,
+                                        vp, vp, vp, vp, sz, vp]
+    lib.jfa_window_backward.restype = i32
     cache = ctypes.POINTER(_Cache)
     lib.jfa_cache_workspace_size.argtypes = [i32, i32, i32, i32]
     lib.jfa_cache_workspace_size.restype = sz
@@ -317,7 +325,7 @@ def jfa_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, bias=None, bias
     return dq, dk, dv, workspace
 
 
-# ---------------------------------------------------------------- paged key/value cache
+# ---------------------------------------------------------------- sliding window with sinks
 def _on(device, stream):
     """Context of a call: `stream` current (so that what the call allocates and clears is
     ordered with its kernels), else `device` current (no-op when it already is)."""
@@ -326,6 +334,107 @@ def _on(device, stream):
     return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
+def window_workspace_size(B, H, H_kv, d, total_q, total_kv, sinks, backward) -> int:
+    return int(load_library().jfa_window_workspace_size(B, H, H_kv, d, total_q, total_kv, sinks, 1 if backward else 0))
+
+
+def new_window_workspace(B, H, H_kv, d, total_q, total_kv, sinks, backward, device) -> torch.Tensor:
+    """A zero-initialised workspace for jfa_window_forward (backward=False) or jfa_window_backward."""
+    nbytes = window_workspace_size(B, H, H_kv, d, total_q, total_kv, sinks, backward)
+    if nbytes == 0:
+        raise ValueError(f"no window workspace for B={B}, H={H}, H_kv={H_kv}, d={d}, sinks={sinks}")
+    return _workspace(nbytes, device)
+
+
+def _check_windowed(q, k, v, q_offsets, kv_offsets, others):
+    """Checks of the inputs both directions share; returns (B, Tq, H, G, d, Tk)."""
+    _check_values("q", q)
+    Tq, H, d = q.shape
+    _check_values("k", k)
+    Tk, G = k.shape[0], k.shape[1]
+    if k.shape[2] != d or G < 1 or H % G:
+        raise ValueError(f"k has shape {tuple(k.shape)}, expected [*, a divisor of {H}, {d}]")
+    _check_values("v", v, rows=Tk, H=G, d=d)
+    _check_offsets("q_offsets", q_offsets)
+    _check_offsets("kv_offsets", kv_offsets)
+    if kv_offsets.numel() != q_offsets.numel():
+        raise ValueError("q_offsets and kv_offsets must have the same length")
+    for name, t in (("k", k), ("v", v), ("q_offsets", q_offsets), ("kv_offsets", kv_offsets), *others):
+        if t.device != q.device:
+            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+    return q_offsets.numel() - 1, Tq, H, G, d, Tk
+
+
+def jfa_window_forward(q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None, out=None, lse=None,
+                       workspace=None, stream=None):
+    """out, lse, workspace = jfa_window_forward(...): causal jagged attention in a sliding window.
+
+    q: bf16 [Tq, H, d]; k, v: bf16 [Tk, H_kv, d], H a multiple of H_kv; offsets: int64 [B+1] on the
+    device.  Query i of a sequence, at position p = i + Lk - Lq, sees key j iff j <= p and
+    (j > p - window or j < sinks); window None: every key up to p.  Returns out bf16 [Tq, H, d]
+    and lse fp32 [H, Tq].  Asynchronous; device-side errors are reported by
+    jfa_check_status(workspace).
+    """
+    lib = load_library()
+    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets, ())
+    window = _check_window(window, sinks)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = int(lib.jfa_window_workspace_size(B, H, G, d, Tq, Tk, int(sinks), 0))
+    with _on(q.device, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = _workspace(nbytes, q.device)
+        _check_values("out", out, rows=Tq, H=H, d=d)
+        _check_lse(lse, H, Tq)
+        for name, t in (("out", out), ("lse", lse)):
+            if t.device != q.device:
+                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+        ws_bytes = _check_workspace(workspace, nbytes, q.device)
+        st = lib.jfa_window_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), kv_offsets.data_ptr(),
+                                    B, H, G, d, Tq, Tk, window, int(sinks), scale, out.data_ptr(), lse.data_ptr(),
+                                    workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    if st != JFA_OK:
+        raise JfaError(st, "jfa_window_forward")
+    return out, lse, workspace
+
+
+def jfa_window_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, window=None, sinks=0, scale=None, dq=None,
+                        dk=None, dv=None, workspace=None, stream=None):
+    """dq, dk, dv, workspace = jfa_window_backward(...): gradients of sum(dout * out), out and lse
+    being jfa_window_forward's results for the same inputs.  dk and dv (shaped like k and v) sum
+    over the query heads that share a key/value head."""
+    lib = load_library()
+    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets, (("dout", dout), ("out", out), ("lse", lse)))
+    for name, t in (("dout", dout), ("out", out)):
+        _check_values(name, t, rows=Tq, H=H, d=d)
+    _check_lse(lse, H, Tq)
+    window = _check_window(window, sinks)
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    nbytes = int(lib.jfa_window_workspace_size(B, H, G, d, Tq, Tk, int(sinks), 1))
+    with _on(q.device, stream):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = _workspace(nbytes, q.device)
+        for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+            _check_values(name, t, rows=ref.shape[0], H=ref.shape[1], d=d)
+            if t.device != q.device:
+                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
+        ws_bytes = _check_workspace(workspace, nbytes, q.device)
+        st = lib.jfa_window_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                     lse.data_ptr(), q_offsets.data_ptr(), kv_offsets.data_ptr(), B, H, G, d, Tq, Tk,
+                                     window, int(sinks), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                                     workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    if st != JFA_OK:
+        raise JfaError(st, "jfa_window_backward")
+    return dq, dk, dv, workspace
+
+
+# ---------------------------------------------------------------- paged key/value cache
 def _check_int32(name, t, shape, device):
     if (not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or tuple(t.shape) != shape
             or not t.is_contiguous()):
@@ -579,3 +688,26 @@ def jagged_attention(q, k, v, q_offsets, kv_offsets, bias=None, bias_center=0, s
     jb_values, jb_offsets = jagged_bias if jagged_bias is not None else (None, None)
     return JaggedAttention.apply(q, k, v, q_offsets, kv_offsets, bias, bias_center, scale, causal, jb_values,
                                  jb_offsets)
+
+
+class WindowAttention(torch.autograd.Function):
+    """Differentiable windowed attention: out = WindowAttention.apply(q, k, v, q_offsets,
+    kv_offsets, window, sinks, scale).  lse is saved for the backward."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None):
+        out, lse, _ = jfa_window_forward(q, k, v, q_offsets, kv_offsets, window, sinks, scale)
+        ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets)
+        ctx.cfg = (window, sinks, scale)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, q_offsets, kv_offsets = ctx.saved_tensors
+        dq, dk, dv, _ = jfa_window_backward(dout.contiguous(), q, k, v, out, lse, q_offsets, kv_offsets, *ctx.cfg)
+        return dq, dk, dv, None, None, None, None, None
+
+
+def window_attention(q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None):
+    """Causal jagged attention in a sliding window with sinks (jfa_window_forward), differentiable."""
+    return WindowAttention.apply(q, k, v, q_offsets, kv_offsets, window, sinks, scale)
