@@ -222,21 +222,25 @@ jfa_status check_window(int H, int H_kv, int d, int64_t total_kv, int window, in
 }
 
 // The templates of a windowed call: K and V have H_kv heads, and maps of their own for the sinks.
-jfa_status window_maps(PlanMaps* maps, const Problem& pr, const void* q, const void* k, const void* v, const void* dout) {
+// The forward loads them in tiles of kWinKeys rows, the backward of kBN.
+jfa_status window_maps(PlanMaps* maps, const Problem& pr, const void* q, const void* k, const void* v, const void* dout,
+                       bool backward) {
   std::memset(maps, 0, sizeof(*maps));
   const int G = pr.win.H_kv;
+  const int keys = backward ? kBN : kWinKeys, sink_box = backward ? sink_rows(pr.win.sinks) : win_sink_box(pr.win.sinks);
   const void* kbase = pr.total_kv > 0 ? k : q;  // maps of a side without rows are never read
   const void* vbase = pr.total_kv > 0 ? v : kbase;
   const void* qbase = pr.total_q > 0 ? q : kbase;
   const void* base[kNumMapSlots] = {qbase, kbase, vbase, pr.total_q > 0 ? dout : kbase};
   for (int i = 0; i < kNumMapSlots; ++i) {
-    if (i == kMapDO && !dout && pr.total_q > 0) continue;  // forward
+    if (i == kMapDO && !backward) continue;
     const bool kv = i == kMapK || i == kMapV;
     const int heads = kv ? G : pr.H;
     const int64_t rows = kv ? pr.total_kv : pr.total_q;
-    jfa_status st = encode_template(&maps->tmpl[i], base[i], rows, heads, pr.d);
-    if (st == JFA_OK && kv) st = encode_template(&maps->sink_tmpl[i - kMapK], base[i], rows, heads, pr.d, sink_rows(pr.win.sinks));
+    jfa_status st = encode_template(&maps->tmpl[i], base[i], rows, heads, pr.d, kv ? keys : kBM);
+    if (st == JFA_OK && kv) st = encode_template(&maps->sink_tmpl[i - kMapK], base[i], rows, heads, pr.d, sink_box);
     if (st != JFA_OK) return st;
+    maps->tile_rows[i] = kv ? keys : kBM;
     maps->base[i] = base[i];
     maps->row_bytes[i] = uint32_t(heads) * uint32_t(pr.d) * 2;
     maps->used[i] = 1;
@@ -296,6 +300,7 @@ jfa_status jfa_forward(const void* q, const void* k, const void* v, const int64_
   maps.base[kMapV] = vbase;
   for (int i = 0; i < 3; ++i) {
     maps.row_bytes[i] = uint32_t(H) * uint32_t(d) * 2;
+    maps.tile_rows[i] = kBM;
     maps.used[i] = 1;
   }
   {
@@ -350,6 +355,7 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
   maps.base[kMapDO] = dobase;
   for (int i = 0; i < kNumMapSlots; ++i) {
     maps.row_bytes[i] = uint32_t(H) * uint32_t(d) * 2;
+    maps.tile_rows[i] = kBM;
     maps.used[i] = 1;
   }
   if (pr.jb_grad)  // pairs no pass visits (hidden by the causal mask) and the row padding read as 0
@@ -410,14 +416,14 @@ jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   PlanMaps maps;
-  if ((st = window_maps(&maps, pr, q, k, v, nullptr)) != JFA_OK) return st;
+  if ((st = window_maps(&maps, pr, q, k, v, nullptr, false)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);
     JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, false, nsm, s), "planner launch");
   }
   {
     KernelTimer t(JFA_KERNEL_FORWARD, s);
-    JFA_CHECK_LAUNCH(launch_forward(pr, workspace, L, out, lse, nsm, s), "forward launch");
+    JFA_CHECK_LAUNCH(launch_win_forward(pr, workspace, L, out, lse, nsm, s), "forward launch");
   }
   g_last_launches = 2;
   return JFA_OK;
@@ -447,7 +453,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   PlanMaps maps;
-  if ((st = window_maps(&maps, pr, q, k, v, dout)) != JFA_OK) return st;
+  if ((st = window_maps(&maps, pr, q, k, v, dout, true)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);
     JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, true, nsm, s), "planner launch");

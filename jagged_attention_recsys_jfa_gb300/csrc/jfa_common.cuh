@@ -171,8 +171,15 @@ struct WindowSpec {
 };
 constexpr int kMaxWindow = 1 << 30;  // at least any sequence length
 constexpr int kMaxSinks = 128;       // one key tile
+// The windowed forward: keys per step, and CTAs per SM.
+constexpr int kWinKeys = 64;
+constexpr int kWinCtasPerSm = 2;
 // Rows of the boxes that load the sinks: whole MMA steps of 16 keys (rows past them arrive as zeros).
 __host__ __device__ inline int sink_rows(int sinks) { return sinks < 1 ? 16 : (sinks + 15) / 16 * 16; }
+// The same in the forward, whose steps have at most kWinKeys keys.
+__host__ __device__ inline int win_sink_box(int sinks) {
+  return sink_rows(sinks) < kWinKeys ? sink_rows(sinks) : kWinKeys;
+}
 // Query tiles of one chunk of the sinks' gradient.  Every query tile of a sequence sees its
 // sinks, so their dK / dV are summed chunk by chunk in fp32 partials, which join_kernel adds up
 // in order.
@@ -204,7 +211,7 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
   L.row_bytes = size_t(H) * size_t(d) * 2;
   L.tail = align_up(off, 1024);
   off = L.tail + size_t(backward ? 4 : 3) * kTailRows * L.row_bytes;
-  L.cap_fwd = int64_t(H) * (total_q / 256 + B + 1);
+  L.cap_fwd = int64_t(H) * (total_q / (windowed ? 128 : 256) + B + 1);
   L.fwd = align_up(off, 16);
   off = L.fwd + size_t(L.cap_fwd) * sizeof(WorkItem);
   L.bias2 = align_up(off, 256);
@@ -294,15 +301,15 @@ __host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S) {
   r.Lk = Lk - r.org;
   return r;
 }
-// Window-part key tiles [*a, *e) that query tile t visits.
-__host__ __device__ inline void win_kv_tiles(int t, int Lq, int Lk, int W, int* a, int* e) {
+// Window-part key tiles of `keys` keys, [*a, *e), that query tile t visits.
+__host__ __device__ inline void win_kv_tiles(int t, int Lq, int Lk, int W, int* a, int* e, int keys = kBN) {
   *a = *e = 0;
   if (t * kBM >= Lq || Lk <= 0) return;
   const int i0 = t * kBM, i1 = i0 + kBM - 1 < Lq - 1 ? i0 + kBM - 1 : Lq - 1, diag = Lk - Lq;
   if (i1 + diag < 0) return;
   const int lo = i0 + diag - W + 1;
-  *a = lo > 0 ? lo / kBN : 0;
-  *e = (i1 + diag) / kBN + 1;
+  *a = lo > 0 ? lo / keys : 0;
+  *e = (i1 + diag) / keys + 1;
 }
 // Whether a row of query tile t sees a sink (i.e. stands at a position >= 0).
 __host__ __device__ inline bool win_sees_sinks(int t, int Lq, const WinSeq& s) {
@@ -357,11 +364,11 @@ struct TileMap {
   bool tail;
 };
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                            int64_t total) {
-  const int64_t g0 = row0 + int64_t(t) * kBM;
-  if (g0 + kBM > total)
-    return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total), 0, true};
-  return {maps + size_t(b) * kNumMapSlots + slot, t * kBM, false};
+                                            int64_t total, int rows = kBM) {
+  const int64_t g0 = row0 + int64_t(t) * rows;
+  if (g0 + rows > total)
+    return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total), 0, true};
+  return {maps + size_t(b) * kNumMapSlots + slot, t * rows, false};
 }
 
 // Pull row tile `t` of a sequence (boxes of 64 columns from column col0) into L2 ahead of

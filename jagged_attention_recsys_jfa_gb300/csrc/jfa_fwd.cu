@@ -61,10 +61,6 @@ struct FwdParams {
   __nv_bfloat16* out;
   float* lse;
   TraceBuf trace;
-  WindowSpec win;            // sliding window with sinks (the kWin kernels)
-  int group;                 // query heads per key/value head
-  const CUtensorMap* smaps;  // the sinks' K / V maps
-  int sink_rows;             // rows of their boxes
 };
 
 template <int D>
@@ -90,18 +86,9 @@ struct ItemInfo {
   int Lq, Lk;
   int nkv0, nkv1, njt;
   bool has1;
-  // window: the unit's steps are the sinks (if any row sees them: nz = 1), then the window-part
-  // key tiles from kt0 on; query tile s of the pair takes part in the sinks' step if z[s], and in
-  // key tiles [a[s], e[s])
-  int nz, kt0, a[2], e[2];
-  bool z[2];
-  __device__ __forceinline__ bool active(int s, int step) const {
-    return step < nz ? z[s] : step < njt && step - nz + kt0 >= a[s] && step - nz + kt0 < e[s];
-  }
 };
 
 // Unit u (query-tile pair {2u, 2u+1}) of work item `it`.
-template <bool kWin = false>
 __device__ __forceinline__ ItemInfo decode(const FwdParams& p, const ItemMeta& it, int u) {
   ItemInfo r;
   r.b = it.b;
@@ -114,22 +101,6 @@ __device__ __forceinline__ ItemInfo decode(const FwdParams& p, const ItemMeta& i
   r.Lq = it.Lq;
   r.Lk = it.Lk;
   r.has1 = r.t1 * kBM < r.Lq;
-  if constexpr (kWin) {
-    const WinSeq ws = meta_win(it);
-    r.nz = 0;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      win_kv_tiles(2 * u + s, r.Lq, r.Lk, p.win.window, &r.a[s], &r.e[s]);
-      r.z[s] = win_sees_sinks(2 * u + s, r.Lq, ws);
-      if (r.z[s]) r.nz = 1;
-    }
-    // the second tile's keys start and end no earlier than the first's, when both have any
-    r.kt0 = r.e[0] > r.a[0] ? r.a[0] : r.a[1];
-    r.nkv0 = r.e[0] - r.a[0] + (r.z[0] ? 1 : 0);
-    r.nkv1 = r.e[1] - r.a[1] + (r.z[1] ? 1 : 0);
-    r.njt = r.nz + max(r.e[0], r.e[1]) - r.kt0;
-    return r;
-  }
   r.nkv0 = kv_tiles_for_q_tile(r.t0, r.Lq, r.Lk, p.causal != 0);
   r.nkv1 = r.has1 ? kv_tiles_for_q_tile(r.t1, r.Lq, r.Lk, p.causal != 0) : 0;
   r.njt = max(r.nkv0, r.nkv1);
@@ -146,10 +117,7 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// kWin: causal attention in a sliding window with sinks, query heads sharing key/value heads.
-// Only the key tiles that the pair's windows reach are visited; the sinks are a step of their
-// own, with as many keys as their boxes hold (16 .. 128).
-template <int D, bool kBias, bool kJBias = false, bool kWin = false>
+template <int D, bool kBias, bool kJBias = false>
 __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
   using C = FwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -215,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
        const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
        for (int u = wi.u0; u < wi.u1 && ok; ++u) {
-        const ItemInfo it = decode<kWin>(p, wi, u);
+        const ItemInfo it = decode(p, wi, u);
         if (it.njt == 0) continue;
         const TileMap q0 = tile_map(p.maps, p.B, kMapQ, it.b, it.qo, it.t0, p.total_q);
         const TileMap q1 = it.has1 ? tile_map(p.maps, p.B, kMapQ, it.b, it.qo, it.t1, p.total_q) : q0;
@@ -274,20 +242,15 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
        const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
        for (int u = wi.u0; u < wi.u1 && ok; ++u) {
-        const ItemInfo it = decode<kWin>(p, wi, u);
+        const ItemInfo it = decode(p, wi, u);
         if (it.njt == 0) continue;
         if (it.b != acq_b) {
           tmap_acquire(p.maps + size_t(it.b) * kNumMapSlots + kMapK);
           tmap_acquire(p.maps + size_t(it.b) * kNumMapSlots + kMapV);
-          if (kWin && p.win.sinks > 0) {
-            tmap_acquire(p.smaps + size_t(it.b) * kNumMapSlots + kMapK);
-            tmap_acquire(p.smaps + size_t(it.b) * kNumMapSlots + kMapV);
-          }
           acq_b = it.b;
         }
-        const int col = (kWin ? it.h / p.group : it.h) * D;  // first column of the key/value head
         // last unit of this item: pull the first key tiles of this CTA's next item into L2
-        if (const ItemMeta* wnp = !kWin && u + 1 == wi.u1 ? meta_peek_next(meta, k) : nullptr) {
+        if (const ItemMeta* wnp = u + 1 == wi.u1 ? meta_peek_next(meta, k) : nullptr) {
           const ItemMeta& wn = *wnp;
           const int64_t nko = p.kv_off[wn.b];
           const int nLk = int(p.kv_off[wn.b + 1] - nko);
@@ -305,12 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
           }
         }
         for (int j = 0; j < it.njt && ok; ++j) {
-          const bool sink = kWin && j < it.nz;
-          const CUtensorMap* maps = sink ? p.smaps : p.maps;
-          const int64_t row0 = sink ? it.ko - meta_win(wi).org : it.ko;
-          const int kt = kWin ? (sink ? 0 : j - it.nz + it.kt0) : j;
-          const TileMap mk = tile_map(maps, p.B, kMapK, it.b, row0, kt, p.total_kv);
-          const TileMap mv = tile_map(maps, p.B, kMapV, it.b, row0, kt, p.total_kv);
+          const TileMap mk = tile_map(p.maps, p.B, kMapK, it.b, it.ko, j, p.total_kv);
+          const TileMap mv = tile_map(p.maps, p.B, kMapV, it.b, it.ko, j, p.total_kv);
           if (mk.tail) {
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
@@ -320,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
             const uint32_t e = ring_n % C::kStages, ph = (ring_n / C::kStages) & 1;
             if (!mbar_wait(&kv_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
             trace_event(p.trace, kTraceProducer, tn, 2);
-            mbar_arrive_expect_tx(&kv_full[e], sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes));
+            mbar_arrive_expect_tx(&kv_full[e], C::kTileBytes);
             uint8_t* dst = sRing + e * C::kTileBytes;
 #pragma unroll
             for (int c = 0; c < C::kBoxes; ++c)
-              tma_load_2d(dst + c * 16384, kv ? mv.map : mk.map, &kv_full[e], col + c * 64, mk.y);
+              tma_load_2d(dst + c * 16384, kv ? mv.map : mk.map, &kv_full[e], it.h * D + c * 64, mk.y);
             ++ring_n;
           }
         }
@@ -357,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
        const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
        for (int u = wi.u0; u < wi.u1 && ok; ++u) {
-        const ItemInfo it = decode<kWin>(p, wi, u);
+        const ItemInfo it = decode(p, wi, u);
         if (it.njt == 0) continue;
         const int nkv[2] = {it.nkv0, it.nkv1};
         if (!C::kQTmem) {
@@ -367,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
         }
         if (lane == 0) trace_event(p.trace, kTraceMma, tn, 10);
         int s_left = it.nkv0 + it.nkv1;
-        auto issue_S = [&](int s, uint32_t e, uint32_t id_s) {
+        auto issue_S = [&](int s, uint32_t e) {
           // descriptor start addresses are in 16-byte units in the low bits: step by adding
           const uint64_t qd = sdesc_sw128(sQ_addr + s * C::kTileBytes, 16, 1024);
           const uint64_t kd = sdesc_sw128(sR_addr + e * C::kTileBytes, 16, 1024);
@@ -376,9 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
               if (C::kQTmem)
-                umma_ts(tmem + colS[s], tmem + (s ? C::kColQ1 : C::kColQ0) + kk * 8, kd + o, id_s, kk > 0);
+                umma_ts(tmem + colS[s], tmem + (s ? C::kColQ1 : C::kColQ0) + kk * 8, kd + o, kIdS, kk > 0);
               else
-                umma_ss(tmem + colS[s], qd + o, kd + o, id_s, kk > 0);
+                umma_ss(tmem + colS[s], qd + o, kd + o, kIdS, kk > 0);
             }
           }
           mma_commit(&s_full[s]);
@@ -394,16 +353,9 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
           tc_fence_after();
           return r;
         };
-        auto issue_PV = [&](int s, uint32_t e, bool acc, bool sink) {
+        auto issue_PV = [&](int s, uint32_t e, bool acc) {
           const uint64_t vd = sdesc_sw128(sR_addr + e * C::kTileBytes, 16384, 1024);
-          if (kWin && sink) {  // the sinks' keys only
-            if (elect_one()) {
-#pragma unroll 1
-              for (int kk = 0; kk < p.sink_rows / 16; ++kk)
-                umma_ts(tmem + colO[s], tmem + colS[s] + kk * 8, vd + uint32_t(kk * 2048 >> 4), kIdPV,
-                        (acc || kk > 0) ? 1u : 0u);
-            }
-          } else if (elect_one()) {
+          if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kBN / 16; ++kk)
               umma_ts(tmem + colO[s], tmem + colS[s] + kk * 8, vd + uint32_t(kk * 2048 >> 4), kIdPV,
@@ -417,26 +369,22 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
           return r;
         };
         const uint32_t n0 = ring_n;  // K_j at n0 + 2j, V_j at n0 + 2j + 1
-        const uint32_t id_sink = idesc_bf16_f32(128, kWin ? p.sink_rows : 128, false, false);
-        auto active = [&](int s, int j) -> bool { return kWin ? it.active(s, j) : j < nkv[s]; };
-        auto id_of = [&](int j) -> uint32_t { return kWin && j < it.nz ? id_sink : kIdS; };
-        int s_seen[2] = {0, 0}, pv_seen[2] = {0, 0};  // window: S and PV products issued per query tile
         if (!wait_full(n0)) { ok = false; break; }
-        for (int s = 0; s < 2 && ok; ++s) {
-          if (active(s, 0)) {
-            if (!wait_qt(s)) { ok = false; break; }
-            ++s_seen[s];
-            issue_S(s, n0 % C::kStages, id_of(0));
-          }
+        if (it.nkv0 > 0) {
+          if (!wait_qt(0)) { ok = false; break; }
+          issue_S(0, n0 % C::kStages);
         }
-        if (!ok) break;
+        if (it.nkv1 > 0) {
+          if (!wait_qt(1)) { ok = false; break; }
+          issue_S(1, n0 % C::kStages);
+        }
         mma_commit(&kv_empty[n0 % C::kStages]);
         for (int j = 0; j < it.njt && ok; ++j) {
           const uint32_t nv = n0 + 2 * j + 1, nk = n0 + 2 * j + 2;
           if (!wait_full(nv)) { ok = false; break; }
           bool k_ready = false;
           for (int s = 0; s < 2 && ok; ++s) {
-            if (active(s, j)) {
+            if (j < nkv[s]) {
               if (!__all_sync(0xffffffffu, mbar_wait(&p_full[s], p_n[s] & 1, abort_flag, kWaitTimeoutNs))) {
                 ok = false;
                 break;
@@ -444,17 +392,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
               ++p_n[s];
               tc_fence_after();
               if (lane == 0) trace_event(p.trace, kTraceMma, tn, 12 + s);
-              issue_PV(s, nv % C::kStages, kWin ? pv_seen[s] > 0 : j > 0, kWin && j < it.nz);
+              issue_PV(s, nv % C::kStages, j > 0);
               if (lane == 0) trace_event(p.trace, kTraceMma, tn, 14 + s);
-              if (kWin ? ++pv_seen[s] == nkv[s] : j == nkv[s] - 1) mma_commit(&o_full[s]);
+              if (j == nkv[s] - 1) mma_commit(&o_full[s]);
             }
-            if (active(s, j + 1)) {
+            if (j + 1 < nkv[s]) {
               if (!k_ready) {
                 if (!wait_full(nk)) { ok = false; break; }
                 k_ready = true;
               }
-              if (kWin && s_seen[s]++ == 0 && !wait_qt(s)) { ok = false; break; }
-              issue_S(s, nk % C::kStages, id_of(j + 1));
+              issue_S(s, nk % C::kStages);
             }
           }
           if (!ok) break;
@@ -471,8 +418,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
     }
   } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, nullptr, p.jb_off, abort_flag,
-                                         p.win.window, p.win.sinks))
+    if (lane == 0 && !meta_publish(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, nullptr, p.jb_off, abort_flag))
       raise_status(p.status, JFA_ERR_TIMEOUT);
   }
   } else {
@@ -495,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
      const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
      if (wi.b < 0) break;  // end of this CTA's items
      for (int u = wi.u0; u < wi.u1 && ok; ++u) {
-      const ItemInfo it = decode<kWin>(p, wi, u);
+      const ItemInfo it = decode(p, wi, u);
       const int t = s ? it.t1 : it.t0;
       const int nkv = s ? it.nkv1 : it.nkv0;
       if (C::kQTmem && it.njt > 0) {
@@ -540,10 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
       const int diag = it.Lk - it.Lq;  // causal: key j visible iff j <= i + diag
       const float* brow = kBias ? p.bias2 + size_t(it.h) * p.num_buckets : nullptr;
       float m = -INFINITY, l = 0.f;
-      const int steps = kWin ? it.njt : nkv;
-      bool first = true;  // window: no step of this tile done yet
-      for (int j = 0; j < steps; ++j) {
-        if (kWin && !it.active(s, j)) continue;
+      for (int j = 0; j < nkv; ++j) {
         uint32_t jbk[kJBias ? 64 : 1];  // general bias for this tile, loaded before the wait
         if (kJBias) {
           const int64_t pitch = (it.Lk + 7) / 8 * 8;  // rows of the sequence's block: bias[i][j] at i * pitch + j
@@ -555,8 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
             prefetch_l2(brow_j + kvj + kBN + 64);
           }
         }
-        const bool sink = kWin && j < it.nz;
-        const int kv0 = kWin ? (j - it.nz + it.kt0) * kBN : j * kBN;
+        const int kv0 = j * kBN;
         const bool last = (j == nkv - 1);
         // relative-position bias * log2(e) of this tile's columns, loaded before the wait so the
         // loads overlap the MMAs (0 on padded key columns, which then score exactly 0)
@@ -615,23 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
           // x = scale*log2e * (q.k) + bias*log2e from this row of the sequence's block
           jbias_apply<128>(x, jbk, sl2, kLog2e);
         }
-        if (kWin) {
-          // visible columns [clo, chi] of this row in this tile; the sinks' step shows its keys
-          // up to the row's own position (columns behind them were not computed)
-          const WinSeq ws = meta_win(wi);
-          const int chi = sink ? min(ws.ns - 1, i + diag + ws.org) : i + diag - kv0;
-          const int clo = sink ? 0 : chi - p.win.window + 1;
-          if (chi < kBN - 1) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > chi) x[c] = -INFINITY;
-          }
-          if (clo > 0) {
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c < clo) x[c] = -INFINITY;
-          }
-        } else if (p.causal) {
+        if (p.causal) {
           const int lim = i + diag - kv0;  // last visible column of this row in this tile
           if (lim < kBN - 1) {
 #pragma unroll
@@ -682,14 +608,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
           sum4[k] = lo + hi;
         }
         float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
-        if (!kWin && last && !p.causal && kv0 + kBN > it.Lk) {
+        if (last && !p.causal && kv0 + kBN > it.Lk) {
           // subtraction scheme: padded keys scored exactly 0, each added exp2(0 - m_use)
           sum -= float(kv0 + kBN - it.Lk) * ex2_approx(-m_use);
         }
         l += sum;
         // O still holds the sum over earlier tiles (their PV MMAs completed before this
         // tile's S did); rescale it now that the S registers are free
-        if (__any_sync(0xffffffffu, need) && (kWin ? !first : j > 0)) {
+        if (__any_sync(0xffffffffu, need) && j > 0) {
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t r[32];
@@ -703,7 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(&p_full[s]);
-        first = false;
         if (leader) trace_event(p.trace, kTraceCompute0 + s, tn, 21);
       }
       if (!ok) break;
@@ -746,10 +671,10 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool kBias, bool kJBias = false, bool kWin = false>
+template <int D, bool kBias, bool kJBias = false>
 cudaError_t launch_fwd_t(const FwdParams& fp, int grid, cudaStream_t stream) {
   using C = FwdCfg<D>;
-  auto kern = fwd_kernel<D, kBias, kJBias, kWin>;
+  auto kern = fwd_kernel<D, kBias, kJBias>;
   cudaError_t e = check_launch_registers(kern);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
@@ -787,13 +712,6 @@ cudaError_t launch_forward(const Problem& pr, void* ws, const WsLayout& L, void*
   fp.lse = lse;
   fp.trace = pr.trace[JFA_KERNEL_FORWARD];
   const int grid = num_sms;
-  fp.win = pr.win;
-  fp.group = pr.win.window > 0 ? pr.H / pr.win.H_kv : 1;
-  fp.smaps = reinterpret_cast<const CUtensorMap*>(w + L.smaps);
-  fp.sink_rows = sink_rows(pr.win.sinks);
-  if (pr.win.window > 0)
-    return pr.d == 128 ? launch_fwd_t<128, false, false, true>(fp, grid, stream)
-                       : launch_fwd_t<64, false, false, true>(fp, grid, stream);
   const bool bias = pr.bias_table != nullptr;
   const bool jb = pr.jbias != nullptr;
   if (pr.d == 128)

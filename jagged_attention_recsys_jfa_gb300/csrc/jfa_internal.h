@@ -28,9 +28,10 @@ struct Problem {
 
 struct PlanMaps {
   CUtensorMap tmpl[kNumMapSlots];  // whole-tensor templates; the planner patches per-sequence copies
-  CUtensorMap sink_tmpl[2];        // window: K and V again, with boxes of sink_rows(sinks) rows
+  CUtensorMap sink_tmpl[2];        // window: K and V again, with boxes for the sinks
   const void* base[kNumMapSlots];  // tensor base pointers (row 0)
   uint32_t row_bytes[kNumMapSlots];
+  int tile_rows[kNumMapSlots];         // rows of the tiles that the kernels load through each map
   int used[kNumMapSlots];
 };
 
@@ -83,6 +84,9 @@ cudaError_t launch_wait_timeout_selftest(void* ws, uint64_t timeout_ns, cudaStre
 
 cudaError_t launch_forward(const Problem& p, void* ws, const WsLayout& L, void* out, float* lse,
                            int num_sms, cudaStream_t stream);
+
+cudaError_t launch_win_forward(const Problem& p, void* ws, const WsLayout& L, void* out, float* lse, int num_sms,
+                               cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const Problem& p, const void* dout, const void* out, const float* lse,
                                   void* ws, const WsLayout& L, int num_sms, cudaStream_t stream);

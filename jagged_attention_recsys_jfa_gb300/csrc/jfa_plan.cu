@@ -39,15 +39,14 @@ enum ListKind { kListFwd = 0, kListDq = 1, kListDkv = 2, kListFused = 3, kListNs
 // once); the others by the split dK/dV and dQ passes.  Units: key tiles, except for the
 // forward (query-tile pairs) and the dQ pass (query tiles); a sequence without keys still
 // gets one unit in the fused and non-sequence-parallel lists (its dq rows are zeroed there).
-// With a sliding window every sequence goes through the forward, dQ and dK/dV lists; the dK/dV
+// With a sliding window the forward's units are query tiles, and every sequence goes through the forward, dQ and dK/dV lists; the dK/dV
 // units are the key tiles of the window part, then the chunks of the sinks.
 __device__ __forceinline__ int list_units(const PlanParams& p, int kind, int Lq, int Lk) {
   const int nsp_max = p.nsp_max_tiles;
   const int nq = (Lq + kBM - 1) / kBM;
   const int nk = (Lk + kBN - 1) / kBN;
   if (p.win.window > 0) {
-    if (kind == kListFwd) return (nq + 1) / 2;
-    if (kind == kListDq) return nq;
+    if (kind == kListFwd || kind == kListDq) return nq;
     const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
     return (s.Lk + kBN - 1) / kBN + win_sink_chunks(Lq, s, p.H / p.win.H_kv);
   }
@@ -58,9 +57,9 @@ __device__ __forceinline__ int list_units(const PlanParams& p, int kind, int Lq,
   return kind == kListDq ? nq : nk;
 }
 
-__device__ __forceinline__ int win_tile_cost(int t, int Lq, const WinSeq& s, int W) {
+__device__ __forceinline__ int win_tile_cost(int t, int Lq, const WinSeq& s, int W, int keys) {
   int a, e;
-  win_kv_tiles(t, Lq, s.Lk, W, &a, &e);
+  win_kv_tiles(t, Lq, s.Lk, W, &a, &e, keys);
   return e - a + (win_sees_sinks(t, Lq, s) ? 1 : 0);
 }
 
@@ -68,8 +67,8 @@ __device__ __forceinline__ int unit_cost(const PlanParams& p, int kind, int u, i
   const bool causal = p.causal != 0;
   if (p.win.window > 0) {
     const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
-    if (kind == kListFwd) return win_tile_cost(2 * u, Lq, s, p.win.window) + win_tile_cost(2 * u + 1, Lq, s, p.win.window);
-    if (kind == kListDq) return win_tile_cost(u, Lq, s, p.win.window);
+    if (kind == kListFwd) return win_tile_cost(u, Lq, s, p.win.window, kWinKeys);
+    if (kind == kListDq) return win_tile_cost(u, Lq, s, p.win.window, kBN);
     const WinKeyUnit k = win_key_unit(u, Lq, s, p.win.window, p.H / p.win.H_kv);
     return k.r1 - k.r0;
   }
@@ -315,6 +314,7 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
     CUtensorMap* out_maps = reinterpret_cast<CUtensorMap*>(p.ws + p.L.maps);
     auto write_map = [&](CUtensorMap* set, const CUtensorMap& tmpl, int b, int slot, int64_t row0, int64_t len) {
       const size_t rb = maps.row_bytes[slot];
+      const int rows = maps.tile_rows[slot];
       const uint4* src = reinterpret_cast<const uint4*>(&tmpl);
       CUtensorMap* dst = set + size_t(b) * kNumMapSlots + slot;
       uint4* d4 = reinterpret_cast<uint4*>(dst);
@@ -324,10 +324,10 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
       const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
       if (len <= 0 || row0 < 0 || row0 + len > total) return;
-      const int64_t g0 = row0 + (len - 1) / kBM * kBM;  // first row of the sequence's last tile
-      if (g0 + kBM > total) {
+      const int64_t g0 = row0 + (len - 1) / rows * rows;  // first row of the sequence's last tile
+      if (g0 + rows > total) {
         const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
-        CUtensorMap* tdst = set + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total);
+        CUtensorMap* tdst = set + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total);
         uint4* t4 = reinterpret_cast<uint4*>(tdst);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t4[i] = src[i];
@@ -435,7 +435,7 @@ cudaError_t launch_plan(const Problem& pr, const PlanMaps& maps, void* ws, const
   p.total_kv = pr.total_kv;
   p.causal = pr.causal;
   p.backward = backward ? 1 : 0;
-  p.grid = num_sms;
+  p.grid = pr.win.window > 0 && !backward ? kWinCtasPerSm * num_sms : num_sms;
   p.nsp_max_tiles = pr.nsp_max_tiles;
   p.d = pr.d;
   p.ws = static_cast<uint8_t*>(ws);
