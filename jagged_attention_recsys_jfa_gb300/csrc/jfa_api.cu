@@ -423,7 +423,7 @@ jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const
   }
   {
     KernelTimer t(JFA_KERNEL_FORWARD, s);
-    JFA_CHECK_LAUNCH(launch_win_forward(pr, workspace, L, out, lse, nsm, s), "forward launch");
+    JFA_CHECK_LAUNCH(launch_win_forward(pr, maps, workspace, L, out, lse, nsm, s), "forward launch");
   }
   g_last_launches = 2;
   return JFA_OK;

@@ -361,7 +361,7 @@ __host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq&
 struct TileMap {
   const CUtensorMap* map;
   int y;
-  bool tail;
+  bool tail;  // to be acquired before the load
 };
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
                                             int64_t total, int rows = kBM) {
@@ -369,6 +369,19 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int 
   if (g0 + rows > total)
     return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total), 0, true};
   return {maps + size_t(b) * kNumMapSlots + slot, t * rows, false};
+}
+
+// The same for a tile that lies wholly inside its sequence of `len` rows: the whole tensor's own
+// map, a kernel parameter, which needs no acquire and whose descriptor is fetched once per launch
+// (switching to another sequence's map costs a load about a microsecond).  Only a sequence's last,
+// partial tile goes through a map of its own.  `whole` is nullptr when row numbers need more than
+// 31 bits.
+__device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUtensorMap* maps, int B, int slot, int b,
+                                            int64_t row0, int t, int len, int64_t total, int rows = kBM) {
+  if (whole != nullptr && (t + 1) * rows <= len) return {whole, int(row0) + t * rows, false};
+  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows);
+  m.tail = true;  // not acquired yet
+  return m;
 }
 
 // Pull row tile `t` of a sequence (boxes of 64 columns from column col0) into L2 ahead of

@@ -85,8 +85,8 @@ cudaError_t launch_wait_timeout_selftest(void* ws, uint64_t timeout_ns, cudaStre
 cudaError_t launch_forward(const Problem& p, void* ws, const WsLayout& L, void* out, float* lse,
                            int num_sms, cudaStream_t stream);
 
-cudaError_t launch_win_forward(const Problem& p, void* ws, const WsLayout& L, void* out, float* lse, int num_sms,
-                               cudaStream_t stream);
+cudaError_t launch_win_forward(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse,
+                               int num_sms, cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const Problem& p, const void* dout, const void* out, const float* lse,
                                   void* ws, const WsLayout& L, int num_sms, cudaStream_t stream);

@@ -150,11 +150,109 @@ __device__ void for_each_range(const PlanParams& p, int kind, int Lq, int Lk, lo
   if (n > 0) f(start, n, acc);
 }
 
+// The windowed lists.  A window bounds what a unit can cost, so every unit is an item of its own
+// and the units, not the sequences, are dealt out to the threads: a thread finds its unit's
+// sequence in the running sums of the threads' runs of sequences (1024 of them) and walks its run
+// to it.  Long sequences then cost no more time than short ones (long-tail batch of 64 sequences:
+// 31 -> 10 us against emit_list).  Costliest first by the same counting sort, the heads of a unit
+// side by side, so that heads which share keys read them at the same time.
+__device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items, int64_t cap, int* count_out, int* hist,
+                                 int* base) {
+  __shared__ long long run_end[1024];
+  __shared__ int run_q[1024], run_k[1024];  // lengths, when a run is one sequence
+  __shared__ long long units_total, cost_total;
+  __shared__ int cost_max;
+  const int tid = threadIdx.x;
+  const int heads = kind == kListDkv ? p.win.H_kv : p.H;
+  const int run = (p.B + 1023) / 1024;
+  auto len_q = [&](int b) { return int(p.q_off[b + 1] - p.q_off[b]); };
+  auto len_k = [&](int b) { return int(p.kv_off[b + 1] - p.kv_off[b]); };
+  for (int c = tid; c < kCostBuckets; c += blockDim.x) hist[c] = 0;
+  if (tid == 0) cost_max = 0;
+  long long mine = 0;
+  for (int b = tid * run; b < min(p.B, (tid + 1) * run); ++b) {
+    run_q[tid] = len_q(b);
+    run_k[tid] = len_k(b);
+    mine += list_units(p, kind, run_q[tid], run_k[tid]);
+  }
+  run_end[tid] = block_scan_incl(mine, &units_total);
+  __syncthreads();
+  const long long n = units_total;
+  if (n * heads > cap) {  // cannot happen for valid offsets (capacities are upper bounds)
+    if (tid == 0) {
+      atomicCAS(&reinterpret_cast<WsHeader*>(p.ws)->status, 0, int(JFA_ERR_WORKSPACE));
+      *count_out = 0;
+    }
+    return;
+  }
+  // calls f(active, b, unit, cost) for this thread's units, all lanes of a warp together
+  auto for_units = [&](auto&& f) {
+    for (long long i = tid; i - tid < n; i += blockDim.x) {
+      int b = 0, u = 0, cost = 0;
+      if (i < n) {
+        int lo = 0, hi = 1023;  // the first run that ends behind unit i
+        while (lo < hi) {
+          const int mid = (lo + hi) >> 1;
+          if (run_end[mid] > i) hi = mid;
+          else lo = mid + 1;
+        }
+        long long at = lo ? run_end[lo - 1] : 0;
+        int lq = run_q[lo], lk = run_k[lo];
+        b = lo * run;
+        if (run > 1) {
+          for (;; ++b) {
+            lq = len_q(b);
+            lk = len_k(b);
+            const int m = list_units(p, kind, lq, lk);
+            if (at + m > i) break;
+            at += m;
+          }
+        }
+        u = int(i - at);
+        cost = unit_cost(p, kind, u, lq, lk);
+      }
+      f(i < n, b, u, cost);
+    }
+  };
+  // Position of this lane's `heads` entries in its bucket.  Most units cost the same, so lanes of
+  // one bucket share one addition.
+  auto claim = [&](int* counts, bool active, int bkt) -> int {
+    const unsigned same = __match_any_sync(0xffffffffu, active ? bkt : -1);
+    const int lane = tid & 31, first = __ffs(same) - 1;
+    int pos = 0;
+    if (active && lane == first) pos = atomicAdd(&counts[bkt], heads * __popc(same));
+    return __shfl_sync(0xffffffffu, pos, first) + heads * __popc(same & ((1u << lane) - 1u));
+  };
+  auto bucket = [](int cost) { return cost < kCostBuckets - 1 ? cost : kCostBuckets - 1; };
+  long long sum = 0;
+  int mx = 0;
+  for_units([&](bool active, int, int, int cost) {
+    claim(hist, active, bucket(cost));
+    sum += cost;
+    mx = max(mx, cost);
+  });
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((tid & 31) == 0) atomicMax(&cost_max, mx);
+  block_scan_incl(sum, &cost_total);
+  const int total = scan_desc(hist, base);
+  for_units([&](bool active, int b, int u, int cost) {
+    const int pos = claim(base, active, bucket(cost));
+    if (active)
+      for (int h = 0; h < heads; ++h) items[pos + h] = WorkItem{b, h, u, u + 1};
+  });
+  if (tid == 0) {
+    *count_out = total;
+    reinterpret_cast<WsHeader*>(p.ws)->wait_ns[kind] =
+        wait_limit_ns(cost_total * heads, p.grid, cost_max);
+  }
+}
+
 __device__ void emit_list(const PlanParams& p, int kind, WorkItem* items, int64_t cap, int* count_out,
                           int* hist, int* base) {
+  if (p.win.window > 0) return emit_window_list(p, kind, items, cap, count_out, hist, base);
   __shared__ long long total_cost;
   const int tid = threadIdx.x;
-  const int heads = p.win.window > 0 && kind == kListDkv ? p.win.H_kv : p.H;
+  const int heads = p.H;
   // total work, to cap range cost at about 1/kItemsPerCta of a CTA's share
   long long local = 0;
   for (int b = tid; b < p.B; b += blockDim.x) {
@@ -311,48 +409,47 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
     //      pointed at that tile's first row and clipped to the tile's rows.  (With invalid
     //      offsets CTA 0 leaves every list empty, so no map is used; a tail map is only
     //      written for a sequence inside its tensor, which keeps its index in range.)
-    CUtensorMap* out_maps = reinterpret_cast<CUtensorMap*>(p.ws + p.L.maps);
-    auto write_map = [&](CUtensorMap* set, const CUtensorMap& tmpl, int b, int slot, int64_t row0, int64_t len) {
-      const size_t rb = maps.row_bytes[slot];
-      const int rows = maps.tile_rows[slot];
-      const uint4* src = reinterpret_cast<const uint4*>(&tmpl);
-      CUtensorMap* dst = set + size_t(b) * kNumMapSlots + slot;
-      uint4* d4 = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d4[i] = src[i];
-      tmap_replace_address(dst, static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb));
-      tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
-      const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
-      if (len <= 0 || row0 < 0 || row0 + len > total) return;
-      const int64_t g0 = row0 + (len - 1) / rows * rows;  // first row of the sequence's last tile
-      if (g0 + rows > total) {
-        const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
-        CUtensorMap* tdst = set + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total);
-        uint4* t4 = reinterpret_cast<uint4*>(tdst);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t4[i] = src[i];
-        tmap_replace_address(
-            tdst, p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(g0 - (total - n)) * rb);
-        tmap_replace_dim1(tdst, uint32_t(row0 + len - g0));
-      }
-    };
-    for (size_t idx = gt; idx < size_t(p.B) * kNumMapSlots; idx += gstride) {
+    //      One thread per map: a replace in global memory takes about a microsecond, so a thread
+    //      that wrote several in turn would be what the planner waits for.
+    const int sets = p.win.window > 0 && p.win.sinks > 0 ? 2 : 1;  // maps, and the sinks' maps
+    for (size_t job = gt; job < size_t(p.B) * kNumMapSlots * 2 * sets; job += gstride) {
+      const bool tail = job & 1, sink = sets == 2 && ((job >> 1) & 1);
+      const size_t idx = job / (2 * sets);
       const int b = int(idx / kNumMapSlots), slot = int(idx % kNumMapSlots);
       if (!maps.used[slot]) continue;
       const bool is_q_side = (slot == kMapQ || slot == kMapDO);
       int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
       int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
-      if (p.win.window > 0 && !is_q_side) {
-        // the window part, and the sinks' own map (with malformed lengths neither is used)
+      if (is_q_side && sink) continue;
+      if (p.win.window > 0 && !is_q_side) {  // the sinks, or the window part
         const int64_t lq = p.q_off[b + 1] - p.q_off[b];
         if (lq < 0 || len < 0 || lq > (int64_t(1) << 30) || len > (int64_t(1) << 30)) continue;
         const WinSeq ws = win_seq(int(lq), int(len), p.win.window, p.win.sinks);
-        if (p.win.sinks > 0)
-          write_map(reinterpret_cast<CUtensorMap*>(p.ws + p.L.smaps), maps.sink_tmpl[slot - kMapK], b, slot, row0, ws.ns);
-        row0 += ws.org;
-        len = ws.Lk;
+        if (!sink) row0 += ws.org;
+        len = sink ? ws.ns : ws.Lk;
       }
-      write_map(out_maps, maps.tmpl[slot], b, slot, row0, len);
+      const size_t rb = maps.row_bytes[slot];
+      const int rows = maps.tile_rows[slot];
+      const int64_t total = is_q_side ? p.total_q : p.total_kv;
+      CUtensorMap* dst = reinterpret_cast<CUtensorMap*>(p.ws + (sink ? p.L.smaps : p.L.maps));
+      const void* base;
+      if (!tail) {
+        dst += idx;
+        base = static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb);
+      } else {
+        if (len <= 0 || row0 < 0 || row0 + len > total) continue;
+        const int64_t g0 = row0 + (len - 1) / rows * rows;  // first row of the sequence's last tile
+        if (g0 + rows <= total) continue;
+        const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
+        dst += size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total);
+        base = p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(g0 - (total - n)) * rb;
+        len = row0 + len - g0;
+      }
+      const uint4* src = reinterpret_cast<const uint4*>(sink ? &maps.sink_tmpl[slot - kMapK] : &maps.tmpl[slot]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
+      tmap_replace_address(dst, base);
+      tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
     }
     tmap_release();
     return;
@@ -447,8 +544,9 @@ cudaError_t launch_plan(const Problem& pr, const PlanMaps& maps, void* ws, const
   p.nb = pr.num_buckets;
   p.win = pr.win;
   // one CTA per list; helpers for the maps (one thread each), tail copies and bias table
-  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots + 1023) / 1024;
-  const int helpers = int(map_ctas < 1 ? 1 : (map_ctas > 32 ? 32 : map_ctas)) + 4;
+  const int sets = pr.win.window > 0 && pr.win.sinks > 0 ? 2 : 1;
+  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots * 2 * sets + 1023) / 1024;
+  const int helpers = int(map_ctas < 1 ? 1 : (map_ctas > 32 ? 32 : map_ctas)) + 24;
   return launch_pdl(plan_kernel, dim3((!backward ? 1 : pr.win.window > 0 ? 2 : 4) + helpers), dim3(1024), 0, stream, maps, p);
 }
 

@@ -47,6 +47,7 @@ struct WinFwdParams {
   int64_t total_q, total_kv;
   float scale_log2;  // scale * log2(e), > 0
   WindowSpec win;
+  bool whole;                // the tensors' own maps serve whole tiles (row numbers fit 31 bits)
   const CUtensorMap* maps;   // [B][kNumMapSlots]: Q, and K / V of the window part
   const CUtensorMap* smaps;  // K / V of the sinks
   int sink_box;              // rows of their boxes (16 .. 64)
@@ -114,7 +115,9 @@ __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
 __device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
 
 template <int D>
-__global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdParams p) {
+__global__ void __launch_bounds__(kWinThreads, 2)
+    win_fwd_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                   const __grid_constant__ CUtensorMap v_map, const __grid_constant__ WinFwdParams p) {
   using C = WinCfg<D>;
   constexpr int R = C::kStages;
   extern __shared__ uint8_t smem_raw[];
@@ -163,15 +166,12 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
     if (lane == 0) {
       uint32_t ring_n = 0, tn = 0;
       bool ok = true;
-      int acq_b = -1;  // sequence whose maps this thread has acquired
-      auto acquire = [&](int b, bool prefetch) {
-        if (b == acq_b) return;
-        int same = -1;
-        acquire_seq_maps(p.maps, b, kMapK, kMapV, same, prefetch);
-        same = -1;
-        if (p.win.sinks > 0) acquire_seq_maps(p.smaps, b, kMapK, kMapV, same, prefetch);
-        acq_b = b;
-      };
+      if (p.whole) {
+        tmap_prefetch(&k_map);
+        tmap_prefetch(&v_map);
+      }
+      const CUtensorMap* const whole_k = p.whole ? &k_map : nullptr;
+      const CUtensorMap* const whole_v = p.whole ? &v_map : nullptr;
       for (uint32_t k = 0; ok; ++k) {
         if (!meta_wait(meta, k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
@@ -181,11 +181,12 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
         for (int t = wi.u0; t < wi.u1 && ok; ++t) {
           const TileSteps st = tile_steps(wi, t, p.win.window);
           if (st.n == 0) continue;
-          acquire(wi.b, false);
           auto fill = [&](int slot, int j) {
             const bool sink = j < st.nz;
-            const TileMap m = sink ? tile_map(p.smaps, p.B, slot, wi.b, wi.ko - ws.org, j, p.total_kv, kWinKeys)
-                                   : tile_map(p.maps, p.B, slot, wi.b, wi.ko, st.a + j - st.nz, p.total_kv, kWinKeys);
+            const TileMap m =
+                sink ? tile_map(nullptr, p.smaps, p.B, slot, wi.b, wi.ko - ws.org, j, ws.ns, p.total_kv, kWinKeys)
+                     : tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, wi.b, wi.ko, st.a + j - st.nz, wi.Lk,
+                                p.total_kv, kWinKeys);
             const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
             if (m.tail) tmap_acquire(m.map);
             if (!mbar_wait(&kv_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
@@ -203,10 +204,7 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
             if (ok && j + C::kBufs < st.n) ok = fill(kMapK, j + C::kBufs);
           }
         }
-        if (ok) {
-          if (const ItemMeta* wn = meta_peek_next(meta, k)) acquire(wn->b, true);
-          meta_release(meta, k);
-        }
+        if (ok) meta_release(meta, k);
       }
       if (!ok) raise_status(p.status, JFA_ERR_TIMEOUT);
       // every copy this thread started has landed before the CTA can exit
@@ -295,18 +293,14 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
     if (lane == 0) {
       uint32_t item_n = 0, tn = 0;
       bool ok = true;
-      int acq_b = -1;
+      if (p.whole) tmap_prefetch(&q_map);
       for (uint32_t k = 0; ok; ++k) {
         if (!meta_wait(meta, k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[k % kMetaSlots];
         if (wi.b < 0) break;
         for (int t = wi.u0; t < wi.u1 && ok; ++t) {
           if (tile_steps(wi, t, p.win.window).n == 0) continue;
-          const TileMap m = tile_map(p.maps, p.B, kMapQ, wi.b, wi.qo, t, p.total_q);
-          if (wi.b != acq_b) {
-            tmap_acquire(p.maps + size_t(wi.b) * kNumMapSlots + kMapQ);
-            acq_b = wi.b;
-          }
+          const TileMap m = tile_map(p.whole ? &q_map : nullptr, p.maps, p.B, kMapQ, wi.b, wi.qo, t, wi.Lq, p.total_q);
           if (m.tail) tmap_acquire(m.map);
           if (!mbar_wait(&q_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
@@ -316,20 +310,12 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
           ++item_n;
           // pull the next query tile into L2 meanwhile: the next of this range, else the first
           // of this CTA's next item
-          int nb = -1, nh = 0, nt = 0;
-          if (t + 1 < wi.u1) {
-            nb = wi.b, nh = wi.h, nt = t + 1;
-          } else if (const ItemMeta* wn = meta_peek_next(meta, k)) {
-            nb = wn->b, nh = wn->h, nt = wn->u0;
-          }
-          if (nb >= 0) {
-            if (nb != acq_b) {
-              const CUtensorMap* nm = p.maps + size_t(nb) * kNumMapSlots + kMapQ;
-              tmap_acquire(nm);
-              tmap_prefetch(nm);
-              acq_b = nb;
-            }
-            prefetch_tile<C::kBoxes>(p.maps, p.B, kMapQ, nb, p.q_off[nb], nt, p.total_q, nh * D);
+          const ItemMeta* nx = t + 1 < wi.u1 ? &wi : meta_peek_next(meta, k);
+          if (nx && p.whole) {
+            const int nt = t + 1 < wi.u1 ? t + 1 : nx->u0;
+            if ((nt + 1) * kBM <= nx->Lq)
+              for (int c = 0; c < C::kBoxes; ++c)
+                tma_prefetch_2d(&q_map, nx->h * D + c * 64, int(nx->qo) + nt * kBM);
           }
         }
         if (ok) meta_release(meta, k);
@@ -511,16 +497,17 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_fwd_kernel(const WinFwdPar
 }
 
 template <int D>
-cudaError_t launch_win_fwd_t(const WinFwdParams& fp, int grid, cudaStream_t stream) {
+cudaError_t launch_win_fwd_t(const PlanMaps& maps, const WinFwdParams& fp, int grid, cudaStream_t stream) {
   auto kern = win_fwd_kernel<D>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, WinCfg<D>::kSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kWinThreads), WinCfg<D>::kSmemBytes, stream, fp);
+  return launch_pdl(kern, dim3(grid), dim3(kWinThreads), WinCfg<D>::kSmemBytes, stream, maps.tmpl[kMapQ], maps.tmpl[kMapK],
+                    maps.tmpl[kMapV], fp);
 }
 
 }  // namespace
 
-cudaError_t launch_win_forward(const Problem& pr, void* ws, const WsLayout& L, void* out, float* lse, int num_sms,
+cudaError_t launch_win_forward(const Problem& pr, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse, int num_sms,
                                cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   WinFwdParams fp;
@@ -533,6 +520,7 @@ cudaError_t launch_win_forward(const Problem& pr, void* ws, const WsLayout& L, v
   fp.total_kv = pr.total_kv;
   fp.scale_log2 = pr.scale * kLog2e;
   fp.win = pr.win;
+  fp.whole = pr.total_q < (int64_t(1) << 31) && pr.total_kv < (int64_t(1) << 31);
   fp.maps = reinterpret_cast<const CUtensorMap*>(w + L.maps);
   fp.smaps = reinterpret_cast<const CUtensorMap*>(w + L.smaps);
   fp.sink_box = win_sink_box(pr.win.sinks);
@@ -545,7 +533,7 @@ cudaError_t launch_win_forward(const Problem& pr, void* ws, const WsLayout& L, v
   fp.lse = lse;
   fp.trace = pr.trace[JFA_KERNEL_FORWARD];
   const int grid = kWinCtasPerSm * num_sms;
-  return pr.d == 128 ? launch_win_fwd_t<128>(fp, grid, stream) : launch_win_fwd_t<64>(fp, grid, stream);
+  return pr.d == 128 ? launch_win_fwd_t<128>(maps, fp, grid, stream) : launch_win_fwd_t<64>(maps, fp, grid, stream);
 }
 
 }  // namespace jfa
