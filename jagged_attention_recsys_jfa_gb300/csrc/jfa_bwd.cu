@@ -115,6 +115,7 @@ struct PreParams {
   int64_t total_q;
   const WorkItem* items;      // dQ list: units are query tiles
   const int* n_items;
+  bool all_heads;             // its entries stand for all heads (window)
   const WorkItem* items2;     // fused list: the sequence's one query tile
   const int* n_items2;
   const WorkItem* items3;     // non-sequence-parallel list: all of the sequence's query tiles
@@ -137,7 +138,9 @@ __global__ void __launch_bounds__(256) preprocess_items_kernel(const PreParams p
   const int n1 = *p.n_items, n2 = *p.n_items2, n3 = *p.n_items3;
   for (int idx = blockIdx.x; idx < n1 + n2 + n3; idx += gridDim.x) {
     const bool whole = idx >= n1;  // fused or non-sequence-parallel: every query tile of the sequence
-    const WorkItem it = idx < n1 ? p.items[idx] : idx < n1 + n2 ? p.items2[idx - n1] : p.items3[idx - n1 - n2];
+    WorkItem it = idx < n1 ? p.items[p.all_heads ? idx / p.H : idx]
+                           : idx < n1 + n2 ? p.items2[idx - n1] : p.items3[idx - n1 - n2];
+    if (p.all_heads) it.h = idx % p.H;
     const int64_t qo = p.q_off[it.b];
     const int Lq = int(p.q_off[it.b + 1] - qo);
     const int64_t pad0 = int64_t(it.h) * p.qpad_cap + p.qpad[it.b];
@@ -783,7 +786,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
-                                         p.win.window, p.win.sinks))
+                                         p.win.window, p.win.sinks, p.win.H_kv))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -1310,7 +1313,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
     if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
-                                         p.win.window, p.win.sinks))
+                                         p.win.window, p.win.sinks, p.H))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -2689,6 +2692,7 @@ cudaError_t launch_bwd_preprocess(const Problem& pr, const void* dout, const voi
   pp.total_q = pr.total_q;
   pp.items = reinterpret_cast<const WorkItem*>(w + L.dq);
   pp.n_items = &reinterpret_cast<const WsHeader*>(w)->n_dq;
+  pp.all_heads = pr.win.window > 0;
   pp.items2 = reinterpret_cast<const WorkItem*>(w + L.fused);
   pp.n_items2 = &reinterpret_cast<const WsHeader*>(w)->n_fused;
   pp.items3 = reinterpret_cast<const WorkItem*>(w + L.nsp);

@@ -154,8 +154,10 @@ __device__ void for_each_range(const PlanParams& p, int kind, int Lq, int Lk, lo
 // and the units, not the sequences, are dealt out to the threads: a thread finds its unit's
 // sequence in the running sums of the threads' runs of sequences (1024 of them) and walks its run
 // to it.  Long sequences then cost no more time than short ones (long-tail batch of 64 sequences:
-// 31 -> 10 us against emit_list).  Costliest first by the same counting sort, the heads of a unit
-// side by side, so that heads which share keys read them at the same time.
+// 31 -> 10 us against emit_list).  Costliest first by the same counting sort.  One entry stands
+// for a unit of all `heads` heads: item i of the launch is entry i / heads, head i % heads, so that
+// heads which share keys read them at the same time (and the list is written in a tenth of the time
+// that one entry per head took).
 __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items, int64_t cap, int* count_out, int* hist,
                                  int* base) {
   __shared__ long long run_end[1024];
@@ -214,14 +216,14 @@ __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items,
       f(i < n, b, u, cost);
     }
   };
-  // Position of this lane's `heads` entries in its bucket.  Most units cost the same, so lanes of
+  // Position of this lane's entry in its bucket.  Most units cost the same, so lanes of
   // one bucket share one addition.
   auto claim = [&](int* counts, bool active, int bkt) -> int {
     const unsigned same = __match_any_sync(0xffffffffu, active ? bkt : -1);
     const int lane = tid & 31, first = __ffs(same) - 1;
     int pos = 0;
-    if (active && lane == first) pos = atomicAdd(&counts[bkt], heads * __popc(same));
-    return __shfl_sync(0xffffffffu, pos, first) + heads * __popc(same & ((1u << lane) - 1u));
+    if (active && lane == first) pos = atomicAdd(&counts[bkt], __popc(same));
+    return __shfl_sync(0xffffffffu, pos, first) + __popc(same & ((1u << lane) - 1u));
   };
   auto bucket = [](int cost) { return cost < kCostBuckets - 1 ? cost : kCostBuckets - 1; };
   long long sum = 0;
@@ -237,11 +239,10 @@ __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items,
   const int total = scan_desc(hist, base);
   for_units([&](bool active, int b, int u, int cost) {
     const int pos = claim(base, active, bucket(cost));
-    if (active)
-      for (int h = 0; h < heads; ++h) items[pos + h] = WorkItem{b, h, u, u + 1};
+    if (active) *reinterpret_cast<int4*>(items + pos) = make_int4(b, 0, u, u + 1);
   });
   if (tid == 0) {
-    *count_out = total;
+    *count_out = total * heads;
     reinterpret_cast<WsHeader*>(p.ws)->wait_ns[kind] =
         wait_limit_ns(cost_total * heads, p.grid, cost_max);
   }
@@ -409,10 +410,11 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
     //      pointed at that tile's first row and clipped to the tile's rows.  (With invalid
     //      offsets CTA 0 leaves every list empty, so no map is used; a tail map is only
     //      written for a sequence inside its tensor, which keeps its index in range.)
-    //      One thread per map: a replace in global memory takes about a microsecond, so a thread
-    //      that wrote several in turn would be what the planner waits for.
+    //      One warp per map: the replaces of a warp's lanes are done one after another, so lanes
+    //      that each wrote a map would be what the planner waits for.
     const int sets = p.win.window > 0 && p.win.sinks > 0 ? 2 : 1;  // maps, and the sinks' maps
-    for (size_t job = gt; job < size_t(p.B) * kNumMapSlots * 2 * sets; job += gstride) {
+    const int lane = tid & 31;
+    for (size_t job = gt / 32; job < size_t(p.B) * kNumMapSlots * 2 * sets; job += gstride / 32) {
       const bool tail = job & 1, sink = sets == 2 && ((job >> 1) & 1);
       const size_t idx = job / (2 * sets);
       const int b = int(idx / kNumMapSlots), slot = int(idx % kNumMapSlots);
@@ -446,10 +448,12 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
         len = row0 + len - g0;
       }
       const uint4* src = reinterpret_cast<const uint4*>(sink ? &maps.sink_tmpl[slot - kMapK] : &maps.tmpl[slot]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) reinterpret_cast<uint4*>(dst)[i] = src[i];
-      tmap_replace_address(dst, base);
-      tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
+      if (lane < 8) reinterpret_cast<uint4*>(dst)[lane] = src[lane];
+      __syncwarp();
+      if (lane == 0) {
+        tmap_replace_address(dst, base);
+        tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
+      }
     }
     tmap_release();
     return;
@@ -543,10 +547,10 @@ cudaError_t launch_plan(const Problem& pr, const PlanMaps& maps, void* ws, const
   p.jb_plane = pr.jb_plane;
   p.nb = pr.num_buckets;
   p.win = pr.win;
-  // one CTA per list; helpers for the maps (one thread each), tail copies and bias table
+  // one CTA per list; helpers for the maps (one warp each), tail copies and bias table
   const int sets = pr.win.window > 0 && pr.win.sinks > 0 ? 2 : 1;
-  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots * 2 * sets + 1023) / 1024;
-  const int helpers = int(map_ctas < 1 ? 1 : (map_ctas > 32 ? 32 : map_ctas)) + 24;
+  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots * 2 * sets + 31) / 32;
+  const int helpers = int(map_ctas < 8 ? 8 : map_ctas > 120 ? 120 : map_ctas);
   return launch_pdl(plan_kernel, dim3((!backward ? 1 : pr.win.window > 0 ? 2 : 4) + helpers), dim3(1024), 0, stream, maps, p);
 }
 

@@ -55,7 +55,7 @@ template <bool kWin = false>
 __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items, int n_items, int* claim,
                                              const int64_t* q_off, const int64_t* kv_off, const int64_t* qpad,
                                              const int64_t* jb_off, volatile int* abort, int window = 0,
-                                             int sinks = 0) {
+                                             int sinks = 0, int heads = 1) {
   for (uint32_t k = 0;; ++k) {
     if (k >= 2) {
       const uint32_t kp = k - 2;
@@ -64,9 +64,9 @@ __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items,
     const int idx = atomicAdd(claim, 1);
     ItemMeta m;
     if (idx < n_items) {
-      const WorkItem wi = items[idx];
+      const WorkItem wi = items[kWin ? idx / heads : idx];  // windowed lists: one entry for all heads
       m.b = wi.b;
-      m.h = wi.h;
+      m.h = kWin ? idx % heads : wi.h;
       m.u0 = wi.u0;
       m.u1 = wi.u1;
       m.qo = q_off[wi.b];

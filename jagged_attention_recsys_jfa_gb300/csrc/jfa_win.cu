@@ -14,15 +14,16 @@
 // query tile against 3.3 of 128).  Masks are applied only in steps that the edge of some row's
 // window crosses, and a warp whose 32 rows see none of a step's keys skips its arithmetic.
 //
-//   warps 0-3  softmax: one TMEM lane = one query row per thread
-//   warp 4     K/V producer (TMA into a ring of 64-key tiles)
-//   warp 5     MMA issuer: the first scores, then for each step PV(j), S(j + kBufs)
-//   warp 6     query tile loader
-//   warp 7     scheduler (claims items, publishes their metadata)
+//   warp 0     K/V producer (TMA into two rings of 64-key tiles)
+//   warp 1     issues the products PV(j)
+//   warp 2     loads the query tile and issues the scores S(j), up to kBufs steps ahead
+//   warp 3     scheduler (claims items, publishes their metadata)
+//   warps 4-7  softmax: one TMEM lane = one query row per thread
 // TMEM (256 of the 512 columns): O [0, d), then kBufs score buffers of 64 columns (P, bf16,
 // overwrites the first 32 of its buffer).  With the next steps' scores computed ahead, the chain
 // of a step is its softmax alone; the products' latency (about 1300 cycles per step otherwise) is
-// off it.
+// off it.  Scores and products have an issuing warp each: a short step's MMAs take less time than
+// the waits and commits around them take one warp (one issuer for both: forward_kernel_times).
 #include <cuda_bf16.h>
 
 #include "jfa_internal.h"
@@ -34,7 +35,11 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+// The reference maximum is raised, and O rescaled, only when a row outgrows it by this much (log2
+// units): until then P is at most 2^16, which bf16 and the fp32 sums hold with the same relative
+// precision.  A rescale stalls its CTA for about 2000 cycles; at 2^8 a tile whose first step is a
+// few sinks met one now and then.
+constexpr float kRescaleThreshold = 16.0f;
 constexpr int kWinThreads = 256;
 constexpr int kSoftmaxWarps = 4;
 constexpr int kWinConsumers = 3 + kSoftmaxWarps;  // of a metadata entry
@@ -67,35 +72,94 @@ struct WinCfg {
   static constexpr int kTileBytes = kWinKeys * D * 2;
   static constexpr int kBoxes = D / 64;
   static constexpr int kBoxBytes = kWinKeys * 128;  // one 64-column box of a K or V tile
-  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kStages = D == 128 ? 2 : 4;  // tiles of the K ring, and of the V ring
   static constexpr int kBufs = D == 128 ? 2 : 3;    // score buffers
-  static constexpr int kSmemBytes = kQBytes + kStages * kTileBytes + 1024;
+  static constexpr int kSmemBytes = kQBytes + 2 * kStages * kTileBytes + 1024;
   static constexpr uint32_t kColO = 0, kColS = D;
   static_assert(kColS + kBufs * kWinKeys <= kWinTmemCols, "TMEM columns");
+  // v_empty of step j is what S(j + kBufs) waits for: it must not have gone round again by then
+  static_assert(kStages >= kBufs, "V ring");
   static_assert(2 * (kSmemBytes + 2048) <= 233472, "two CTAs per SM");
 };
 
-// A query tile's steps: nz of sinks, then the window part's 64-key tiles from a on; n in all.
-struct TileSteps {
+// What the roles need to know of an item, a query tile, worked out once by the scheduler: its
+// steps are nz of sinks, then the window part's 64-key tiles from a on, n in all.
+struct WinTile {
+  int b, h, t;          // sequence (-1: no more items), query head, query tile
   int nz, a, n;
+  int rows;             // rows of the tile that are queries
+  int pos;              // position of its first row, counted from the window part's first key
+  int Lq, Lk, org, ns;  // as in ItemMeta and WinSeq
+  int64_t qo, ko;       // first query row of the sequence, first key row of its window part
 };
-__device__ __forceinline__ TileSteps tile_steps(const ItemMeta& m, int t, int window) {
-  const WinSeq ws = meta_win(m);
-  TileSteps r;
-  int e;
-  win_kv_tiles(t, m.Lq, m.Lk, window, &r.a, &e, kWinKeys);
-  r.nz = win_sees_sinks(t, m.Lq, ws) ? (ws.ns + kWinKeys - 1) / kWinKeys : 0;
-  r.n = r.nz + e - r.a;
-  return r;
+struct TileRing {
+  WinTile e[kMetaSlots];
+  uint64_t full[kMetaSlots], empty[kMetaSlots];
+  const uint64_t* wait_ns;  // the planner's hand-off limit for this launch
+};
+// The scheduler (one thread): claims item k once item k - 2 is released by every role, so the
+// CTA never holds more than one item that it has not started; an end marker closes the ring.
+__device__ __forceinline__ bool publish_tiles(TileRing& r, const WinFwdParams& p, volatile int* abort) {
+  const int n_items = *p.n_items;
+  for (uint32_t k = 0;; ++k) {
+    if (k >= 2) {
+      const uint32_t kp = k - 2;
+      if (!mbar_wait(&r.empty[kp % kMetaSlots], (kp / kMetaSlots) & 1, abort, r.wait_ns, kWaitTimeoutNs)) return false;
+    }
+    const int idx = atomicAdd(p.claim, 1);
+    WinTile w = {};
+    w.b = -1;
+    if (idx < n_items) {
+      const WorkItem wi = p.items[idx / p.H];  // one entry for all heads
+      w.b = wi.b;
+      w.h = idx % p.H;
+      w.t = wi.u0;
+      w.qo = p.q_off[wi.b];
+      w.ko = p.kv_off[wi.b];
+      w.Lq = int(p.q_off[wi.b + 1] - w.qo);
+      const WinSeq ws = win_seq(w.Lq, int(p.kv_off[wi.b + 1] - w.ko), p.win.window, p.win.sinks);
+      w.ko += ws.org;
+      w.Lk = ws.Lk;
+      w.org = ws.org;
+      w.ns = ws.ns;
+      int e;
+      win_kv_tiles(w.t, w.Lq, w.Lk, p.win.window, &w.a, &e, kWinKeys);
+      w.nz = win_sees_sinks(w.t, w.Lq, ws) ? (ws.ns + kWinKeys - 1) / kWinKeys : 0;
+      w.n = w.nz + e - w.a;
+      w.rows = min(kBM, w.Lq - w.t * kBM);
+      w.pos = w.t * kBM + w.Lk - w.Lq;
+    }
+    r.e[k % kMetaSlots] = w;
+    mbar_arrive(&r.full[k % kMetaSlots]);  // release: the entry is visible to every thread that waits on it
+    if (w.b < 0) {
+      grid_launch_dependents();  // nothing left to claim: the next kernel may take freed SMs
+      return true;
+    }
+  }
 }
-// Order of a tile's loads, which is the order the products need them in: the scores run kBufs
-// steps ahead, so K0 .. K(kBufs-1), then V0, K(kBufs), V1, ..
-template <int kBufs>
-__device__ __forceinline__ uint32_t k_pos(int j) { return j < kBufs ? j : 2 * j - kBufs + 1; }
-template <int kBufs>
-__device__ __forceinline__ uint32_t v_pos(int j, int n) {
-  return min(j + kBufs, n) + j;  // the V tiles before it, and the K tiles of steps < j + kBufs
+// Entry k, read in place until it is released; all lanes of a warp together (see meta_wait_warp).
+__device__ __forceinline__ bool tile_wait(TileRing& r, uint32_t k, volatile int* abort) {
+  return mbar_wait(&r.full[k % kMetaSlots], (k / kMetaSlots) & 1, abort, r.wait_ns, kWaitTimeoutNs);
 }
+__device__ __forceinline__ bool tile_wait_warp(TileRing& r, uint32_t k, volatile int* abort) {
+  return __all_sync(0xffffffffu, tile_wait(r, k, abort));
+}
+__device__ __forceinline__ void tile_release_warp(TileRing& r, uint32_t k) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&r.empty[k % kMetaSlots]);
+}
+
+// A ring position: entry and the parity of its current round.
+template <int N>
+struct Ring {
+  uint32_t e = 0, ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++e == N) {
+      e = 0;
+      ph ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ void raise_status(int* status, int code) { atomicCAS(status, 0, code); }
 
@@ -123,13 +187,14 @@ __global__ void __launch_bounds__(kWinThreads, 2)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sQ = smem;
-  uint8_t* sRing = smem + C::kQBytes;
+  uint8_t* sK = smem + C::kQBytes;
+  uint8_t* sV = sK + R * C::kTileBytes;
 
-  __shared__ uint64_t q_full, q_empty, o_full, mma_done;
-  __shared__ uint64_t kv_full[R], kv_empty[R], s_full[C::kBufs], p_full[C::kBufs];
+  __shared__ uint64_t q_full, q_empty, o_full, pv_done, s_done;
+  __shared__ uint64_t k_full[R], k_empty[R], v_full[R], v_empty[R], s_full[C::kBufs], p_full[C::kBufs];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
-  __shared__ MetaRing meta;
+  __shared__ TileRing tiles;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -137,19 +202,26 @@ __global__ void __launch_bounds__(kWinThreads, 2)
     mbar_init(&q_full, 1);
     mbar_init(&q_empty, 1);
     mbar_init(&o_full, 1);
-    mbar_init(&mma_done, 1);
+    mbar_init(&pv_done, 1);
+    mbar_init(&s_done, 1);
     for (int i = 0; i < R; ++i) {
-      mbar_init(&kv_full[i], 1);
-      mbar_init(&kv_empty[i], 1);
+      mbar_init(&k_full[i], 1);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_full[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int i = 0; i < C::kBufs; ++i) {
       mbar_init(&s_full[i], 1);
       mbar_init(&p_full[i], 32 * kSoftmaxWarps);
     }
-    meta_init(meta, p.wait_ns, kWinConsumers);
+    for (int i = 0; i < kMetaSlots; ++i) {
+      mbar_init(&tiles.full[i], 1);
+      mbar_init(&tiles.empty[i], kWinConsumers);
+    }
+    tiles.wait_ns = p.wait_ns;
     fence_mbar_init();
   }
-  if (warp == 5) {
+  if (warp == 1) {
     tmem_alloc(&tmem_base_sh, kWinTmemCols);
     tmem_relinquish();
   }
@@ -160,11 +232,12 @@ __global__ void __launch_bounds__(kWinThreads, 2)
   const uint32_t tmem = tmem_base_sh;
   volatile int* abort_flag = &abort_sh;
 
-  if (warp >= kSoftmaxWarps) {
-   if (warp == 4) {
+  if (warp < kFirstComputeWarp) {
+   if (warp == 0) {
     // ------------------------------------------------------------ K/V producer
     if (lane == 0) {
-      uint32_t ring_n = 0, tn = 0;
+      Ring<R> kr, vr;
+      uint32_t n_k = 0, n_v = 0, tn = 0;  // tiles loaded
       bool ok = true;
       if (p.whole) {
         tmap_prefetch(&k_map);
@@ -173,319 +246,303 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       const CUtensorMap* const whole_k = p.whole ? &k_map : nullptr;
       const CUtensorMap* const whole_v = p.whole ? &v_map : nullptr;
       for (uint32_t k = 0; ok; ++k) {
-        if (!meta_wait(meta, k, abort_flag)) { ok = false; break; }
-        const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
-        if (wi.b < 0) break;  // end of this CTA's items
-        const WinSeq ws = meta_win(wi);
-        const int col = wi.h / p.group * D;  // first column of the key/value head
-        for (int t = wi.u0; t < wi.u1 && ok; ++t) {
-          const TileSteps st = tile_steps(wi, t, p.win.window);
-          if (st.n == 0) continue;
-          auto fill = [&](int slot, int j) {
-            const bool sink = j < st.nz;
-            const TileMap m =
-                sink ? tile_map(nullptr, p.smaps, p.B, slot, wi.b, wi.ko - ws.org, j, ws.ns, p.total_kv, kWinKeys)
-                     : tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, wi.b, wi.ko, st.a + j - st.nz, wi.Lk,
-                                p.total_kv, kWinKeys);
-            const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
-            if (m.tail) tmap_acquire(m.map);
-            if (!mbar_wait(&kv_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
-            trace_event(p.trace, kTraceProducer, tn, 2);
-            mbar_arrive_expect_tx(&kv_full[e], uint32_t(sink ? p.sink_box : kWinKeys) * D * 2);
+        if (!tile_wait(tiles, k, abort_flag)) { ok = false; break; }
+        const WinTile& w = tiles.e[k % kMetaSlots];
+        if (w.b < 0) break;  // end of this CTA's items
+        const int col = w.h / p.group * D;  // first column of the key/value head
+        auto fill = [&](int slot, int j, Ring<R>& r, uint64_t* full, uint64_t* empty, uint8_t* smem_tiles) {
+          const bool sink = j < w.nz;
+          const TileMap m =
+              sink ? tile_map(nullptr, p.smaps, p.B, slot, w.b, w.ko - w.org, j, w.ns, p.total_kv, kWinKeys)
+                   : tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, w.b, w.ko, w.a + j - w.nz, w.Lk,
+                              p.total_kv, kWinKeys);
+          if (m.tail) tmap_acquire(m.map);
+          if (!mbar_wait(&empty[r.e], r.ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
+          trace_event(p.trace, kTraceProducer, tn, slot);
+          mbar_arrive_expect_tx(&full[r.e], uint32_t(sink ? p.sink_box : kWinKeys) * D * 2);
 #pragma unroll
-            for (int c = 0; c < C::kBoxes; ++c)
-              tma_load_2d(sRing + e * C::kTileBytes + c * C::kBoxBytes, m.map, &kv_full[e], col + c * 64, m.y);
-            ++ring_n;
-            return true;
-          };
-          for (int j = 0; j < min(C::kBufs, st.n) && ok; ++j) ok = fill(kMapK, j);
-          for (int j = 0; j < st.n && ok; ++j) {
-            ok = fill(kMapV, j);
-            if (ok && j + C::kBufs < st.n) ok = fill(kMapK, j + C::kBufs);
-          }
+          for (int c = 0; c < C::kBoxes; ++c)
+            tma_load_2d(smem_tiles + r.e * C::kTileBytes + c * C::kBoxBytes, m.map, &full[r.e], col + c * 64, m.y);
+          r.next();
+          return true;
+        };
+        auto fill_k = [&](int j) { return ++n_k, fill(kMapK, j, kr, k_full, k_empty, sK); };
+        auto fill_v = [&](int j) { return ++n_v, fill(kMapV, j, vr, v_full, v_empty, sV); };
+        for (int j = 0; j < min(C::kBufs, w.n) && ok; ++j) ok = fill_k(j);
+        for (int j = 0; j < w.n && ok; ++j) {
+          ok = fill_v(j);
+          if (ok && j + C::kBufs < w.n) ok = fill_k(j + C::kBufs);
         }
-        if (ok) meta_release(meta, k);
+        if (ok) mbar_arrive(&tiles.empty[k % kMetaSlots]);
       }
       if (!ok) raise_status(p.status, JFA_ERR_TIMEOUT);
       // every copy this thread started has landed before the CTA can exit
-      const uint32_t first = ring_n > uint32_t(R) ? ring_n - R : 0;
-      for (uint32_t n = first; n < ring_n; ++n) drain_wait(&kv_full[n % R], (n / R) & 1);
+      for (uint32_t n = n_k > R ? n_k - R : 0; n < n_k; ++n) drain_wait(&k_full[n % R], (n / R) & 1);
+      for (uint32_t n = n_v > R ? n_v - R : 0; n < n_v; ++n) drain_wait(&v_full[n % R], (n / R) & 1);
     }
-   } else if (warp == 5) {
-    // ------------------------------------------------------------ MMA issuer
+   } else if (warp == 1) {
+    // ------------------------------------------------------------ products P V
     // the whole warp walks the schedule; one elected lane issues the tcgen05 instructions
-    constexpr uint32_t kIdS = idesc_bf16_f32(128, kWinKeys, false, false);
     constexpr uint32_t kIdPV = idesc_bf16_f32(128, D, false, true);
-    const uint32_t id_sink = idesc_bf16_f32(128, p.sink_box, false, false);
-    const uint32_t aQ = smem_u32(sQ), aR = smem_u32(sRing);
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) umma_commit(bar);
-    };
-    uint32_t ring_n = 0, item_n = 0, tn = 0;
-    uint32_t sb = 0, pb = 0, p_par = 0;  // score buffers of the next S and PV, parity of the latter's P
+    const uint64_t vd0 = sdesc_sw128(smem_u32(sV), C::kBoxBytes, 1024);
+    uint32_t tn = 0;
+    Ring<R> vr;
+    Ring<C::kBufs> pr;
     bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
-      const bool r = warp_wait(bar, par, abort_flag);
-      tc_fence_after();
-      return r;
-    };
     for (uint32_t k = 0; ok; ++k) {
-      if (!meta_wait_warp(meta, k, abort_flag)) { ok = false; break; }
-      const ItemMeta& wi = meta.e[k % kMetaSlots];
-      if (wi.b < 0) break;
-      for (int t = wi.u0; t < wi.u1 && ok; ++t) {
-        const TileSteps st = tile_steps(wi, t, p.win.window);
-        if (st.n == 0) continue;
-        if (!wait(&q_full, item_n & 1)) { ok = false; break; }
-        ++item_n;
-        if (lane == 0) trace_event(p.trace, kTraceMma, tn, 10);
-        const uint32_t n0 = ring_n;
-        auto issue_S = [&](int j) -> bool {
-          const uint32_t n = n0 + k_pos<C::kBufs>(j), e = n % R;
-          if (!wait(&kv_full[e], (n / R) & 1)) return false;
-          const uint64_t qd = sdesc_sw128(aQ, 16, 1024), kd = sdesc_sw128(aR + e * C::kTileBytes, 16, 1024);
-          const uint32_t id = j < st.nz ? id_sink : kIdS, col = tmem + C::kColS + sb * kWinKeys;
-          if (elect_one()) {
+      if (!tile_wait_warp(tiles, k, abort_flag)) { ok = false; break; }
+      const int n = tiles.e[k % kMetaSlots].n, nz = tiles.e[k % kMetaSlots].nz;
+      const bool end = tiles.e[k % kMetaSlots].b < 0;
+      tile_release_warp(tiles, k);  // all it needs is in registers
+      if (end) break;
+      for (int j = 0; j < n; ++j) {
+        if (!warp_wait(&v_full[vr.e], vr.ph, abort_flag) || !warp_wait(&p_full[pr.e], pr.ph, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        if (lane == 0) trace_event(p.trace, kTraceMma, tn, 12);
+        const uint64_t vd = vd0 + vr.e * uint32_t(C::kTileBytes >> 4);
+        const uint32_t col = tmem + C::kColS + pr.e * kWinKeys;
+        const int kks = j < nz ? p.sink_box / 16 : kWinKeys / 16;  // 16 keys per product
+        if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
-              umma_ss(col, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                      kd + (((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), id, kk > 0);
-            umma_commit(&s_full[sb]);
-            umma_commit(&kv_empty[e]);
-            if (j + 1 == st.n) umma_commit(&q_empty);
-          }
-          sb = sb + 1 == C::kBufs ? 0 : sb + 1;
-          if (lane == 0) trace_event(p.trace, kTraceMma, tn, 16);
-          return true;
-        };
-        for (int j = 0; j < min(C::kBufs, st.n) && ok; ++j) ok = issue_S(j);
-        for (int j = 0; j < st.n && ok; ++j) {
-          const uint32_t n = n0 + v_pos<C::kBufs>(j, st.n), e = n % R;
-          if (!wait(&kv_full[e], (n / R) & 1) || !wait(&p_full[pb], p_par)) { ok = false; break; }
-          if (lane == 0) trace_event(p.trace, kTraceMma, tn, 12);
-          const uint64_t vd = sdesc_sw128(aR + e * C::kTileBytes, C::kBoxBytes, 1024);
-          const uint32_t col = tmem + C::kColS + pb * kWinKeys;
-          const int kks = j < st.nz ? p.sink_box / 16 : kWinKeys / 16;  // 16 keys per product
-          if (elect_one()) {
-#pragma unroll
-            for (int kk = 0; kk < kWinKeys / 16; ++kk)
-              if (kk < kks)
-                umma_ts(tmem + C::kColO, col + kk * 8, vd + uint32_t(kk * 2048 >> 4), kIdPV, j > 0 || kk > 0);
-            umma_commit(&kv_empty[e]);
-            if (j + 1 == st.n) umma_commit(&o_full);
-          }
-          if (++pb == C::kBufs) {
-            pb = 0;
-            p_par ^= 1;
-          }
-          if (lane == 0) trace_event(p.trace, kTraceMma, tn, 14);
-          if (j + C::kBufs < st.n) ok = issue_S(j + C::kBufs);
+          for (int kk = 0; kk < kWinKeys / 16; ++kk)
+            if (kk < kks)
+              umma_ts(tmem + C::kColO, col + kk * 8, vd + uint32_t(kk * 2048 >> 4), kIdPV, j > 0 || kk > 0);
+          umma_commit(&v_empty[vr.e]);
+          if (j + 1 == n) umma_commit(&o_full);
         }
-        ring_n = n0 + 2 * st.n;
+        vr.next();
+        pr.next();
+        if (lane == 0) trace_event(p.trace, kTraceMma, tn, 14);
       }
-      if (ok) meta_release_warp(meta, k);
     }
     if (!ok && lane == 0) raise_status(p.status, JFA_ERR_TIMEOUT);
-    commit(&mma_done);
-    drain_wait(&mma_done, 0);
-   } else if (warp == 6) {
-    // ------------------------------------------------------------ query tile loader
-    if (lane == 0) {
-      uint32_t item_n = 0, tn = 0;
-      bool ok = true;
-      if (p.whole) tmap_prefetch(&q_map);
-      for (uint32_t k = 0; ok; ++k) {
-        if (!meta_wait(meta, k, abort_flag)) { ok = false; break; }
-        const ItemMeta& wi = meta.e[k % kMetaSlots];
-        if (wi.b < 0) break;
-        for (int t = wi.u0; t < wi.u1 && ok; ++t) {
-          if (tile_steps(wi, t, p.win.window).n == 0) continue;
-          const TileMap m = tile_map(p.whole ? &q_map : nullptr, p.maps, p.B, kMapQ, wi.b, wi.qo, t, wi.Lq, p.total_q);
-          if (m.tail) tmap_acquire(m.map);
-          if (!mbar_wait(&q_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-          trace_event(p.trace, kTraceLoader, tn, 1);
-          mbar_arrive_expect_tx(&q_full, C::kQBytes);
-#pragma unroll
-          for (int c = 0; c < C::kBoxes; ++c) tma_load_2d(sQ + c * 16384, m.map, &q_full, wi.h * D + c * 64, m.y);
-          ++item_n;
-          // pull the next query tile into L2 meanwhile: the next of this range, else the first
-          // of this CTA's next item
-          const ItemMeta* nx = t + 1 < wi.u1 ? &wi : meta_peek_next(meta, k);
-          if (nx && p.whole) {
-            const int nt = t + 1 < wi.u1 ? t + 1 : nx->u0;
-            if ((nt + 1) * kBM <= nx->Lq)
-              for (int c = 0; c < C::kBoxes; ++c)
-                tma_prefetch_2d(&q_map, nx->h * D + c * 64, int(nx->qo) + nt * kBM);
-          }
-        }
-        if (ok) meta_release(meta, k);
+    if (elect_one()) umma_commit(&pv_done);
+    drain_wait(&pv_done, 0);
+   } else if (warp == 2) {
+    // ------------------------------------------------------------ query tile, scores Q K^T
+    constexpr uint32_t kIdS = idesc_bf16_f32(128, kWinKeys, false, false);
+    const uint32_t id_sink = idesc_bf16_f32(128, p.sink_box, false, false);
+    const uint64_t qd = sdesc_sw128(smem_u32(sQ), 16, 1024), kd0 = sdesc_sw128(smem_u32(sK), 16, 1024);
+    uint32_t n_q = 0, g = 0, tn = 0;  // query tiles loaded, scores issued
+    Ring<R> kr, vr;                   // vr: V tile of the step whose buffer is taken over
+    Ring<C::kBufs> sr;
+    bool ok = true;
+    if (lane == 0 && p.whole) tmap_prefetch(&q_map);
+    for (uint32_t k = 0; ok; ++k) {
+      if (!tile_wait_warp(tiles, k, abort_flag)) { ok = false; break; }
+      const WinTile& w = tiles.e[k % kMetaSlots];
+      if (w.b < 0) break;
+      const int n = w.n, nz = w.nz;
+      if (n == 0) {
+        tile_release_warp(tiles, k);
+        continue;
       }
-      if (!ok) raise_status(p.status, JFA_ERR_TIMEOUT);
-      if (item_n > 0) drain_wait(&q_full, (item_n - 1) & 1);
+      // the last scores of the previous tile have read the buffer
+      if (!warp_wait(&q_empty, (n_q & 1) ^ 1, abort_flag)) { ok = false; break; }
+      if (lane == 0) {
+        const TileMap m = tile_map(p.whole ? &q_map : nullptr, p.maps, p.B, kMapQ, w.b, w.qo, w.t, w.Lq, p.total_q);
+        if (m.tail) tmap_acquire(m.map);
+        trace_event(p.trace, kTraceLoader, tn, 1);
+        mbar_arrive_expect_tx(&q_full, C::kQBytes);
+#pragma unroll
+        for (int c = 0; c < C::kBoxes; ++c) tma_load_2d(sQ + c * 16384, m.map, &q_full, w.h * D + c * 64, m.y);
+        // pull the CTA's next query tile into L2 meanwhile, if the scheduler has it already
+        const uint32_t kn = k + 1;
+        if (p.whole && mbar_test_wait(&tiles.full[kn % kMetaSlots], (kn / kMetaSlots) & 1)) {
+          const WinTile& x = tiles.e[kn % kMetaSlots];
+          if (x.b >= 0 && x.rows == kBM)
+            for (int c = 0; c < C::kBoxes; ++c) tma_prefetch_2d(&q_map, x.h * D + c * 64, int(x.qo) + x.t * kBM);
+        }
+      }
+      tile_release_warp(tiles, k);
+      ++n_q;
+      if (!warp_wait(&q_full, (n_q - 1) & 1, abort_flag)) { ok = false; break; }
+      for (int j = 0; j < n; ++j, ++g) {
+        if (!warp_wait(&k_full[kr.e], kr.ph, abort_flag)) { ok = false; break; }
+        if (g >= C::kBufs) {  // the buffer's last product has read its P
+          if (!warp_wait(&v_empty[vr.e], vr.ph, abort_flag)) { ok = false; break; }
+          vr.next();
+        }
+        tc_fence_after();
+        const uint64_t kd = kd0 + kr.e * uint32_t(C::kTileBytes >> 4);
+        const uint32_t id = j < nz ? id_sink : kIdS, col = tmem + C::kColS + sr.e * kWinKeys;
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            umma_ss(col, qd + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                    kd + (((kk >> 2) * C::kBoxBytes + (kk & 3) * 32) >> 4), id, kk > 0);
+          umma_commit(&s_full[sr.e]);
+          umma_commit(&k_empty[kr.e]);
+          if (j + 1 == n) umma_commit(&q_empty);
+        }
+        sr.next();
+        kr.next();
+        if (lane == 0) trace_event(p.trace, kTraceLoader, tn, 16);
+      }
     }
+    if (!ok && lane == 0) raise_status(p.status, JFA_ERR_TIMEOUT);
+    // the query copy and the scores have landed before the CTA can exit
+    if (n_q > 0) drain_wait(&q_full, (n_q - 1) & 1);
+    if (elect_one()) umma_commit(&s_done);
+    drain_wait(&s_done, 0);
    } else {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish<true>(meta, p.items, *p.n_items, p.claim, p.q_off, p.kv_off, nullptr, nullptr,
-                                         abort_flag, p.win.window, p.win.sinks))
+    if (lane == 0 && !publish_tiles(tiles, p, abort_flag))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else {
     // ------------------------------------------------------------ softmax warps
-    const uint32_t lane_addr = uint32_t(warp * 32) << 16;
+    const int quarter = warp & 3;  // TMEM lane quarter this warp may access
+    const uint32_t lane_addr = uint32_t(quarter * 32) << 16;
     const uint32_t tO = tmem + lane_addr + C::kColO;
     const float sl2 = p.scale_log2;
-    uint32_t ring_n = 0, b = 0, s_par = 0, o_n = 0, tn = 0;  // b: score buffer of the next step
-    const bool leader = threadIdx.x == 0;
+    uint32_t v_n = 0, o_n = 0, tn = 0;  // v_n: steps before this tile
+    Ring<C::kBufs> sr;                  // score buffer of the next step
+    const bool leader = quarter == 0 && lane == 0;
     bool ok = true;
     for (uint32_t k = 0; ok; ++k) {
-      if (!meta_wait_warp(meta, k, abort_flag)) { ok = false; break; }
-      const ItemMeta& wi = meta.e[k % kMetaSlots];
-      if (wi.b < 0) break;
-      const WinSeq ws = meta_win(wi);
-      const int Lq = wi.Lq, diag = wi.Lk - Lq;
-      for (int t = wi.u0; t < wi.u1 && ok; ++t) {
-        const TileSteps st = tile_steps(wi, t, p.win.window);
-        const int r0 = t * kBM + warp * 32, i = r0 + lane;  // the warp's first row, this thread's
-        const bool valid = i < Lq;
-        __nv_bfloat16* orow = p.out + ((wi.qo + i) * p.H + wi.h) * int64_t(D);
-        float* lrow = p.lse + int64_t(wi.h) * p.total_q + wi.qo + i;
-        if (st.n == 0) {
-          if (valid) {
+      if (!tile_wait_warp(tiles, k, abort_flag)) { ok = false; break; }
+      const WinTile& w = tiles.e[k % kMetaSlots];
+      if (w.b < 0) break;
+      const int n = w.n, nz = w.nz, ns = w.ns, rows = w.rows;
+      const int r0 = quarter * 32, i = r0 + lane;  // the warp's first row, this thread's
+      const bool valid = i < rows;
+      const int64_t q_row = w.qo + w.t * kBM + i;
+      __nv_bfloat16* orow = p.out + (q_row * p.H + w.h) * int64_t(D);
+      float* lrow = p.lse + int64_t(w.h) * p.total_q + q_row;
+      int hi0 = r0 + w.pos + w.org, last = ns - 1, lo0 = -(1 << 30);  // first step of sinks
+      const int hi_win = r0 + w.pos - w.a * kWinKeys;                  // first key tile of the window part
+      tile_release_warp(tiles, k);  // the rest is in registers
+      if (n == 0) {
+        if (valid) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
-            *lrow = -INFINITY;
-          }
-          continue;
+          for (int c = 0; c < D / 8; ++c) reinterpret_cast<uint4*>(orow)[c] = make_uint4(0, 0, 0, 0);
+          *lrow = -INFINITY;
         }
-        // Row i sees columns [clo, chi] of a step.  The warp's rows see a band: rows r0 and r0 + 31
-        // up to hi0 and hi0 + 31 (the sinks' step: `last` at most), row r0 from lo0 and row r0 + 31
-        // from lo0 + 31 on.
-        float m = -INFINITY, l = 0.f;
-        int hi0 = r0 + diag + ws.org, last = ws.ns - 1, lo0 = -(1 << 30);  // first step of sinks
-        for (int j = 0; j < st.n; ++j) {
-          if (j == st.nz) {  // first key tile of the window part
-            hi0 = r0 + diag - st.a * kWinKeys;
-            last = 1 << 30;
-            lo0 = hi0 - p.win.window + 1;
-          }
-          const bool hidden = min(last, hi0 + 31) < 0 || lo0 >= kWinKeys || r0 >= Lq;  // from all 32 rows
-          const bool whole = min(last, hi0) >= kWinKeys - 1 && lo0 <= -31;             // seen by all 32
-          const uint32_t tS = tmem + lane_addr + C::kColS + b * kWinKeys;
-          if (!warp_wait(&s_full[b], s_par, abort_flag)) { ok = false; break; }
-          tc_fence_after();
-          if (leader) trace_event(p.trace, kTraceCompute0, tn, 20);
-          uint32_t pk[32];
-          if (!hidden) {
-            float x[64];
-            {
-              uint32_t r[2][32];
-              tmem_ld32(tS, r[0]);
-              tmem_ld32(tS + 32, r[1]);
-              tmem_ld_wait();
-#pragma unroll
-              for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
-            }
-            if (!whole) {
-              const int chi = min(last, hi0 + lane), clo = lo0 + lane;
-              const uint32_t bits[2] = {low_bits(chi + 1) & ~low_bits(clo), low_bits(chi - 31) & ~low_bits(clo - 32)};
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (!(bits[c >> 5] & (1u << (c & 31)))) x[c] = -INFINITY;
-            }
-            float mx4[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float m0 = fmaxf(x[16 * q], x[16 * q + 1]);
-#pragma unroll
-              for (int c = 2; c < 16; c += 2) m0 = fmax3(m0, x[16 * q + c], x[16 * q + c + 1]);
-              mx4[q] = m0;
-            }
-            const float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
-            // raise the reference maximum only when it grows by more than 2^8
-            const bool need = m_tile > m + kRescaleThreshold;
-            const float m_new = need ? m_tile : m;
-            const float alpha = need ? ex2_approx(m - m_new) : 1.f;  // m = -inf gives 0
-            const bool rescale = __any_sync(0xffffffffu, need && m != -INFINITY);
-            l *= alpha;
-            m = m_new;
-            const float m_use = m == -INFINITY ? 0.f : m;
-            const uint64_t k_scale = f2_pack(sl2, sl2), k_negm = f2_pack(-m_use, -m_use);
-            uint64_t sum2[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int c2 = 0; c2 < 32; ++c2) {
-              float e0, e1;
-              f2_unpack(f2_fma(f2_pack(x[2 * c2], x[2 * c2 + 1]), k_scale, k_negm), e0, e1);
-              e0 = ex2_approx(e0);
-              e1 = ex2_approx(e1);
-              sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
-              pk[c2] = pack_bf16x2(e0, e1);
-            }
-            tmem_st32(tS, pk);
-            float s0, s1;
-            f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), s0, s1);
-            l += s0 + s1;
-            if (rescale) {
-              // O holds earlier steps; the last of their products frees its V tile when done
-              const uint32_t n = ring_n + v_pos<C::kBufs>(j - 1, st.n);
-              if (!warp_wait(&kv_empty[n % R], (n / R) & 1, abort_flag)) { ok = false; break; }
-              tc_fence_after();
-#pragma unroll 1
-              for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t r[32];
-                tmem_ld32(tO + cc * 32, r);
-                tmem_ld_wait();
-#pragma unroll
-                for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
-                tmem_st32(tO + cc * 32, r);
-              }
-            }
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) pk[c] = 0u;
-            tmem_st32(tS, pk);
-          }
-          tmem_st_wait();
-          tc_fence_before();
-          mbar_arrive(&p_full[b]);
-          if (leader) trace_event(p.trace, kTraceCompute0, tn, 21);
-          if (++b == C::kBufs) {
-            b = 0;
-            s_par ^= 1;
-          }
-          hi0 -= kWinKeys;
-          lo0 -= kWinKeys;
-          last -= kWinKeys;
+        continue;
+      }
+      // Row i sees columns [clo, chi] of a step.  The warp's rows see a band: rows r0 and r0 + 31
+      // up to hi0 and hi0 + 31 (the sinks' step: `last` at most), row r0 from lo0 and row r0 + 31
+      // from lo0 + 31 on.
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n; ++j) {
+        if (j == nz) {  // first key tile of the window part
+          hi0 = hi_win;
+          last = 1 << 30;
+          lo0 = hi0 - p.win.window + 1;
         }
-        if (!ok) break;
-        ring_n += 2 * st.n;
-        // ---- epilogue: O / l -> bf16, lse = ln(sum) = (m + log2 l) * ln 2
-        if (!warp_wait(&o_full, o_n & 1, abort_flag)) { ok = false; break; }
-        ++o_n;
+        const bool hidden = min(last, hi0 + 31) < 0 || lo0 >= kWinKeys || r0 >= rows;  // from all 32 rows
+        const bool whole = min(last, hi0) >= kWinKeys - 1 && lo0 <= -31;             // seen by all 32
+        const uint32_t tS = tmem + lane_addr + C::kColS + sr.e * kWinKeys;
+        if (!warp_wait(&s_full[sr.e], sr.ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
-        if (leader) trace_event(p.trace, kTraceCompute0, tn, 22);
-        const bool live = l > 0.f;
-        const float inv_l = live ? 1.f / l : 0.f;
+        if (leader) trace_event(p.trace, kTraceCompute0, tn, 20);
+        uint32_t pk[32];
+        if (!hidden) {
+          float x[64];
+          {
+            uint32_t r[2][32];
+            tmem_ld32(tS, r[0]);
+            tmem_ld32(tS + 32, r[1]);
+            tmem_ld_wait();
 #pragma unroll
-        for (int c0 = 0; c0 < D; c0 += 64) {
-          uint32_t r[2][32];
-          tmem_ld32(tO + c0, r[0]);
-          tmem_ld32(tO + c0 + 32, r[1]);
-          tmem_ld_wait();
+            for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
+          }
+          if (!whole) {
+            const int chi = min(last, hi0 + lane), clo = lo0 + lane;
+            const uint32_t bits[2] = {low_bits(chi + 1) & ~low_bits(clo), low_bits(chi - 31) & ~low_bits(clo - 32)};
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if (!(bits[c >> 5] & (1u << (c & 31)))) x[c] = -INFINITY;
+          }
+          float mx4[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t w[8];
+            float m0 = fmaxf(x[16 * q], x[16 * q + 1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              w[e] = pack_bf16x2(__uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e]) * inv_l,
-                                 __uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e + 1]) * inv_l);
-            if (valid) st_global_v8(orow + c0 + q * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+            for (int c = 2; c < 16; c += 2) m0 = fmax3(m0, x[16 * q + c], x[16 * q + c + 1]);
+            mx4[q] = m0;
           }
+          const float m_tile = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * sl2;
+          const bool need = m_tile > m + kRescaleThreshold;
+          const float m_new = need ? m_tile : m;
+          const float alpha = need ? ex2_approx(m - m_new) : 1.f;  // m = -inf gives 0
+          const bool rescale = __any_sync(0xffffffffu, need && m != -INFINITY);
+          l *= alpha;
+          m = m_new;
+          const float m_use = m == -INFINITY ? 0.f : m;
+          const uint64_t k_scale = f2_pack(sl2, sl2), k_negm = f2_pack(-m_use, -m_use);
+          uint64_t sum2[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int c2 = 0; c2 < 32; ++c2) {
+            float e0, e1;
+            f2_unpack(f2_fma(f2_pack(x[2 * c2], x[2 * c2 + 1]), k_scale, k_negm), e0, e1);
+            e0 = ex2_approx(e0);
+            e1 = ex2_approx(e1);
+            sum2[c2 & 3] = f2_add(sum2[c2 & 3], f2_pack(e0, e1));
+            pk[c2] = pack_bf16x2(e0, e1);
+          }
+          tmem_st32(tS, pk);
+          float s0, s1;
+          f2_unpack(f2_add(f2_add(sum2[0], sum2[1]), f2_add(sum2[2], sum2[3])), s0, s1);
+          l += s0 + s1;
+          if (rescale) {
+            // O holds earlier steps; the last of their products frees its V tile when done
+            const uint32_t n = v_n + j - 1;
+            if (!warp_wait(&v_empty[n % R], (n / R) & 1, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t r[32];
+              tmem_ld32(tO + cc * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = __float_as_uint(__uint_as_float(r[c]) * alpha);
+              tmem_st32(tO + cc * 32, r);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) pk[c] = 0u;
+          tmem_st32(tS, pk);
         }
-        if (valid) *lrow = live ? ((m == -INFINITY ? 0.f : m) + __log2f(l)) * kLn2 : -INFINITY;
+        tmem_st_wait();
         tc_fence_before();
-        if (leader) trace_event(p.trace, kTraceCompute0, tn, 23);
+        mbar_arrive(&p_full[sr.e]);
+        if (leader) trace_event(p.trace, kTraceCompute0, tn, 21);
+        sr.next();
+        hi0 -= kWinKeys;
+        lo0 -= kWinKeys;
+        last -= kWinKeys;
       }
-      if (ok) meta_release_warp(meta, k);
+      if (!ok) break;
+      v_n += n;
+      // ---- epilogue: O / l -> bf16, lse = ln(sum) = (m + log2 l) * ln 2
+      const bool live = l > 0.f;
+      const float inv_l = live ? 1.f / l : 0.f;
+      if (valid) *lrow = live ? ((m == -INFINITY ? 0.f : m) + __log2f(l)) * kLn2 : -INFINITY;
+      if (!warp_wait(&o_full, o_n & 1, abort_flag)) { ok = false; break; }
+      ++o_n;
+      tc_fence_after();
+      if (leader) trace_event(p.trace, kTraceCompute0, tn, 22);
+#pragma unroll
+      for (int c0 = 0; c0 < D; c0 += 64) {
+        uint32_t r[2][32];
+        tmem_ld32(tO + c0, r[0]);
+        tmem_ld32(tO + c0 + 32, r[1]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w8[e] = pack_bf16x2(__uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e]) * inv_l,
+                                __uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e + 1]) * inv_l);
+          if (valid) st_global_v8(orow + c0 + q * 16, w8[0], w8[1], w8[2], w8[3], w8[4], w8[5], w8[6], w8[7]);
+        }
+      }
+      tc_fence_before();
+      if (leader) trace_event(p.trace, kTraceCompute0, tn, 23);
     }
     if (!ok) raise_status(p.status, JFA_ERR_TIMEOUT);
   }
@@ -493,7 +550,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kWinTmemCols);
+  if (warp == 1) tmem_dealloc(tmem, kWinTmemCols);
 }
 
 template <int D>
