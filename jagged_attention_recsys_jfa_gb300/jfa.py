@@ -7,8 +7,8 @@ without the built library, or with CPU tensors, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import Optional, Tuple
@@ -326,12 +326,52 @@ def jfa_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, bias=None, bias
 
 
 # ---------------------------------------------------------------- sliding window with sinks
-def _on(device, stream):
-    """Context of a call: `stream` current (so that what the call allocates and clears is
-    ordered with its kernels), else `device` current (no-op when it already is)."""
+_BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+def _call(device, stream, run):
+    """run(stream handle) with `stream` current (so that what the call allocates and clears is
+    ordered with its kernels), else on `device`'s current stream."""
     if stream is not None:
-        return torch.cuda.stream(stream)
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        with torch.cuda.stream(stream):
+            return run(int(stream.cuda_stream))
+    if device.index == torch.cuda.current_device():
+        return run(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device):
+        return run(torch._C._cuda_getCurrentRawStream(device.index))
+
+
+def _rows_ok(t, shape, device):
+    """Whether `t` is a contiguous bfloat16 CUDA tensor of that shape on `device`: the one test of
+    the usual call.  A call takes microseconds, so only a tensor that fails it is looked at again,
+    check by check, for the message."""
+    return t.dtype is _BF16 and t.shape == shape and t.is_contiguous() and t.device == device
+
+
+def _require_rows(name, t, shape, device):
+    try:
+        if _rows_ok(t, shape, device):
+            return
+    except AttributeError:
+        pass
+    _check_values(name, t, *shape)
+    raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
+
+
+def _require_lse(t, H, rows, device):
+    _check_lse(t, H, rows)
+    if t.device != device:
+        raise ValueError(f"lse is on {t.device}, the other tensors on {device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _window_bytes(B, H, G, d, Tq, Tk, sinks, backward):
+    return int(load_library().jfa_window_workspace_size(B, H, G, d, Tq, Tk, sinks, backward))
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_bytes(B, H, G, d):
+    return int(load_library().jfa_cache_workspace_size(B, H, G, d))
 
 
 def window_workspace_size(B, H, H_kv, d, total_q, total_kv, sinks, backward) -> int:
@@ -346,23 +386,22 @@ def new_window_workspace(B, H, H_kv, d, total_q, total_kv, sinks, backward, devi
     return _workspace(nbytes, device)
 
 
-def _check_windowed(q, k, v, q_offsets, kv_offsets, others):
+def _check_windowed(q, k, v, q_offsets, kv_offsets):
     """Checks of the inputs both directions share; returns (B, Tq, H, G, d, Tk)."""
     _check_values("q", q)
     Tq, H, d = q.shape
-    _check_values("k", k)
-    Tk, G = k.shape[0], k.shape[1]
-    if k.shape[2] != d or G < 1 or H % G:
+    if getattr(k, "ndim", 0) != 3 or k.shape[2] != d or k.shape[1] < 1 or H % k.shape[1]:
+        _check_values("k", k)
         raise ValueError(f"k has shape {tuple(k.shape)}, expected [*, a divisor of {H}, {d}]")
-    _check_values("v", v, rows=Tk, H=G, d=d)
-    _check_offsets("q_offsets", q_offsets)
-    _check_offsets("kv_offsets", kv_offsets)
-    if kv_offsets.numel() != q_offsets.numel():
-        raise ValueError("q_offsets and kv_offsets must have the same length")
-    for name, t in (("k", k), ("v", v), ("q_offsets", q_offsets), ("kv_offsets", kv_offsets), *others):
-        if t.device != q.device:
-            raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-    return q_offsets.numel() - 1, Tq, H, G, d, Tk
+    device, (Tk, G, _) = q.device, k.shape
+    _require_rows("k", k, (Tk, G, d), device)
+    _require_rows("v", v, (Tk, G, d), device)
+    n = q_offsets.numel()
+    for name, t in (("q_offsets", q_offsets), ("kv_offsets", kv_offsets)):
+        if not (t.dtype is _I64 and t.shape == (n,) and n > 1 and t.is_contiguous() and t.device == device):
+            _check_offsets(name, t)
+            raise ValueError(f"{name} must hold as many offsets as q_offsets, on {device}")
+    return n - 1, Tq, H, G, d, Tk
 
 
 def jfa_window_forward(q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None, out=None, lse=None,
@@ -376,29 +415,27 @@ def jfa_window_forward(q, k, v, q_offsets, kv_offsets, window=None, sinks=0, sca
     jfa_check_status(workspace).
     """
     lib = load_library()
-    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets, ())
-    window = _check_window(window, sinks)
+    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets)
+    device, window, sinks = q.device, _check_window(window, sinks), int(sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    nbytes = int(lib.jfa_window_workspace_size(B, H, G, d, Tq, Tk, int(sinks), 0))
-    with _on(q.device, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((H, Tq), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = _workspace(nbytes, q.device)
-        _check_values("out", out, rows=Tq, H=H, d=d)
-        _check_lse(lse, H, Tq)
-        for name, t in (("out", out), ("lse", lse)):
-            if t.device != q.device:
-                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-        ws_bytes = _check_workspace(workspace, nbytes, q.device)
-        st = lib.jfa_window_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(), kv_offsets.data_ptr(),
-                                    B, H, G, d, Tq, Tk, window, int(sinks), scale, out.data_ptr(), lse.data_ptr(),
-                                    workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != JFA_OK:
-        raise JfaError(st, "jfa_window_forward")
-    return out, lse, workspace
+    nbytes = _window_bytes(B, H, G, d, Tq, Tk, sinks, 0)
+
+    def run(handle):
+        o = torch.empty_like(q) if out is None else out
+        z = torch.empty((H, Tq), dtype=_F32, device=device) if lse is None else lse
+        ws = _workspace(nbytes, device) if workspace is None else workspace
+        if out is not None:
+            _require_rows("out", o, (Tq, H, d), device)
+        if lse is not None:
+            _require_lse(z, H, Tq, device)
+        st = lib.jfa_window_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_offsets.data_ptr(),
+                                    kv_offsets.data_ptr(), B, H, G, d, Tq, Tk, window, sinks, scale, o.data_ptr(),
+                                    z.data_ptr(), ws.data_ptr(), _check_workspace(ws, nbytes, device), handle)
+        if st != JFA_OK:
+            raise JfaError(st, "jfa_window_forward")
+        return o, z, ws
+
+    return _call(device, stream, run)
 
 
 def jfa_window_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, window=None, sinks=0, scale=None, dq=None,
@@ -407,31 +444,29 @@ def jfa_window_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, window=N
     being jfa_window_forward's results for the same inputs.  dk and dv (shaped like k and v) sum
     over the query heads that share a key/value head."""
     lib = load_library()
-    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets, (("dout", dout), ("out", out), ("lse", lse)))
-    for name, t in (("dout", dout), ("out", out)):
-        _check_values(name, t, rows=Tq, H=H, d=d)
-    _check_lse(lse, H, Tq)
-    window = _check_window(window, sinks)
+    B, Tq, H, G, d, Tk = _check_windowed(q, k, v, q_offsets, kv_offsets)
+    device, window, sinks = q.device, _check_window(window, sinks), int(sinks)
+    _require_rows("dout", dout, (Tq, H, d), device)
+    _require_rows("out", out, (Tq, H, d), device)
+    _require_lse(lse, H, Tq, device)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    nbytes = int(lib.jfa_window_workspace_size(B, H, G, d, Tq, Tk, int(sinks), 1))
-    with _on(q.device, stream):
-        dq = torch.empty_like(q) if dq is None else dq
-        dk = torch.empty_like(k) if dk is None else dk
-        dv = torch.empty_like(v) if dv is None else dv
-        if workspace is None:
-            workspace = _workspace(nbytes, q.device)
-        for name, t, ref in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-            _check_values(name, t, rows=ref.shape[0], H=ref.shape[1], d=d)
-            if t.device != q.device:
-                raise ValueError(f"{name} is on {t.device}, q on {q.device}")
-        ws_bytes = _check_workspace(workspace, nbytes, q.device)
+    nbytes = _window_bytes(B, H, G, d, Tq, Tk, sinks, 1)
+
+    def run(handle):
+        grads = [torch.empty_like(x) if g is None else g for g, x in ((dq, q), (dk, k), (dv, v))]
+        for name, g, given, x in zip(("dq", "dk", "dv"), grads, (dq, dk, dv), (q, k, v)):
+            if given is not None:
+                _require_rows(name, g, tuple(x.shape), device)
+        ws = _workspace(nbytes, device) if workspace is None else workspace
         st = lib.jfa_window_backward(dout.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                      lse.data_ptr(), q_offsets.data_ptr(), kv_offsets.data_ptr(), B, H, G, d, Tq, Tk,
-                                     window, int(sinks), scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                                     workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != JFA_OK:
-        raise JfaError(st, "jfa_window_backward")
-    return dq, dk, dv, workspace
+                                     window, sinks, scale, grads[0].data_ptr(), grads[1].data_ptr(), grads[2].data_ptr(),
+                                     ws.data_ptr(), _check_workspace(ws, nbytes, device), handle)
+        if st != JFA_OK:
+            raise JfaError(st, "jfa_window_backward")
+        return (*grads, ws)
+
+    return _call(device, stream, run)
 
 
 # ---------------------------------------------------------------- paged key/value cache
@@ -443,6 +478,14 @@ def _check_int32(name, t, shape, device):
 
 def _check_tokens(name, t, rows, heads, d, device):
     """Token rows [T, heads, d], each row contiguous; tokens may be strided."""
+    try:
+        n, h, w = t.shape
+        if (t.dtype is _BF16 and w == d and t.device == device and (rows is None or n == rows)
+                and (heads is None or h == heads) and n > 1 and h > 0 and t.stride() == (t.stride(0), d, 1)
+                and t.stride(0) % 8 == 0 and t.stride(0) >= h * d and t.data_ptr() % 16 == 0):
+            return
+    except (AttributeError, ValueError):
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device} (the library has no CPU path)")
     if t.dtype != torch.bfloat16:
@@ -456,6 +499,24 @@ def _check_tokens(name, t, rows, heads, d, device):
 
 
 def _cache_struct(k_cache, v_cache, page_table, lengths):
+    try:
+        device, shape = k_cache.device, k_cache.shape
+        ok = (k_cache.is_cuda and len(shape) == 4 and page_table.dim() == 2 and _rows_ok(k_cache, shape, device)
+              and _rows_ok(v_cache, shape, device) and page_table.dtype is _I32 and lengths.dtype is _I32
+              and page_table.shape[0] > 0 and lengths.shape == page_table.shape[:1] and page_table.is_contiguous()
+              and lengths.is_contiguous() and page_table.device == device and lengths.device == device)
+    except AttributeError:
+        ok = False
+    if not ok:
+        _explain_cache(k_cache, v_cache, page_table, lengths)
+    P, G, page, d = shape
+    B, width = page_table.shape
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), P, G, page, d, page_table.data_ptr(), width,
+                  lengths.data_ptr(), B)
+
+
+def _explain_cache(k_cache, v_cache, page_table, lengths):
+    """Raises for the first thing wrong with a cache."""
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
@@ -465,12 +526,10 @@ def _cache_struct(k_cache, v_cache, page_table, lengths):
                              "(both of one shape, on one device)")
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2 or page_table.shape[0] < 1:
         raise ValueError("page_table must be an int32 CUDA tensor [B, max_pages]")
-    device, B = k_cache.device, page_table.shape[0]
-    _check_int32("page_table", page_table, (B, page_table.shape[1]), device)
-    _check_int32("lengths", lengths, (B,), device)
-    P, G, page, d = k_cache.shape
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), P, G, page, d, page_table.data_ptr(), page_table.shape[1],
-                  lengths.data_ptr(), B)
+    B = page_table.shape[0]
+    _check_int32("page_table", page_table, (B, page_table.shape[1]), k_cache.device)
+    _check_int32("lengths", lengths, (B,), k_cache.device)
+    raise ValueError("unusable cache")
 
 
 def cache_workspace_size(B, H, H_kv, d) -> int:
@@ -508,13 +567,13 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
     """
     lib = load_library()
     cache = _cache_struct(k_cache, v_cache, page_table, lengths)
-    device, G, d = k_cache.device, cache.H_kv, cache.d
+    device, G, d, B = k_cache.device, cache.H_kv, cache.d, cache.B
     _check_tokens("k", k, None, G, d, device)
     T = k.shape[0]
     _check_tokens("v", v, T, G, d, device)
-    _check_offsets("offsets", offsets)
-    if offsets.device != device or offsets.numel() != cache.B + 1:
-        raise ValueError(f"offsets must have {cache.B + 1} entries on {device}")
+    if not (offsets.dtype is _I64 and offsets.shape == (B + 1,) and offsets.is_contiguous() and offsets.device == device):
+        _check_offsets("offsets", offsets)
+        raise ValueError(f"offsets must have {B + 1} entries on {device}")
     H = 0
     if q is not None:
         _check_tokens("q", q, T, None, d, device)
@@ -527,29 +586,32 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
                 or frequencies.dim() != 1 or not frequencies.is_contiguous()):
             raise ValueError("frequencies must be a contiguous float64 CPU tensor [rot_dim / 2]")
         rot, freq_ptr = 2 * frequencies.numel(), frequencies.data_ptr()
-    with _on(device, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty((T, H, d), dtype=torch.bfloat16, device=device)
+
+    def run(handle):
+        qo, ws = q_out, workspace
+        if q is not None and qo is None:
+            qo = torch.empty((T, H, d), dtype=_BF16, device=device)
+        elif qo is not None:
+            _require_rows("q_out", qo, (T, H, d), device)
+        if k_out is not None:
+            _require_rows("k_out", k_out, (T, G, d), device)
         if lengths_out is None:
-            lengths_out = torch.empty_like(lengths)
-        if workspace is None:
-            workspace = _workspace(256, device)
-        _check_int32("lengths_out", lengths_out, (cache.B,), device)
-        for name, t, heads in (("q_out", q_out, H), ("k_out", k_out, G)):
-            if t is not None:
-                _check_values(name, t, rows=T, H=heads, d=d)
-                if t.device != device:
-                    raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-        ws_bytes = _check_workspace(workspace, 256, device)
+            n = torch.empty_like(lengths)
+        else:
+            n = lengths_out
+            _check_int32("lengths_out", n, (B,), device)
+        if ws is None:
+            ws = _workspace(256, device)
         st = lib.jfa_cache_append(ctypes.byref(cache), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
-                                  q.data_ptr() if q is not None else None, q.stride(0) if q is not None else 0, H,
-                                  offsets.data_ptr(), T, freq_ptr, rot, 1 if interleaved else 0,
-                                  q_out.data_ptr() if q is not None else None,
-                                  k_out.data_ptr() if k_out is not None else None, lengths_out.data_ptr(),
-                                  workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != JFA_OK:
-        raise JfaError(st, "jfa_cache_append")
-    return q_out, k_out, lengths_out, workspace
+                                  q.data_ptr() if H else None, q.stride(0) if H else 0, H, offsets.data_ptr(), T,
+                                  freq_ptr, rot, 1 if interleaved else 0, qo.data_ptr() if H else None,
+                                  k_out.data_ptr() if k_out is not None else None, n.data_ptr(), ws.data_ptr(),
+                                  _check_workspace(ws, 256, device), handle)
+        if st != JFA_OK:
+            raise JfaError(st, "jfa_cache_append")
+        return qo, k_out, n, ws
+
+    return _call(device, stream, run)
 
 
 def jfa_cache_attention(q, k_cache, v_cache, page_table, lengths, window=None, sinks=0, scale=None, out=None, lse=None,
@@ -565,31 +627,30 @@ def jfa_cache_attention(q, k_cache, v_cache, page_table, lengths, window=None, s
     lib = load_library()
     cache = _cache_struct(k_cache, v_cache, page_table, lengths)
     device, G, d, B = k_cache.device, cache.H_kv, cache.d, cache.B
-    _check_values("q", q)
-    if q.device != device or q.shape[0] != B or q.shape[2] != d or q.shape[1] % G:
-        raise ValueError(f"q has shape {tuple(q.shape)} on {q.device}, expected [{B}, a multiple of {G}, {d}] on {device}")
-    H = q.shape[1]
-    window = _check_window(window, sinks)
+    H = q.shape[1] if getattr(q, "ndim", 0) == 3 else 0
+    if H < 1 or H % G:
+        _check_values("q", q)
+        raise ValueError(f"q has shape {tuple(q.shape)}, expected [{B}, a multiple of {G}, {d}]")
+    _require_rows("q", q, (B, H, d), device)
+    window, sinks = _check_window(window, sinks), int(sinks)
     scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
-    nbytes = int(lib.jfa_cache_workspace_size(B, H, G, d))
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty((H, B), dtype=torch.float32, device=device)
-        if workspace is None:
-            workspace = _workspace(nbytes, device)
-        _check_values("out", out, rows=B, H=H, d=d)
-        _check_lse(lse, H, B)
-        for name, t in (("out", out), ("lse", lse)):
-            if t.device != device:
-                raise ValueError(f"{name} is on {t.device}, the cache on {device}")
-        ws_bytes = _check_workspace(workspace, nbytes, device)
-        st = lib.jfa_cache_attention(ctypes.byref(cache), q.data_ptr(), H, window, int(sinks), scale, out.data_ptr(),
-                                     lse.data_ptr(), workspace.data_ptr(), ws_bytes, _stream_handle(stream))
-    if st != JFA_OK:
-        raise JfaError(st, "jfa_cache_attention")
-    return out, lse, workspace
+    nbytes = _cache_bytes(B, H, G, d)
+
+    def run(handle):
+        o = torch.empty_like(q) if out is None else out
+        z = torch.empty((H, B), dtype=_F32, device=device) if lse is None else lse
+        ws = _workspace(nbytes, device) if workspace is None else workspace
+        if out is not None:
+            _require_rows("out", o, (B, H, d), device)
+        if lse is not None:
+            _require_lse(z, H, B, device)
+        st = lib.jfa_cache_attention(ctypes.byref(cache), q.data_ptr(), H, window, sinks, scale, o.data_ptr(),
+                                     z.data_ptr(), ws.data_ptr(), _check_workspace(ws, nbytes, device), handle)
+        if st != JFA_OK:
+            raise JfaError(st, "jfa_cache_attention")
+        return o, z, ws
+
+    return _call(device, stream, run)
 
 
 def jfa_check_status(workspace, stream=None) -> int:
