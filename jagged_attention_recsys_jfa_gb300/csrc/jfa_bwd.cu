@@ -1499,7 +1499,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
      if (!meta_wait_warp(meta, item_k, abort_flag)) { ok = false; break; }
      const ItemMeta& it = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
      if (it.b < 0) break;  // end of this CTA's items
-     const int Lq = it.Lq, Lk = it.Lk;
+     const int Lq = it.Lq;
      for (int qt = it.u0; qt < it.u1 && ok; ++qt) {
       const int i = qt * kBM + row;
       const bool valid = i < Lq;

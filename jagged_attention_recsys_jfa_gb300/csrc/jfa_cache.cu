@@ -36,22 +36,19 @@ struct AppendParams {
   int32_t* lengths_out;                        // nullptr, or tokens cached after it (may be `lengths`)
   __nv_bfloat16 *q_out, *k_out;                // rotated rows, contiguous; k_out may be nullptr
   int64_t num_pages;
-  int B, H, Hkv, d, page_size, max_pages;
+  int B, H, Hkv, page_size, max_pages;         // H: query heads, 0 without q
   int rot;                                     // leading dims of each head that are rotated (0: none)
   int interleaved;
-  int tokens_per_cta;
+  int warps_per_token;                         // 1, 2, 4 or 8
   int* status;
   unsigned* done;                              // CTAs that have read `lengths` (left at 0)
   uint64_t turn[64];
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendMaxTokens = 8;  // per CTA: one setup warp each
-
-struct TokenInfo {
-  int64_t row;   // element offset of the token's row 0 of head 0 in the cache, -1: not stored
-  int valid;     // a token of some sequence
-};
+// Rows per lane in flight (841 MB of prompts, d = 128: 1 row 168 us, 2 rows 154, 3 rows 158, 6 rows
+// 180; with 2, five CTAs per SM 150).
+constexpr int kAppendBatch = 2;
 
 // The last b with offsets[b] <= t (offsets non-decreasing, offsets[0] <= t), by the whole
 // warp: 32 probes per step, so B = 1024 takes two dependent loads instead of ten.
@@ -80,19 +77,24 @@ __device__ __forceinline__ uint32_t rot_pair(uint32_t a, const float2& c) {
   return pack_bf16x2(bf16lo(a) * c.x - bf16hi(a) * c.y, bf16hi(a) * c.x + bf16lo(a) * c.y);
 }
 
-// One CTA: up to tokens_per_cta consecutive tokens.  A thread moves two 16-byte chunks of a
-// row at a time: chunks c and c + r/16 of a half-split pair, else neighbours, so that both
-// halves of every pair meet in one thread's registers.
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
-  __shared__ TokenInfo info[kAppendMaxTokens];
-  __shared__ float2 cs[kAppendMaxTokens][64];  // cos, sin
+// A token is one warp's (or, when there are few tokens, split over warps_per_token warps of a
+// CTA): D / 16 lanes share a row, and a lane moves two 16-byte chunks of it, chunks c and c + r/16
+// where they are a half-split pair's halves, else neighbours, so that both elements of every pair
+// meet in one lane.  A lane's pairs are the same in every row of the token, so its 8 sines and
+// cosines stay in registers for all heads (read again for every row from shared memory, the call
+// took 166 us on 841 MB instead of 150, 5.6 TB/s).  The first rows' loads are under way while the
+// token's sequence, page and angles are found.
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 16, kSlots = 32 / kLanes;  // lanes per row, rows a warp takes at a time
+  constexpr int kWarps = kAppendThreads / 32;
+  __shared__ __align__(16) float2 cs_all[kWarps][D / 2];  // cos, sin of each warp's token
   __shared__ bool last_cta;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int64_t t0 = int64_t(blockIdx.x) * p.tokens_per_cta;
-  const int64_t n_rows = p.total - t0;
-  const int n_tok = n_rows <= 0 ? 0 : (n_rows < p.tokens_per_cta ? int(n_rows) : p.tokens_per_cta);
+  const int64_t t = (int64_t(blockIdx.x) * kWarps + warp) / p.warps_per_token;
+  const int sub = warp % p.warps_per_token;
 
   if (blockIdx.x == 0) {  // malformed offsets or lengths: every access below stays in bounds all the same
     int bad = 0;
@@ -100,88 +102,96 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     if (tid == 0) bad |= p.offsets[0] != 0 || p.offsets[p.B] > p.total;
     if (bad) raise_status(p.status, JFA_ERR_BAD_OFFSETS);
   }
-  if (warp < n_tok) {
-    const int64_t t = t0 + warp;
-    TokenInfo ti = {-1, 0};
-    if (t < __ldg(p.offsets + p.B) && t >= __ldg(p.offsets)) {
-      const int b = find_sequence(p.offsets, p.B, t, lane);
-      const int64_t pos = int64_t(p.lengths[b]) + (t - __ldg(p.offsets + b));
-      const int64_t pg = pos / p.page_size;
-      ti.valid = 1;
-      if (pos >= 0 && pg < p.max_pages) {
-        const int page = __ldg(p.page_table + int64_t(b) * p.max_pages + pg);
-        if (page >= 0 && page < p.num_pages)
-          ti.row = (int64_t(page) * p.Hkv * p.page_size + (pos - pg * p.page_size)) * p.d;
+  const int64_t first = __ldg(p.offsets), last = __ldg(p.offsets + p.B);
+  if (t < p.total && t >= first && t < last) {  // rows of a sequence; others are left alone
+    const int c = lane % kLanes;  // this lane's chunk pair
+    const int half = p.rot / 16;  // chunks in half of the rotated dims
+    const bool split = !p.interleaved && c < half, inter = p.interleaved && 16 * c < p.rot;
+    const int a = split ? c : 2 * c, b = split ? c + half : a + 1;
+    // rows of the token: H_kv of k, H_kv of v, H of q
+    const int rows = 2 * p.Hkv + p.H, step = kSlots * p.warps_per_token;
+    const __nv_bfloat16 *kt = p.k + t * p.k_stride, *vt = p.v + t * p.v_stride, *qt = p.q + t * p.q_stride;
+    uint4 x[kAppendBatch], y[kAppendBatch];
+    auto load = [&](int r0) {
+#pragma unroll
+      for (int u = 0; u < kAppendBatch; ++u) {
+        const int r = r0 + u * step;
+        if (r >= rows) break;
+        const __nv_bfloat16* src = r < p.Hkv ? kt + r * D : r < 2 * p.Hkv ? vt + (r - p.Hkv) * D : qt + (r - 2 * p.Hkv) * D;
+        x[u] = reinterpret_cast<const uint4*>(src)[a];
+        y[u] = reinterpret_cast<const uint4*>(src)[b];
       }
-      if (ti.row < 0 && lane == 0) raise_status(p.status, JFA_ERR_BAD_PAGES);
-      for (int i = lane; i < p.rot / 2; i += 32) {
-        const uint64_t turns = uint64_t(pos) * p.turn[i];
-        float s, c;
-        // top 32 bits as a signed fraction of a turn: [-1/2, 1/2)
-        sincospif(float(int32_t(turns >> 32)) * 4.656612873077393e-10f, &s, &c);  // 2^-31
-        cs[warp][i] = make_float2(c, s);
-      }
-    }
-    if (lane == 0) info[warp] = ti;
-  }
-  __syncthreads();
+    };
+    const int r_first = sub * kSlots + lane / kLanes;
+    load(r_first);
 
-  // rows of a token: H_kv of k, H_kv of v, H of q
-  const int pairs = p.d / 16;  // 16-byte chunk pairs per row
-  const int rows = 2 * p.Hkv + (p.q ? p.H : 0);
-  const int per_token = rows * pairs;
-  const int half = p.rot / 16;  // chunks in half of the rotated dims
-  for (int i = tid; i < n_tok * per_token; i += kAppendThreads) {
-    const int tk = i / per_token, e = i - tk * per_token;
-    const int r = e / pairs, c = e - r * pairs;
-    const TokenInfo ti = info[tk];
-    if (!ti.valid) continue;
-    const int64_t t = t0 + tk;
-    const bool is_v = r >= p.Hkv && r < 2 * p.Hkv, is_q = r >= 2 * p.Hkv;
-    const int h = is_q ? r - 2 * p.Hkv : is_v ? r - p.Hkv : r;
-    const __nv_bfloat16* src = is_q ? p.q + t * p.q_stride : is_v ? p.v + t * p.v_stride : p.k + t * p.k_stride;
-    // chunk pair c of the row: (a, b)
-    int a, b;
-    if (p.interleaved || c >= half) {
-      a = p.interleaved ? 2 * c : 2 * half + 2 * (c - half);
-      b = a + 1;
-    } else {
-      a = c;
-      b = c + half;
+    // ---- the token's place and angles
+    const int seq = find_sequence(p.offsets, p.B, t, lane);
+    const int64_t pos = int64_t(p.lengths[seq]) + (t - __ldg(p.offsets + seq));
+    const int64_t pg = pos / p.page_size;
+    int64_t at = -1;  // element offset of the token's row of head 0 in the cache, -1: not stored
+    if (pos >= 0 && pg < p.max_pages) {
+      const int page = __ldg(p.page_table + int64_t(seq) * p.max_pages + pg);
+      if (page >= 0 && page < p.num_pages)
+        at = (int64_t(page) * p.Hkv * p.page_size + (pos - pg * p.page_size)) * D;
     }
-    const uint4* s4 = reinterpret_cast<const uint4*>(src + int64_t(h) * p.d);
-    uint4 x = s4[a], y = s4[b];
-    if (!is_v && p.rot > 0) {
-      const float2* t2 = cs[tk];
-      if (p.interleaved) {
-        if (8 * a < p.rot) {
-          t2 += 4 * a;
-          x = make_uint4(rot_pair(x.x, t2[0]), rot_pair(x.y, t2[1]), rot_pair(x.z, t2[2]), rot_pair(x.w, t2[3]));
-          y = make_uint4(rot_pair(y.x, t2[4]), rot_pair(y.y, t2[5]), rot_pair(y.z, t2[6]), rot_pair(y.w, t2[7]));
+    if (at < 0 && lane == 0) raise_status(p.status, JFA_ERR_BAD_PAGES);
+    float2* cs = cs_all[warp];
+    for (int i = lane; i < p.rot / 2; i += 32) {
+      const uint64_t turns = uint64_t(pos) * p.turn[i];
+      float sn, cn;
+      // top 32 bits as a signed fraction of a turn: [-1/2, 1/2)
+      sincospif(float(int32_t(turns >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
+      cs[i] = make_float2(cn, sn);
+    }
+    __syncwarp();
+    float2 w[8];  // this lane's pairs: 8 of a split pair of chunks, 4 + 4 of two interleaved ones
+    if (split || inter) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float4 f = reinterpret_cast<const float4*>(cs + 8 * c)[e];
+        w[2 * e] = make_float2(f.x, f.y);
+        w[2 * e + 1] = make_float2(f.z, f.w);
+      }
+    }
+
+    // ---- rotate and store, kAppendBatch rows at a time
+    for (int r0 = r_first; r0 < rows; r0 += kAppendBatch * step) {
+      if (r0 != r_first) load(r0);
+#pragma unroll
+      for (int u = 0; u < kAppendBatch; ++u) {
+        const int r = r0 + u * step;
+        if (r >= rows) break;
+        const bool is_k = r < p.Hkv, is_q = r >= 2 * p.Hkv;
+        if (is_k || is_q) {
+          const uint4 x0 = x[u], y0 = y[u];
+          if (inter) {
+            x[u] = make_uint4(rot_pair(x0.x, w[0]), rot_pair(x0.y, w[1]), rot_pair(x0.z, w[2]), rot_pair(x0.w, w[3]));
+            y[u] = make_uint4(rot_pair(y0.x, w[4]), rot_pair(y0.y, w[5]), rot_pair(y0.z, w[6]), rot_pair(y0.w, w[7]));
+          } else if (split) {
+            x[u] = make_uint4(rot_lo(x0.x, y0.x, w[0], w[1]), rot_lo(x0.y, y0.y, w[2], w[3]),
+                              rot_lo(x0.z, y0.z, w[4], w[5]), rot_lo(x0.w, y0.w, w[6], w[7]));
+            y[u] = make_uint4(rot_hi(x0.x, y0.x, w[0], w[1]), rot_hi(x0.y, y0.y, w[2], w[3]),
+                              rot_hi(x0.z, y0.z, w[4], w[5]), rot_hi(x0.w, y0.w, w[6], w[7]));
+          }
         }
-      } else if (c < half) {
-        t2 += 8 * c;
-        const uint4 x0 = x, y0 = y;
-        x = make_uint4(rot_lo(x0.x, y0.x, t2[0], t2[1]), rot_lo(x0.y, y0.y, t2[2], t2[3]),
-                       rot_lo(x0.z, y0.z, t2[4], t2[5]), rot_lo(x0.w, y0.w, t2[6], t2[7]));
-        y = make_uint4(rot_hi(x0.x, y0.x, t2[0], t2[1]), rot_hi(x0.y, y0.y, t2[2], t2[3]),
-                       rot_hi(x0.z, y0.z, t2[4], t2[5]), rot_hi(x0.w, y0.w, t2[6], t2[7]));
-      }
-    }
-    if (is_q) {
-      uint4* o = reinterpret_cast<uint4*>(p.q_out + (t * p.H + h) * p.d);
-      o[a] = x;
-      o[b] = y;
-    } else {
-      if (ti.row >= 0) {
-        uint4* o = reinterpret_cast<uint4*>((is_v ? p.v_cache : p.k_cache) + ti.row + int64_t(h) * p.page_size * p.d);
-        o[a] = x;
-        o[b] = y;
-      }
-      if (!is_v && p.k_out) {
-        uint4* o = reinterpret_cast<uint4*>(p.k_out + (t * p.Hkv + h) * p.d);
-        o[a] = x;
-        o[b] = y;
+        if (is_q) {
+          uint4* o = reinterpret_cast<uint4*>(p.q_out + (t * p.H + r - 2 * p.Hkv) * D);
+          o[a] = x[u];
+          o[b] = y[u];
+        } else {
+          const int h = is_k ? r : r - p.Hkv;
+          if (at >= 0) {
+            uint4* o = reinterpret_cast<uint4*>((is_k ? p.k_cache : p.v_cache) + at + int64_t(h) * p.page_size * D);
+            o[a] = x[u];
+            o[b] = y[u];
+          }
+          if (is_k && p.k_out) {
+            uint4* o = reinterpret_cast<uint4*>(p.k_out + (t * p.Hkv + h) * D);
+            o[a] = x[u];
+            o[b] = y[u];
+          }
+        }
       }
     }
   }
@@ -687,7 +697,6 @@ cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* 
   p.B = c.B;
   p.H = a.H;
   p.Hkv = c.H_kv;
-  p.d = c.d;
   p.page_size = c.page_size;
   p.max_pages = c.max_pages;
   p.rot = a.rot;
@@ -696,11 +705,14 @@ cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* 
   p.done = reinterpret_cast<unsigned*>(&static_cast<WsHeader*>(ws)->claim_fwd);
   for (int i = 0; i < a.rot / 2; ++i) p.turn[i] = a.turn[i];
   for (int i = a.rot / 2; i < 64; ++i) p.turn[i] = 0;
-  // a few tokens: one per CTA, so that the call spreads over the SMs; else eight, so that a
-  // CTA's setup (sequence search, angles) is shared by enough rows
-  p.tokens_per_cta = a.total <= 4 * num_sms ? 1 : kAppendMaxTokens;
-  const int64_t ctas = (a.total + p.tokens_per_cta - 1) / p.tokens_per_cta;
-  return launch_pdl(append_kernel, dim3(unsigned(ctas > 0 ? ctas : 1)), dim3(kAppendThreads), 0, stream, p);
+  // few tokens: several warps for each, until the warps fill the card about twice over; then one
+  constexpr int kWarps = kAppendThreads / 32;
+  p.warps_per_token = kWarps;
+  while (p.warps_per_token > 1 && a.total * p.warps_per_token > int64_t(64) * num_sms) p.warps_per_token /= 2;
+  const int64_t ctas = (a.total * p.warps_per_token + kWarps - 1) / kWarps;
+  const dim3 grid(unsigned(ctas > 0 ? ctas : 1));
+  return c.d == 128 ? launch_pdl(append_kernel<128>, grid, dim3(kAppendThreads), 0, stream, p)
+                    : launch_pdl(append_kernel<64>, grid, dim3(kAppendThreads), 0, stream, p);
 }
 
 cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& km, const CUtensorMap& vm, const void* q, int H,
