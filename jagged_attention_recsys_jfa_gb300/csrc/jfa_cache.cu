@@ -393,46 +393,57 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
 
   if (warp == kAttnWarps) {
     // ------------------------------------------------------------ producer
-    // lane i of the first lanes copies page i of a tile (K and V, D / 64 boxes each)
+    // A tile is `boxes` boxes of K and of V, one page's rows each (64 at most).  The warp looks up
+    // the pages of 32 boxes at a time, a batch ahead of the copies: lane x holds box x % boxes of
+    // the batch's tile x / boxes.  (With one lookup per tile in front of its copies: 43 us instead of
+    // 40 on 189 MB in pages of 16, d = 64.)
     const int box = p.page_size < kTileKeys ? p.page_size : kTileKeys;
-    const int boxes = kTileKeys / box;
+    const int boxes = kTileKeys / box, batch = 32 / boxes;
     uint32_t n = 0;
     bool ok = true;
     for (int64_t t = t0; t < t1 && ok; next_unit(p, w)) {
       const int64_t end = min(t1, w.unit0 + w.s.n);
       const int32_t* table = p.page_table + int64_t(w.b) * p.max_pages;
-      for (; t < end && ok; ++t, ++n) {
-        const int i = int(t - w.unit0);
+      // this lane's box of the batch that starts at tile t: its page (-1: none to copy) and row in it
+      auto look_up = [&](int64_t tb, int& page, int& off) {
+        const int i = int(tb - w.unit0) + lane / boxes;
         const bool sink = i < w.s.n_sink;
         const int j0 = (sink ? i : w.s.lo / kTileKeys + i - w.s.n_sink) * kTileKeys;
-        const int v_lo = sink ? 0 : w.s.lo, v_hi = sink ? w.s.s_end : w.s.len;
-        // this lane's box: keys [jb, jb + box)
-        const int jb = j0 + lane * box;
-        bool load = lane < boxes && jb < v_hi && jb + box > v_lo;
-        int64_t row = 0;
-        if (load) {
-          const int page = __ldg(table + jb / p.page_size);
+        const int jb = j0 + lane % boxes * box;  // keys [jb, jb + box)
+        page = -1;
+        off = jb % p.page_size;
+        if (tb + lane / boxes < end && jb < (sink ? w.s.s_end : w.s.len) && jb + box > (sink ? 0 : w.s.lo)) {
+          page = __ldg(table + jb / p.page_size);
           if (page < 0 || page >= p.num_pages) {
             raise_status(p.status, JFA_ERR_BAD_PAGES);
-            load = false;
-          } else {
-            row = (int64_t(page) * p.Hkv + w.hk) * p.page_size + (jb % p.page_size);
+            page = -1;
           }
         }
-        const uint32_t e = n % C::kStages, ph = (n / C::kStages) & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs));
-        if (!ok) break;
-        const int count = __popc(__ballot_sync(0xffffffffu, load));
-        if (lane == 0) mbar_arrive_expect_tx(&full[e], uint32_t(count) * box * D * 4);
-        __syncwarp();
-        if (load) {
-          uint8_t* dst = ring + e * C::kStageBytes + lane * box * 128;
+      };
+      int page, off, page_next = -1, off_next = 0;
+      look_up(t, page, off);
+      while (t < end && ok) {
+        if (t + batch < end) look_up(t + batch, page_next, off_next);
+        const unsigned loads = __ballot_sync(0xffffffffu, page >= 0);
+        const int row = int((int64_t(page) * p.Hkv + w.hk) * p.page_size + off);  // below 2^31
+        for (int x = 0; x < batch && t < end; ++x, ++t, ++n) {
+          const uint32_t e = n % C::kStages, ph = (n / C::kStages) & 1;
+          ok = __all_sync(0xffffffffu, mbar_wait(&empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs));
+          if (!ok) break;
+          const unsigned group = ((1u << boxes) - 1u) << (x * boxes);
+          if (lane == 0) mbar_arrive_expect_tx(&full[e], uint32_t(__popc(loads & group)) * box * D * 4);
+          __syncwarp();
+          if ((loads & group) >> lane & 1u) {
+            uint8_t* dst = ring + e * C::kStageBytes + (lane - x * boxes) * box * 128;
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            tma_load_2d(dst + c * C::kHalf, &k_map, &full[e], c * 64, int32_t(row));
-            tma_load_2d(dst + C::kTileBytes + c * C::kHalf, &v_map, &full[e], c * 64, int32_t(row));
+            for (int c = 0; c < D / 64; ++c) {
+              tma_load_2d(dst + c * C::kHalf, &k_map, &full[e], c * 64, row);
+              tma_load_2d(dst + C::kTileBytes + c * C::kHalf, &v_map, &full[e], c * 64, row);
+            }
           }
         }
+        page = page_next;
+        off = off_next;
       }
     }
     if (!ok && lane == 0) raise_status(p.status, JFA_ERR_TIMEOUT);
