@@ -590,8 +590,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
           const bool sink = kWin && ku.chunk >= 0;
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
           const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv);
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv);
+          const int pad = kWin && !sink ? meta_win(wi).pad : 0;
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, pad);
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, pad);
           if (mk.tail) {
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
@@ -604,7 +605,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
           ++item_n;
           // pull the next key tile into L2 meanwhile: the next of this range, else the first
           // of this CTA's next item
-          if (!kWin) {
+          if (kWin) {  // items are single units
+            const ItemMeta* wn = meta_peek_next(meta, item_k);
+            if (wn && wn->u0 * kBN < wn->Lk) {
+              acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
+              prefetch_tile<D / 64>(p.maps, p.B, kMapK, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).pad);
+              prefetch_tile<D / 64>(p.maps, p.B, kMapV, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).pad);
+            }
+          } else {
             int nb = -1, nh = 0, nt = 0;
             if (kt + 1 < wi.u1) {
               nb = wi.b, nh = wi.h, nt = kt + 1;
@@ -656,6 +664,17 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
           const KeyUnit ku = key_unit<kWin>(p, wi, kt);
+          if (const ItemMeta* wnp = kWin ? meta_peek_next(meta, item_k) : nullptr) {
+            // the first query tiles of this CTA's next item into L2 meanwhile
+            const KeyUnit nu = key_unit<kWin>(p, *wnp, wnp->u0);
+            const int64_t nqo = wnp->qo;
+            acquire_seq_maps(p.maps, wnp->b, kMapQ, kMapDO, acq_b, true);
+            for (int r = 0; r < min(nu.count, 2); ++r) {
+              const int t = nu.first + (nu.r0 + r) % nu.n, col = (wnp->h * p.group + (nu.r0 + r) / nu.n) * D;
+              prefetch_tile<D / 64>(p.maps, p.B, kMapDO, wnp->b, nqo, t, p.total_q, col);
+              prefetch_tile<D / 64>(p.maps, p.B, kMapQ, wnp->b, nqo, t, p.total_q, col);
+            }
+          }
           if (const ItemMeta* wnp = !kWin && kt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
             // pull the first query tiles of this CTA's next item into L2 meanwhile
             const ItemMeta& wn = *wnp;
@@ -857,9 +876,32 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         if (!mbar_wait(&st_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 20);
+        const int i0 = qt * kBM + 64 * w;  // local query index of column 0 of this half
+        if (kWin && D == 64) {
+          // the warp's 32 keys against these 64 queries: none sees any -> nothing to compute (d = 64:
+          // 130 -> 127 us on the ragged step; at d = 128 the products set the pace, 334 -> 338 us)
+          const int j0 = j - lane, w_hi = sink ? Lq : j0 + 31 - diag + p.win.window - 1;  // last query that may see one
+          if (i0 + 63 < j0 - diag || i0 > w_hi || i0 >= Lq ||
+              quarter * 32 >= (sink ? meta_win(it).ns : Lk - kt * kBN)) {
+            uint32_t z[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) z[c] = 0u;
+            tmem_st32(tPT, z);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&p_full);
+            if (!mbar_wait(&dpt_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+            ++tile_n;
+            tc_fence_after();
+            tmem_st32(tDST, z);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ds_full);
+            continue;
+          }
+        }
         float x[64];
         ld_cols64(tS, x);
-        const int i0 = qt * kBM + 64 * w;  // local query index of column 0 of this half
         if (kJBias) {
           uint32_t jbk[32];
           jbias_col_transpose(jbk, jbw, jb_scratch + (warp - kFirstComputeWarp) * 128, j < Lk, lane);
@@ -968,7 +1010,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
       const KeyUnit ku = key_unit<kWin>(p, it, kt);
       const int count = ku.count;
       const int j = kt * kBN + row;  // local key index
-      const bool valid = j < Lk;
+      const bool valid = j < Lk && (!kWin || j >= meta_win(it).pad);
       const int heads = kWin ? p.win.H_kv : p.H;
       __nv_bfloat16* dk_row = p.g0 + ((ko + j) * heads + it.h) * int64_t(D);
       __nv_bfloat16* dv_row = p.g1 + ((ko + j) * heads + it.h) * int64_t(D);
@@ -1028,7 +1070,7 @@ __device__ __forceinline__ QueryUnit query_unit(const BwdParams& p, const ItemMe
   QueryUnit u = {0, 0, 0};
   if (kWin) {
     int e;
-    win_kv_tiles(qt, m.Lq, m.Lk, p.win.window, &u.a, &e);
+    win_kv_tiles(qt, m.Lq, meta_win(m), p.win.window, &u.a, &e);
     u.nz = win_sees_sinks(qt, m.Lq, meta_win(m)) ? 1 : 0;
     u.nkv = e - u.a + u.nz;
   } else {
@@ -1180,6 +1222,16 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
         const QueryUnit qu = query_unit<kWin>(p, wi, qt);
         const int nkv = qu.nkv;
+        if (const ItemMeta* wnp = kWin && D == 128 ? meta_peek_next(meta, item_k) : nullptr) {
+          // the first key tiles of this CTA's next item into L2 meanwhile
+          const QueryUnit nu = query_unit<kWin>(p, *wnp, wnp->u0);
+          const int pad = meta_win(*wnp).pad;
+          acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
+          for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
+            prefetch_tile<D / 64>(p.maps, p.B, kMapV, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, pad);
+            prefetch_tile<D / 64>(p.maps, p.B, kMapK, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, pad);
+          }
+        }
         if (const ItemMeta* wnp = !kWin && qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
           // pull the first key tiles of this CTA's next item into L2 meanwhile
           const ItemMeta& wn = *wnp;
@@ -1196,8 +1248,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
           const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
           const int kt = kWin ? (sink ? 0 : qu.a + jt - qu.nz) : jt;
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv);
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv);
+          const int pad = kWin && !sink ? meta_win(wi).pad : 0;
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv, kBN, pad);
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv, kBN, pad);
           const uint32_t bytes = sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes);
           if (!fill(mv, col, bytes) || !fill(mk, col, bytes)) { ok = false; break; }
         }
@@ -1409,15 +1462,35 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
         if (!mbar_wait(&s_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 20);
+        const bool sink = kWin && jt < qu.nz;
+        // local key index of column 0 of this half (sinks: behind org)
+        const int j0 = (kWin ? (sink ? -meta_win(it).org : (qu.a + jt - qu.nz) * kBN) : jt * kBN) + 64 * w;
+        const int n_real = sink ? meta_win(it).ns - 64 * w : Lk - j0;  // columns >= n_real hold no key
+        if (kWin && D == 64) {
+          // the warp's 32 queries against these 64 keys: none is seen -> nothing to compute (d = 64:
+          // 106 -> 101 us on the ragged step; no gain at d = 128)
+          const int r0 = i - lane;
+          if (r0 >= Lq || n_real <= 0 || r0 + 31 + diag < j0 || (!sink && r0 + diag - p.win.window + 1 > j0 + 63)) {
+            mbar_arrive(&s_free);
+            const uint32_t g = tile_n;
+            if (!mbar_wait(&dp_full[g & 1], (g >> 1) & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+            ++tile_n;
+            tc_fence_after();
+            uint32_t z[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) z[c] = 0u;
+            tmem_st32(tmem + lane_addr + colP(g) + 64 * w, z);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive(&ds_full[g & 1]);
+            continue;
+          }
+        }
         float x[64];
         ld_cols64(tS, x);
         tc_fence_before();
         mbar_arrive(&s_free);
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 21);
-        const bool sink = kWin && jt < qu.nz;
-        // local key index of column 0 of this half (sinks: behind org)
-        const int j0 = (kWin ? (sink ? -meta_win(it).org : (qu.a + jt - qu.nz) * kBN) : jt * kBN) + 64 * w;
-        const int n_real = sink ? meta_win(it).ns - 64 * w : Lk - j0;  // columns >= n_real hold no key
         if (kJBias) {
           jbias_apply<64>(x, jbk, sl2, kLog2e);
 #pragma unroll
@@ -1444,7 +1517,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
               if (c > lim) x[c] = -INFINITY;
           }
           if (kWin && !sink) {
-            const int clo = lim - p.win.window + 1;  // columns c < clo are behind the window
+            // columns c < clo are behind the window, or hold no key
+            const int clo = max(lim - p.win.window + 1, meta_win(it).pad - j0);
             if (clo > 0) {
 #pragma unroll
               for (int c = 0; c < 64; ++c)
@@ -2642,7 +2716,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
   for (int b = warp / per_seq; b < p.B; b += warps / per_seq) {
     const int Lq = int(p.q_off[b + 1] - p.q_off[b]);
     const int64_t ko = p.kv_off[b];
-    const WinSeq ws = win_seq(Lq, int(p.kv_off[b + 1] - ko), p.win.window, p.win.sinks);
+    const WinSeq ws = win_seq(Lq, int(p.kv_off[b + 1] - ko), p.win.window, p.win.sinks, kBN);
     const int chunks = win_sink_chunks(Lq, ws, p.group);
     const int64_t slot0 = sink_slot0(p.qpad[b] / kBM, b, p.group) * Hkv;
     const int64_t row_vecs = int64_t(Hkv) * D / 8;  // 16-byte pieces of a key row, all heads
@@ -2673,7 +2747,7 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
       dv[i] = make_uint4(pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]), pack_bf16x2(sv[4], sv[5]),
                          pack_bf16x2(sv[6], sv[7]));
     }
-    for (int64_t i = ws.ns * row_vecs + first; i < ws.org * row_vecs; i += step) {
+    for (int64_t i = ws.ns * row_vecs + first; i < (ws.org + ws.pad) * row_vecs; i += step) {
       dk[i] = make_uint4(0, 0, 0, 0);
       dv[i] = make_uint4(0, 0, 0, 0);
     }

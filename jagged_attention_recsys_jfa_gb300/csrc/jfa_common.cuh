@@ -211,7 +211,8 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
   L.row_bytes = size_t(H) * size_t(d) * 2;
   L.tail = align_up(off, 1024);
   off = L.tail + size_t(backward ? 4 : 3) * kTailRows * L.row_bytes;
-  L.cap_fwd = int64_t(H) * (total_q / (windowed ? 128 : 256) + B + 1);
+  // windowed lists: one entry per query tile (key tile, chunk of the sinks) for all heads
+  L.cap_fwd = windowed ? total_q / 128 + B + 1 : int64_t(H) * (total_q / 256 + B + 1);
   L.fwd = align_up(off, 16);
   off = L.fwd + size_t(L.cap_fwd) * sizeof(WorkItem);
   L.bias2 = align_up(off, 256);
@@ -221,12 +222,12 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
     off = L.smaps + (win.sinks > 0 ? (size_t(B) + kTailMaps) * kNumMapSlots * 128 : 0);
   }
   if (backward) {
-    L.cap_dq = int64_t(H) * (total_q / 128 + B + 1);
+    L.cap_dq = windowed ? total_q / 128 + B + 1 : int64_t(H) * (total_q / 128 + B + 1);
     L.dq = align_up(off, 16);
     off = L.dq + size_t(L.cap_dq) * sizeof(WorkItem);
     L.cap_dkv = int64_t(H) * (total_kv / 128 + B + 1);
     const int64_t chunks = windowed && win.sinks > 0 ? sink_slots(B, H, win.H_kv, total_q) : 0;
-    if (windowed) L.cap_dkv = int64_t(win.H_kv) * (total_kv / 128 + B + 1) + chunks;
+    if (windowed) L.cap_dkv = total_kv / 128 + 2 * int64_t(B) + 1 + chunks / win.H_kv;
     L.dkv = align_up(off, 16);
     off = L.dkv + size_t(L.cap_dkv) * sizeof(WorkItem);
     L.cap_fused = int64_t(H) * (B + 1);
@@ -287,28 +288,36 @@ __host__ __device__ inline void q_tiles_for_kv_tile(int t, int Lq, int Lk, bool 
 
 // ---- Sliding window with sinks.  Query i stands at p = i + Lk - Lq and sees key j iff j <= p and
 // (j > p - W or j < S).  A sequence's keys fall into two parts that no key is in both of: the
-// sinks, keys [0, ns), and the window part, keys from org = max(first query's window, ns) on,
-// which is bottom-right aligned again with Lk' = Lk - org keys: i + Lk' - Lq = p - org.  Keys in
-// between are seen by no query and never read.
+// sinks, keys [0, ns), and the window part, the keys from max(first query's window, ns) on.  Keys
+// in between are seen by no query and never read.
+// The window part's tiles are laid on a grid that starts `pad` (0 .. align - 1) empty rows before
+// its first key, so that a query tile's last position ends a key tile: it then meets
+// ceil((W + 127) / 128) tiles of 128 and not one more (16 sinks, W = 512: 5 instead of 6).  The empty
+// rows load as zeros (a box that starts in front of the map's first row) and are masked.  Counted
+// from the grid's start, key org, the part is bottom-right aligned again with Lk keys, pad included.
 struct WinSeq {
-  int ns, org, Lk;  // sinks; first key and key count of the window part
+  int ns;   // sinks
+  int org;  // key number of the grid's start (negative where the padding reaches before key 0)
+  int Lk;   // rows of the grid: pad, then the window part's keys
+  int pad;
 };
-__host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S) {
+__host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S, int align) {
   WinSeq r;
   r.ns = S < Lk ? S : Lk;
-  const int lo = Lk - Lq - W + 1;
-  r.org = lo > r.ns ? lo : r.ns;
-  r.Lk = Lk - r.org;
+  const int lo = Lk - Lq - W + 1, first = lo > r.ns ? lo : r.ns, n = Lk - first;
+  r.pad = n > 0 ? (Lq - n) & (align - 1) : 0;  // align: a power of two
+  r.org = first - r.pad;
+  r.Lk = n + r.pad;
   return r;
 }
-// Window-part key tiles of `keys` keys, [*a, *e), that query tile t visits.
-__host__ __device__ inline void win_kv_tiles(int t, int Lq, int Lk, int W, int* a, int* e, int keys = kBN) {
+// Grid tiles of `keys` keys, [*a, *e), that query tile t visits.
+__host__ __device__ inline void win_kv_tiles(int t, int Lq, const WinSeq& s, int W, int* a, int* e, int keys = kBN) {
   *a = *e = 0;
-  if (t * kBM >= Lq || Lk <= 0) return;
-  const int i0 = t * kBM, i1 = i0 + kBM - 1 < Lq - 1 ? i0 + kBM - 1 : Lq - 1, diag = Lk - Lq;
-  if (i1 + diag < 0) return;
+  if (t * kBM >= Lq || s.Lk <= 0) return;
+  const int i0 = t * kBM, i1 = i0 + kBM - 1 < Lq - 1 ? i0 + kBM - 1 : Lq - 1, diag = s.Lk - Lq;
+  if (i1 + diag < s.pad) return;
   const int lo = i0 + diag - W + 1;
-  *a = lo > 0 ? lo / keys : 0;
+  *a = (lo > s.pad ? lo : s.pad) / keys;
   *e = (i1 + diag) / keys + 1;
 }
 // Whether a row of query tile t sees a sink (i.e. stands at a position >= 0).
@@ -343,7 +352,7 @@ __host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq&
   }
   if (Lq <= 0) return u;
   // key j' is seen by queries j' - diag .. j' - diag + W - 1
-  const int diag = s.Lk - Lq, j0 = kt * kBN, j1 = j0 + kBN - 1 < s.Lk - 1 ? j0 + kBN - 1 : s.Lk - 1;
+  const int diag = s.Lk - Lq, j0 = kt * kBN > s.pad ? kt * kBN : s.pad, j1 = kt * kBN + kBN - 1 < s.Lk - 1 ? kt * kBN + kBN - 1 : s.Lk - 1;
   const int lo = j0 - diag > 0 ? j0 - diag : 0;
   const int hi = j1 - diag > Lq - W ? Lq - 1 : j1 - diag + W - 1;  // min(Lq - 1, j1 - diag + W - 1)
   if (hi < lo) return u;
@@ -363,12 +372,16 @@ struct TileMap {
   int y;
   bool tail;  // to be acquired before the load
 };
+// Windowed key tiles have `pad` empty rows in front of the first (see WinSeq): row0 is then the
+// grid's start, the maps start at the first real row (of the tile, for a tail map), and a tile with
+// empty rows is loaded from a negative coordinate.
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                            int64_t total, int rows = kBM) {
+                                            int64_t total, int rows = kBM, int pad = 0) {
   const int64_t g0 = row0 + int64_t(t) * rows;
+  const int empty = t * rows < pad ? pad - t * rows : 0;  // empty rows of this tile
   if (g0 + rows > total)
-    return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total), 0, true};
-  return {maps + size_t(b) * kNumMapSlots + slot, t * rows, false};
+    return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + empty + rows - total), -empty, true};
+  return {maps + size_t(b) * kNumMapSlots + slot, t * rows - pad, false};
 }
 
 // The same for a tile that lies wholly inside its sequence of `len` rows: the whole tensor's own
@@ -377,9 +390,9 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int 
 // partial tile goes through a map of its own.  `whole` is nullptr when row numbers need more than
 // 31 bits.
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUtensorMap* maps, int B, int slot, int b,
-                                            int64_t row0, int t, int len, int64_t total, int rows = kBM) {
-  if (whole != nullptr && (t + 1) * rows <= len) return {whole, int(row0) + t * rows, false};
-  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows);
+                                            int64_t row0, int t, int len, int64_t total, int rows = kBM, int pad = 0) {
+  if (whole != nullptr && (t + 1) * rows <= len && t * rows >= pad) return {whole, int(row0) + t * rows, false};
+  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows, pad);
   m.tail = true;  // not acquired yet
   return m;
 }
@@ -388,9 +401,9 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUte
 // its load.  Tiles whose box would reach past the tensor's last row are skipped.
 template <int kBoxes>
 __device__ __forceinline__ void prefetch_tile(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                              int64_t total, int col0) {
-  const TileMap m = tile_map(maps, B, slot, b, row0, t, total);
-  if (m.tail) return;
+                                              int64_t total, int col0, int pad = 0) {
+  const TileMap m = tile_map(maps, B, slot, b, row0, t, total, kBM, pad);
+  if (m.tail || m.y < 0) return;
 #pragma unroll
   for (int c = 0; c < kBoxes; ++c)
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m.map), "r"(col0 + c * 64),

@@ -33,6 +33,11 @@ struct PlanParams {
 
 enum ListKind { kListFwd = 0, kListDq = 1, kListDkv = 2, kListFused = 3, kListNsp = 4 };
 
+// A sequence's window part and sinks; the forward's key tiles have kWinKeys rows.
+__device__ __forceinline__ WinSeq plan_seq(const PlanParams& p, int Lq, int Lk) {
+  return win_seq(Lq, Lk, p.win.window, p.win.sinks, p.backward ? kBN : kWinKeys);
+}
+
 // Backward: a sequence whose queries fit one tile (Lq <= 128) is done by the fused pass
 // (one CTA per sequence and head, every key tile once); one of 2 .. kNspMaxTiles query
 // tiles by the non-sequence-parallel pass (one CTA per sequence and head, every tile pair
@@ -47,7 +52,7 @@ __device__ __forceinline__ int list_units(const PlanParams& p, int kind, int Lq,
   const int nk = (Lk + kBN - 1) / kBN;
   if (p.win.window > 0) {
     if (kind == kListFwd || kind == kListDq) return nq;
-    const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
+    const WinSeq s = plan_seq(p, Lq, Lk);
     return (s.Lk + kBN - 1) / kBN + win_sink_chunks(Lq, s, p.H / p.win.H_kv);
   }
   if (kind == kListFwd) return (nq + 1) / 2;
@@ -59,14 +64,14 @@ __device__ __forceinline__ int list_units(const PlanParams& p, int kind, int Lq,
 
 __device__ __forceinline__ int win_tile_cost(int t, int Lq, const WinSeq& s, int W, int keys) {
   int a, e;
-  win_kv_tiles(t, Lq, s.Lk, W, &a, &e, keys);
+  win_kv_tiles(t, Lq, s, W, &a, &e, keys);
   return e - a + (win_sees_sinks(t, Lq, s) ? 1 : 0);
 }
 
 __device__ __forceinline__ int unit_cost(const PlanParams& p, int kind, int u, int Lq, int Lk) {
   const bool causal = p.causal != 0;
   if (p.win.window > 0) {
-    const WinSeq s = win_seq(Lq, Lk, p.win.window, p.win.sinks);
+    const WinSeq s = plan_seq(p, Lq, Lk);
     if (kind == kListFwd) return win_tile_cost(u, Lq, s, p.win.window, kWinKeys);
     if (kind == kListDq) return win_tile_cost(u, Lq, s, p.win.window, kBN);
     const WinKeyUnit k = win_key_unit(u, Lq, s, p.win.window, p.H / p.win.H_kv);
@@ -180,7 +185,7 @@ __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items,
   run_end[tid] = block_scan_incl(mine, &units_total);
   __syncthreads();
   const long long n = units_total;
-  if (n * heads > cap) {  // cannot happen for valid offsets (capacities are upper bounds)
+  if (n > cap) {  // cannot happen for valid offsets (capacities are upper bounds)
     if (tid == 0) {
       atomicCAS(&reinterpret_cast<WsHeader*>(p.ws)->status, 0, int(JFA_ERR_WORKSPACE));
       *count_out = 0;
@@ -422,13 +427,15 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       const bool is_q_side = (slot == kMapQ || slot == kMapDO);
       int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
       int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
+      int pad = 0;  // empty rows in front of the first key's tile
       if (is_q_side && sink) continue;
       if (p.win.window > 0 && !is_q_side) {  // the sinks, or the window part
         const int64_t lq = p.q_off[b + 1] - p.q_off[b];
         if (lq < 0 || len < 0 || lq > (int64_t(1) << 30) || len > (int64_t(1) << 30)) continue;
-        const WinSeq ws = win_seq(int(lq), int(len), p.win.window, p.win.sinks);
-        if (!sink) row0 += ws.org;
-        len = sink ? ws.ns : ws.Lk;
+        const WinSeq ws = plan_seq(p, int(lq), int(len));
+        pad = sink ? 0 : ws.pad;
+        if (!sink) row0 += ws.org + ws.pad;
+        len = sink ? ws.ns : ws.Lk - ws.pad;
       }
       const size_t rb = maps.row_bytes[slot];
       const int rows = maps.tile_rows[slot];
@@ -440,12 +447,13 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
         base = static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb);
       } else {
         if (len <= 0 || row0 < 0 || row0 + len > total) continue;
-        const int64_t g0 = row0 + (len - 1) / rows * rows;  // first row of the sequence's last tile
+        // the sequence's last tile: its box's first row, and its first row that holds something
+        const int64_t g0 = row0 - pad + (pad + len - 1) / rows * rows, r0 = g0 > row0 ? g0 : row0;
         if (g0 + rows <= total) continue;
         const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
-        dst += size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + rows - total);
-        base = p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(g0 - (total - n)) * rb;
-        len = row0 + len - g0;
+        dst += size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(r0 + rows - total);
+        base = p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(r0 - (total - n)) * rb;
+        len = row0 + len - r0;
       }
       const uint4* src = reinterpret_cast<const uint4*>(sink ? &maps.sink_tmpl[slot - kMapK] : &maps.tmpl[slot]);
       if (lane < 8) reinterpret_cast<uint4*>(dst)[lane] = src[lane];

@@ -24,9 +24,11 @@ struct ItemMeta {
   int64_t jb;         // general jagged bias: the sequence's block offset in each head's plane
 };
 
-// With a sliding window, ko and Lk are those of the sequence's window part, and jb holds its
-// (org, sinks) instead.
-__device__ __forceinline__ WinSeq meta_win(const ItemMeta& m) { return {int(m.jb), int(m.jb >> 32), m.Lk}; }
+// With a sliding window, ko and Lk are those of the window part's grid, and jb holds the rest of
+// its WinSeq instead.
+__device__ __forceinline__ WinSeq meta_win(const ItemMeta& m) {
+  return {int(m.jb & 0xffff), int(m.jb >> 32), m.Lk, int(m.jb >> 16 & 0xffff)};
+}
 
 struct MetaRing {
   ItemMeta e[kMetaSlots];
@@ -76,10 +78,10 @@ __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items,
       m.qp = qpad ? qpad[wi.b] : 0;
       m.jb = jb_off ? jb_off[wi.b] : 0;
       if (kWin) {
-        const WinSeq ws = win_seq(m.Lq, m.Lk, window, sinks);
+        const WinSeq ws = win_seq(m.Lq, m.Lk, window, sinks, kBN);
         m.ko += ws.org;
         m.Lk = ws.Lk;
-        m.jb = (int64_t(ws.org) << 32) | int64_t(ws.ns);
+        m.jb = int64_t((uint64_t(uint32_t(ws.org)) << 32) | uint32_t(ws.pad << 16 | ws.ns));
       }
     } else {
       m = ItemMeta{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};

@@ -88,9 +88,9 @@ struct WinTile {
   int b, h, t;          // sequence (-1: no more items), query head, query tile
   int nz, a, n;
   int rows;             // rows of the tile that are queries
-  int pos;              // position of its first row, counted from the window part's first key
-  int Lq, Lk, org, ns;  // as in ItemMeta and WinSeq
-  int64_t qo, ko;       // first query row of the sequence, first key row of its window part
+  int pos;              // position of its first row, counted from the grid's start
+  int Lq, Lk, org, ns, pad;  // as in WinSeq
+  int64_t qo, ko;       // first query row of the sequence, first row of its window part's grid
 };
 struct TileRing {
   WinTile e[kMetaSlots];
@@ -117,13 +117,14 @@ __device__ __forceinline__ bool publish_tiles(TileRing& r, const WinFwdParams& p
       w.qo = p.q_off[wi.b];
       w.ko = p.kv_off[wi.b];
       w.Lq = int(p.q_off[wi.b + 1] - w.qo);
-      const WinSeq ws = win_seq(w.Lq, int(p.kv_off[wi.b + 1] - w.ko), p.win.window, p.win.sinks);
+      const WinSeq ws = win_seq(w.Lq, int(p.kv_off[wi.b + 1] - w.ko), p.win.window, p.win.sinks, kWinKeys);
       w.ko += ws.org;
       w.Lk = ws.Lk;
       w.org = ws.org;
       w.ns = ws.ns;
+      w.pad = ws.pad;
       int e;
-      win_kv_tiles(w.t, w.Lq, w.Lk, p.win.window, &w.a, &e, kWinKeys);
+      win_kv_tiles(w.t, w.Lq, ws, p.win.window, &w.a, &e, kWinKeys);
       w.nz = win_sees_sinks(w.t, w.Lq, ws) ? (ws.ns + kWinKeys - 1) / kWinKeys : 0;
       w.n = w.nz + e - w.a;
       w.rows = min(kBM, w.Lq - w.t * kBM);
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           const TileMap m =
               sink ? tile_map(nullptr, p.smaps, p.B, slot, w.b, w.ko - w.org, j, w.ns, p.total_kv, kWinKeys)
                    : tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, w.b, w.ko, w.a + j - w.nz, w.Lk,
-                              p.total_kv, kWinKeys);
+                              p.total_kv, kWinKeys, w.pad);
           if (m.tail) tmap_acquire(m.map);
           if (!mbar_wait(&empty[r.e], r.ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
           trace_event(p.trace, kTraceProducer, tn, slot);
@@ -410,8 +411,8 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       const int64_t q_row = w.qo + w.t * kBM + i;
       __nv_bfloat16* orow = p.out + (q_row * p.H + w.h) * int64_t(D);
       float* lrow = p.lse + int64_t(w.h) * p.total_q + q_row;
-      int hi0 = r0 + w.pos + w.org, last = ns - 1, lo0 = -(1 << 30);  // first step of sinks
-      const int hi_win = r0 + w.pos - w.a * kWinKeys;                  // first key tile of the window part
+      int hi0 = r0 + w.pos + w.org, last = ns - 1, lo0 = -(1 << 30), pad = 0;     // first step of sinks
+      const int hi_win = r0 + w.pos - w.a * kWinKeys, pad_win = w.pad - w.a * kWinKeys;  // first tile of the window part
       tile_release_warp(tiles, k);  // the rest is in registers
       if (n == 0) {
         if (valid) {
@@ -430,9 +431,10 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           hi0 = hi_win;
           last = 1 << 30;
           lo0 = hi0 - p.win.window + 1;
+          pad = pad_win;  // columns before it hold no key
         }
-        const bool hidden = min(last, hi0 + 31) < 0 || lo0 >= kWinKeys || r0 >= rows;  // from all 32 rows
-        const bool whole = min(last, hi0) >= kWinKeys - 1 && lo0 <= -31;             // seen by all 32
+        const bool hidden = min(last, hi0 + 31) < 0 || lo0 >= kWinKeys || r0 >= rows;      // from all 32 rows
+        const bool whole = min(last, hi0) >= kWinKeys - 1 && lo0 <= -31 && pad <= 0;  // seen by all 32
         const uint32_t tS = tmem + lane_addr + C::kColS + sr.e * kWinKeys;
         if (!warp_wait(&s_full[sr.e], sr.ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
             for (int c = 0; c < 64; ++c) x[c] = __uint_as_float(r[c >> 5][c & 31]);
           }
           if (!whole) {
-            const int chi = min(last, hi0 + lane), clo = lo0 + lane;
+            const int chi = min(last, hi0 + lane), clo = max(lo0 + lane, pad);
             const uint32_t bits[2] = {low_bits(chi + 1) & ~low_bits(clo), low_bits(chi - 31) & ~low_bits(clo - 32)};
 #pragma unroll
             for (int c = 0; c < 64; ++c)
@@ -513,6 +515,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
         sr.next();
         hi0 -= kWinKeys;
         lo0 -= kWinKeys;
+        pad -= kWinKeys;
         last -= kWinKeys;
       }
       if (!ok) break;
