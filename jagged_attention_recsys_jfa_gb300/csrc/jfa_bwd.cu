@@ -590,9 +590,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
           const bool sink = kWin && ku.chunk >= 0;
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
           const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
-          const int pad = kWin && !sink ? meta_win(wi).pad : 0;
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, pad);
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, pad);
+          const int skip = kWin && !sink ? meta_win(wi).skip : 0;
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
           if (mk.tail) {
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
@@ -609,8 +609,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
             const ItemMeta* wn = meta_peek_next(meta, item_k);
             if (wn && wn->u0 * kBN < wn->Lk) {
               acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapK, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).pad);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapV, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).pad);
+              prefetch_tile<D / 64>(p.maps, p.B, kMapK, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
+              prefetch_tile<D / 64>(p.maps, p.B, kMapV, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
             }
           } else {
             int nb = -1, nh = 0, nt = 0;
@@ -1225,11 +1225,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
         if (const ItemMeta* wnp = kWin && D == 128 ? meta_peek_next(meta, item_k) : nullptr) {
           // the first key tiles of this CTA's next item into L2 meanwhile
           const QueryUnit nu = query_unit<kWin>(p, *wnp, wnp->u0);
-          const int pad = meta_win(*wnp).pad;
+          const int skip = meta_win(*wnp).skip;
           acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
           for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
-            prefetch_tile<D / 64>(p.maps, p.B, kMapV, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, pad);
-            prefetch_tile<D / 64>(p.maps, p.B, kMapK, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, pad);
+            prefetch_tile<D / 64>(p.maps, p.B, kMapV, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
+            prefetch_tile<D / 64>(p.maps, p.B, kMapK, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
           }
         }
         if (const ItemMeta* wnp = !kWin && qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
@@ -1248,9 +1248,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
           const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
           const int kt = kWin ? (sink ? 0 : qu.a + jt - qu.nz) : jt;
-          const int pad = kWin && !sink ? meta_win(wi).pad : 0;
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv, kBN, pad);
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv, kBN, pad);
+          const int skip = kWin && !sink ? meta_win(wi).skip : 0;
+          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv, kBN, skip);
+          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv, kBN, skip);
           const uint32_t bytes = sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes);
           if (!fill(mv, col, bytes) || !fill(mk, col, bytes)) { ok = false; break; }
         }

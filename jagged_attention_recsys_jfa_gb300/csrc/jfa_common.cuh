@@ -293,13 +293,15 @@ __host__ __device__ inline void q_tiles_for_kv_tile(int t, int Lq, int Lk, bool 
 // The window part's tiles are laid on a grid that starts `pad` (0 .. align - 1) empty rows before
 // its first key, so that a query tile's last position ends a key tile: it then meets
 // ceil((W + 127) / 128) tiles of 128 and not one more (16 sinks, W = 512: 5 instead of 6).  The empty
-// rows load as zeros (a box that starts in front of the map's first row) and are masked.  Counted
-// from the grid's start, key org, the part is bottom-right aligned again with Lk keys, pad included.
+// rows are masked.  They load as what they are where they are the sequence's own sinks, else as zeros
+// (`skip` rows: a box that starts in front of the map's first row).  Counted from the grid's start,
+// key org, the part is bottom-right aligned again with Lk keys, pad included.
 struct WinSeq {
   int ns;   // sinks
   int org;  // key number of the grid's start (negative where the padding reaches before key 0)
   int Lk;   // rows of the grid: pad, then the window part's keys
   int pad;
+  int skip;  // 0, or pad
 };
 __host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S, int align) {
   WinSeq r;
@@ -308,6 +310,7 @@ __host__ __device__ inline WinSeq win_seq(int Lq, int Lk, int W, int S, int alig
   r.pad = n > 0 ? (Lq - n) & (align - 1) : 0;  // align: a power of two
   r.org = first - r.pad;
   r.Lk = n + r.pad;
+  r.skip = r.org >= 0 && first == r.ns ? 0 : r.pad;
   return r;
 }
 // Grid tiles of `keys` keys, [*a, *e), that query tile t visits.
@@ -372,16 +375,16 @@ struct TileMap {
   int y;
   bool tail;  // to be acquired before the load
 };
-// Windowed key tiles have `pad` empty rows in front of the first (see WinSeq): row0 is then the
+// Windowed key tiles may have `skip` empty rows in front of the first (see WinSeq): row0 is then the
 // grid's start, the maps start at the first real row (of the tile, for a tail map), and a tile with
 // empty rows is loaded from a negative coordinate.
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                            int64_t total, int rows = kBM, int pad = 0) {
+                                            int64_t total, int rows = kBM, int skip = 0) {
   const int64_t g0 = row0 + int64_t(t) * rows;
-  const int empty = t * rows < pad ? pad - t * rows : 0;  // empty rows of this tile
+  const int empty = t * rows < skip ? skip - t * rows : 0;  // empty rows of this tile
   if (g0 + rows > total)
     return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + empty + rows - total), -empty, true};
-  return {maps + size_t(b) * kNumMapSlots + slot, t * rows - pad, false};
+  return {maps + size_t(b) * kNumMapSlots + slot, t * rows - skip, false};
 }
 
 // The same for a tile that lies wholly inside its sequence of `len` rows: the whole tensor's own
@@ -390,9 +393,9 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int 
 // partial tile goes through a map of its own.  `whole` is nullptr when row numbers need more than
 // 31 bits.
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUtensorMap* maps, int B, int slot, int b,
-                                            int64_t row0, int t, int len, int64_t total, int rows = kBM, int pad = 0) {
-  if (whole != nullptr && (t + 1) * rows <= len && t * rows >= pad) return {whole, int(row0) + t * rows, false};
-  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows, pad);
+                                            int64_t row0, int t, int len, int64_t total, int rows = kBM, int skip = 0) {
+  if (whole != nullptr && (t + 1) * rows <= len && t * rows >= skip) return {whole, int(row0) + t * rows, false};
+  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows, skip);
   m.tail = true;  // not acquired yet
   return m;
 }
@@ -401,8 +404,8 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUte
 // its load.  Tiles whose box would reach past the tensor's last row are skipped.
 template <int kBoxes>
 __device__ __forceinline__ void prefetch_tile(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                              int64_t total, int col0, int pad = 0) {
-  const TileMap m = tile_map(maps, B, slot, b, row0, t, total, kBM, pad);
+                                              int64_t total, int col0, int skip = 0) {
+  const TileMap m = tile_map(maps, B, slot, b, row0, t, total, kBM, skip);
   if (m.tail || m.y < 0) return;
 #pragma unroll
   for (int c = 0; c < kBoxes; ++c)

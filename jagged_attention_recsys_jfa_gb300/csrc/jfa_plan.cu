@@ -427,15 +427,15 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       const bool is_q_side = (slot == kMapQ || slot == kMapDO);
       int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
       int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
-      int pad = 0;  // empty rows in front of the first key's tile
+      int skip = 0;  // empty rows in front of the first key's tile
       if (is_q_side && sink) continue;
       if (p.win.window > 0 && !is_q_side) {  // the sinks, or the window part
         const int64_t lq = p.q_off[b + 1] - p.q_off[b];
         if (lq < 0 || len < 0 || lq > (int64_t(1) << 30) || len > (int64_t(1) << 30)) continue;
         const WinSeq ws = plan_seq(p, int(lq), int(len));
-        pad = sink ? 0 : ws.pad;
-        if (!sink) row0 += ws.org + ws.pad;
-        len = sink ? ws.ns : ws.Lk - ws.pad;
+        skip = sink ? 0 : ws.skip;
+        if (!sink) row0 += ws.org + ws.skip;
+        len = sink ? ws.ns : ws.Lk - ws.skip;
       }
       const size_t rb = maps.row_bytes[slot];
       const int rows = maps.tile_rows[slot];
@@ -448,7 +448,7 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       } else {
         if (len <= 0 || row0 < 0 || row0 + len > total) continue;
         // the sequence's last tile: its box's first row, and its first row that holds something
-        const int64_t g0 = row0 - pad + (pad + len - 1) / rows * rows, r0 = g0 > row0 ? g0 : row0;
+        const int64_t g0 = row0 - skip + (skip + len - 1) / rows * rows, r0 = g0 > row0 ? g0 : row0;
         if (g0 + rows <= total) continue;
         const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
         dst += size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(r0 + rows - total);

@@ -27,7 +27,7 @@ struct ItemMeta {
 // With a sliding window, ko and Lk are those of the window part's grid, and jb holds the rest of
 // its WinSeq instead.
 __device__ __forceinline__ WinSeq meta_win(const ItemMeta& m) {
-  return {int(m.jb & 0xffff), int(m.jb >> 32), m.Lk, int(m.jb >> 16 & 0xffff)};
+  return {int(m.jb & 0xff), int(m.jb >> 32), m.Lk, int(m.jb >> 8 & 0xff), int(m.jb >> 16 & 0xff)};
 }
 
 struct MetaRing {
@@ -81,7 +81,7 @@ __device__ __forceinline__ bool meta_publish(MetaRing& r, const WorkItem* items,
         const WinSeq ws = win_seq(m.Lq, m.Lk, window, sinks, kBN);
         m.ko += ws.org;
         m.Lk = ws.Lk;
-        m.jb = int64_t((uint64_t(uint32_t(ws.org)) << 32) | uint32_t(ws.pad << 16 | ws.ns));
+        m.jb = int64_t((uint64_t(uint32_t(ws.org)) << 32) | uint32_t(ws.skip << 16 | ws.pad << 8 | ws.ns));
       }
     } else {
       m = ItemMeta{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};

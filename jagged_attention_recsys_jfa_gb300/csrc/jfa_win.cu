@@ -89,7 +89,7 @@ struct WinTile {
   int nz, a, n;
   int rows;             // rows of the tile that are queries
   int pos;              // position of its first row, counted from the grid's start
-  int Lq, Lk, org, ns, pad;  // as in WinSeq
+  int Lq, Lk, org, ns, pad, skip;  // as in WinSeq
   int64_t qo, ko;       // first query row of the sequence, first row of its window part's grid
 };
 struct TileRing {
@@ -123,6 +123,7 @@ __device__ __forceinline__ bool publish_tiles(TileRing& r, const WinFwdParams& p
       w.org = ws.org;
       w.ns = ws.ns;
       w.pad = ws.pad;
+      w.skip = ws.skip;
       int e;
       win_kv_tiles(w.t, w.Lq, ws, p.win.window, &w.a, &e, kWinKeys);
       w.nz = win_sees_sinks(w.t, w.Lq, ws) ? (ws.ns + kWinKeys - 1) / kWinKeys : 0;
@@ -256,7 +257,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           const TileMap m =
               sink ? tile_map(nullptr, p.smaps, p.B, slot, w.b, w.ko - w.org, j, w.ns, p.total_kv, kWinKeys)
                    : tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, w.b, w.ko, w.a + j - w.nz, w.Lk,
-                              p.total_kv, kWinKeys, w.pad);
+                              p.total_kv, kWinKeys, w.skip);
           if (m.tail) tmap_acquire(m.map);
           if (!mbar_wait(&empty[r.e], r.ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
           trace_event(p.trace, kTraceProducer, tn, slot);
