@@ -192,8 +192,11 @@ typedef struct {
   int B;
 } jfa_cache;
 
-/* Bytes of workspace the two calls below need (256-byte aligned, zero before its first use;
- * every call leaves what it needs zero, zero again).  Returns 0 on invalid sizes. */
+/* Bytes of workspace jfa_cache_attention needs (jfa_cache_append needs the first 256 of them);
+ * 256-byte aligned, zero before its first use, every call leaves what it needs zero, zero again.
+ * One workspace serves both calls, at any sizes that it is large enough for, but only one call
+ * at a time.  Zero it again after a JFA_ERR_TIMEOUT, and before it serves these calls when other
+ * calls of this library have used it.  Returns 0 on invalid sizes. */
 size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
 
 /* Append new tokens, keys rotated by their position on the way.  Sequence b's new tokens are

@@ -480,7 +480,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
 
 size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d) {
   if (B < 1 || H_kv < 1 || H < H_kv || H > 4096 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
-  return cache_workspace_bytes(B, H, H_kv, d);
+  return cache_workspace_bytes(B, H, H_kv);
 }
 
 jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -534,7 +534,7 @@ jfa_status jfa_cache_attention(const jfa_cache* cache, const void* q, int H, int
   if (H < cache->H_kv || H > 4096 || H % cache->H_kv != 0 || window < 1 || sinks < 0) return JFA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !(scale < 3.0e38f)) return JFA_ERR_INVALID_ARG;
   if (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse)) return JFA_ERR_INVALID_ARG;
-  if ((st = check_workspace_bytes(workspace, workspace_bytes, cache_workspace_bytes(cache->B, H, cache->H_kv, cache->d))) !=
+  if ((st = check_workspace_bytes(workspace, workspace_bytes, cache_workspace_bytes(cache->B, H, cache->H_kv))) !=
       JFA_OK)
     return st;
   const int nsm = sm_count();

@@ -658,18 +658,12 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
 
 constexpr int kMaxAttnCtas = 512;  // bounds the partial rows in the workspace
 
-struct CacheWs {
-  size_t arrived, partial, total;
-};
-CacheWs cache_layout(int B, int H, int Hkv, int d) {
-  CacheWs L;
-  const int G = H / Hkv, rows = G < 16 ? G : 16;
-  const int64_t units = int64_t(B) * Hkv * ((G + 15) / 16);
-  L.arrived = sizeof(WsHeader);
-  L.partial = align_up(L.arrived + size_t(units) * 4, 256);
-  L.total = align_up(L.partial + size_t(2) * kMaxAttnCtas * rows * (d + 2) * 4, 256);
-  return L;
-}
+// The workspace behind its header: the partial rows, then the units' counters.  The counters start
+// at the same place for every call, behind the most partial rows that any call writes: calls of
+// different sizes may share a workspace, and one call's partial rows must not be found where
+// another expects its counters at zero.
+constexpr size_t kPartialAt = sizeof(WsHeader);
+constexpr size_t kArrivedAt = kPartialAt + size_t(2) * kMaxAttnCtas * 16 * (128 + 2) * sizeof(float);
 
 template <int D>
 cudaError_t launch_attn_t(const CUtensorMap& km, const CUtensorMap& vm, const CacheAttnParams& p, int num_sms,
@@ -685,7 +679,10 @@ cudaError_t launch_attn_t(const CUtensorMap& km, const CUtensorMap& vm, const Ca
 
 }  // namespace
 
-size_t cache_workspace_bytes(int B, int H, int Hkv, int d) { return cache_layout(B, H, Hkv, d).total; }
+size_t cache_workspace_bytes(int B, int H, int Hkv) {
+  const int64_t units = int64_t(B) * Hkv * ((H / Hkv + 15) / 16);
+  return align_up(kArrivedAt + size_t(units) * sizeof(unsigned), 256);
+}
 
 cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* ws, int num_sms, cudaStream_t stream) {
   AppendParams p;
@@ -729,7 +726,6 @@ cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* 
 cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& km, const CUtensorMap& vm, const void* q, int H,
                                    int window, int sinks, float scale, void* out, float* lse, void* ws, int num_sms,
                                    cudaStream_t stream) {
-  const CacheWs L = cache_layout(c.B, H, c.H_kv, c.d);
   uint8_t* w = static_cast<uint8_t*>(ws);
   CacheAttnParams p;
   p.q = static_cast<const __nv_bfloat16*>(q);
@@ -750,8 +746,8 @@ cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& km, co
   p.sinks = sinks;
   p.scale_log2 = scale * kLog2e;
   p.status = &reinterpret_cast<WsHeader*>(w)->status;
-  p.arrived = reinterpret_cast<unsigned*>(w + L.arrived);
-  p.partial = reinterpret_cast<float*>(w + L.partial);
+  p.arrived = reinterpret_cast<unsigned*>(w + kArrivedAt);
+  p.partial = reinterpret_cast<float*>(w + kPartialAt);
   return c.d == 128 ? launch_attn_t<128>(km, vm, p, num_sms, stream) : launch_attn_t<64>(km, vm, p, num_sms, stream);
 }
 

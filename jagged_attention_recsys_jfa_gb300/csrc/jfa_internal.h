@@ -117,7 +117,7 @@ struct CacheAppend {
   int rot, interleaved;
   uint64_t turn[64];  // angle per position of each rotated pair, in 2^-64 turns
 };
-size_t cache_workspace_bytes(int B, int H, int Hkv, int d);
+size_t cache_workspace_bytes(int B, int H, int Hkv);
 cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* ws, int num_sms, cudaStream_t stream);
 cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& k_map, const CUtensorMap& v_map, const void* q,
                                    int H, int window, int sinks, float scale, void* out, float* lse, void* ws,

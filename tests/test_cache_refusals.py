@@ -84,6 +84,8 @@ def test_workspace_size():
     assert f(0, 4, 2, 64) == 0 and f(2, 3, 2, 64) == 0 and f(2, 4, 2, 80) == 0 and f(2, 1, 2, 64) == 0
     assert f(2, 4, 2, 64) > 256 and f(2, 4, 2, 64) % 256 == 0
     assert f(100000, 64, 2, 128) > f(2, 64, 2, 128)
+    # calls of different sizes share a workspace, so only the number of units makes it larger
+    assert f(7, 16, 4, 64) == f(7, 4, 4, 128)
     with pytest.raises(ValueError):
         jfa.new_cache_workspace(2, 3, 2, 64, "cpu")
 

@@ -114,10 +114,39 @@ def test_attention_splits_long_sequences(lens):
     q = normal(g, len(lens), 4, 128)
     ws = jfa.new_cache_workspace(len(lens), 4, 2, 128, DEV)
     a = check_attention(q, k, v, table, n, None, 0, workspace=ws)
-    assert int(ws[256:256 + 4 * len(lens) * 2].view(torch.int32).abs().sum()) == 0  # counters left at zero
+    at = ws.numel() - -(-len(lens) * 2 * 4 // 256) * 256  # the counters are the workspace's last part
+    assert int(ws[at:].view(torch.int32).abs().sum()) == 0  # left at zero
     for _ in range(3):  # the order of the joins is fixed: the same bits every time
         b = jfa.jfa_cache_attention(q, k, v, table, n, workspace=ws)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_one_workspace_for_calls_of_different_sizes():
+    """A workspace made for the largest call serves the others in between: what one call leaves
+    behind is never where another expects its counters at zero."""
+    g = gen(13)
+    ws = jfa.new_cache_workspace(900, 16, 2, 128, DEV)
+    r = np.random.RandomState(1)
+    sizes = [([20000], 16, 1, 128), ([int(x) for x in r.randint(100, 900, 900)], 2, 2, 64),
+             ([9000, 5], 3, 1, 64), ([30000], 34, 2, 64)]
+    calls = []
+    for lens, H, G, d in sizes:
+        k, v, table, n = filled(g, lens, G, d, 64)
+        q = normal(g, len(lens), H, d)
+        calls.append((q, k, v, table, n))
+    alone = [jfa.jfa_cache_attention(*c)[:2] for c in calls]
+    for i in (0, 1, 0, 2, 3, 1, 2, 0):
+        out, lse, _ = jfa.jfa_cache_attention(*calls[i], workspace=ws)
+        assert torch.equal(out, alone[i][0]) and torch.equal(lse, alone[i][1])
+    check_attention(*calls[1], None, 0, workspace=ws)
+    # an append in between, its lengths among the results
+    rows = normal(g, 900, 2, 64)
+    k, v, table, n = make_cache(g, [1] * 900, 2, 64, 16) + (torch.zeros(900, dtype=torch.int32, device=DEV),)
+    jfa.jfa_cache_append(rows, rows, torch.arange(901, device=DEV), k, v, table, n, lengths_out=n, workspace=ws)
+    assert bool((n == 1).all())
+    out, lse, _ = jfa.jfa_cache_attention(*calls[3], workspace=ws)
+    assert torch.equal(out, alone[3][0]) and torch.equal(lse, alone[3][1])
+    assert jfa.jfa_check_status(ws) == 0
 
 
 def test_attention_of_many_sequences():
