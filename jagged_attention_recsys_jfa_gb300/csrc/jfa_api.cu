@@ -419,7 +419,7 @@ jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const
   if ((st = window_maps(&maps, pr, q, k, v, nullptr, false)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);
-    JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, false, nsm, s), "planner launch");
+    JFA_CHECK_LAUNCH(launch_win_plan(pr, maps, workspace, L, false, nsm, s), "planner launch");
   }
   {
     KernelTimer t(JFA_KERNEL_FORWARD, s);
@@ -456,7 +456,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   if ((st = window_maps(&maps, pr, q, k, v, dout, true)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);
-    JFA_CHECK_LAUNCH(launch_plan(pr, maps, workspace, L, true, nsm, s), "planner launch");
+    JFA_CHECK_LAUNCH(launch_win_plan(pr, maps, workspace, L, true, nsm, s), "planner launch");
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_PREPROCESS, s);
@@ -464,15 +464,15 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_DKDV, s);
-    JFA_CHECK_LAUNCH(launch_bwd_dkdv(pr, lse, workspace, L, dk, dv, nsm, s), "dK/dV launch");
+    JFA_CHECK_LAUNCH(launch_win_dkdv(pr, workspace, L, dk, dv, nsm, s), "dK/dV launch");
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_DQ, s);
-    JFA_CHECK_LAUNCH(launch_bwd_dq(pr, lse, workspace, L, dq, nsm, s), "dQ launch");
+    JFA_CHECK_LAUNCH(launch_win_dq(pr, workspace, L, dq, nsm, s), "dQ launch");
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_JOIN, s);
-    JFA_CHECK_LAUNCH(launch_bwd_join(pr, workspace, L, dk, dv, nsm, s), "sink gradient launch");
+    JFA_CHECK_LAUNCH(launch_win_join(pr, workspace, L, dk, dv, nsm, s), "sink gradient launch");
   }
   g_last_launches = 5;
   return JFA_OK;

@@ -25,22 +25,13 @@
 // accumulators from 256.  P and dS are written back as bf16 (over the S / dP columns the
 // warpgroup owns at d = 128, in the free columns from 384 at d = 64 in the dK/dV pass) and
 // feed the accumulating MMAs straight from TMEM.
-#include <cuda_bf16.h>
-
-#include "jfa_internal.h"
-#include "sm100_ptx.cuh"
-#include "jfa_sched.cuh"
+#include "jfa_bwd.cuh"
 
 namespace jfa {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr uint32_t kRegsLoad = 104, kRegsCompute = 200;
 static_assert(reg_split_fits(kRegsLoad, kRegsCompute), "register split exceeds the launch allocation");
-// dK/dV pass (512 threads): role warps, compute warpgroups, epilogue warpgroup
-constexpr uint32_t kRegsLoadDkdv = 96, kRegsComputeDkdv = 168, kRegsEpiDkdv = 72;
-static_assert(reg_split_fits_dkdv(kRegsLoadDkdv, kRegsComputeDkdv, kRegsEpiDkdv),
-              "register split exceeds the launch allocation");
 // the non-sequence-parallel pass: the epilogue warps also sum and finish the dQ rows
 constexpr uint32_t kRegsLoadNsp = 104, kRegsComputeNsp = 160, kRegsEpiNsp = 88;
 static_assert(reg_split_fits_dkdv(kRegsLoadNsp, kRegsComputeNsp, kRegsEpiNsp),
@@ -49,51 +40,6 @@ static_assert(reg_split_fits_dkdv(kRegsLoadNsp, kRegsComputeNsp, kRegsEpiNsp),
 constexpr uint32_t kRegsLoadFused = 112, kRegsComputeFused = 168, kRegsEpiFused = 64;
 static_assert(reg_split_fits_dkdv(kRegsLoadFused, kRegsComputeFused, kRegsEpiFused),
               "register split exceeds the launch allocation");
-
-struct BwdParams {
-  const int64_t* q_off;
-  const int64_t* kv_off;
-  int B, H;
-  int64_t total_q, total_kv;
-  float scale, scale_log2;
-  int causal;
-  const float* bias2;  // [H][num_buckets] bias * log2(e), or nullptr
-  float* bias_grad;    // [H][num_buckets] gradient of the bias table (cleared by the planner), or nullptr
-  int num_buckets, center;
-  const __nv_bfloat16* jbias;  // general jagged bias [H][jb_plane], or nullptr
-  const int64_t* jb_off;       // its block offsets [B+1]
-  int64_t jb_plane;
-  __nv_bfloat16* jb_grad;      // its gradient (dK/dV and fused passes), or nullptr
-  const CUtensorMap* maps;
-  const WorkItem* items;
-  const int* n_items;
-  int* claim;  // the list's claim counter (zeroed by the planner)
-  int* status;
-  const uint64_t* wait_ns;  // the planner's item hand-off wait limit for this launch (ns)
-  const float* lse2;    // [H][qpad_cap]  -lse * log2(e), padded per sequence to 128 rows
-  const float* delta;   // [H][qpad_cap]  -D, same layout
-  const int64_t* qpad;  // [B+1] sequence offsets in the padded vectors
-  int64_t qpad_cap;
-  __nv_bfloat16* g0;   // dK (dK/dV and fused passes) or dQ (dQ pass)
-  __nv_bfloat16* g1;   // dV (dK/dV and fused passes)
-  __nv_bfloat16* g2;   // dQ (fused and non-sequence-parallel passes)
-  float* dqacc;        // non-sequence-parallel pass: fp32 dQ sums [total_q][H][D]
-  TraceBuf trace;
-  WindowSpec win;            // sliding window with sinks (the kWin kernels)
-  int group;                 // query heads per key/value head
-  const CUtensorMap* smaps;  // the sinks' K / V maps
-  int sink_rows;             // rows of their boxes
-  float* spart;              // partial dK, dV of the sinks (dK/dV pass): [slot][2][sinks][D]
-};
-
-__device__ __forceinline__ void raise_status(int* status, int code) { atomicCAS(status, 0, code); }
-
-__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = globaltimer_ns();
-  while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer_ns() - t0 > kWaitTimeoutNs) return;
-  }
-}
 
 // ---------------------------------------------------------------- preprocess
 // For every query row of the 128-row-padded per-query vectors (every sequence's rows,
@@ -115,7 +61,6 @@ struct PreParams {
   int64_t total_q;
   const WorkItem* items;      // dQ list: units are query tiles
   const int* n_items;
-  bool all_heads;             // its entries stand for all heads (window)
   const WorkItem* items2;     // fused list: the sequence's one query tile
   const int* n_items2;
   const WorkItem* items3;     // non-sequence-parallel list: all of the sequence's query tiles
@@ -130,7 +75,8 @@ struct PreParams {
   float* delta;
 };
 
-template <int D>
+// kAllHeads (windowed lists): an entry of the dQ list stands for all heads.
+template <int D, bool kAllHeads>
 __global__ void __launch_bounds__(256) preprocess_items_kernel(const PreParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
@@ -138,9 +84,9 @@ __global__ void __launch_bounds__(256) preprocess_items_kernel(const PreParams p
   const int n1 = *p.n_items, n2 = *p.n_items2, n3 = *p.n_items3;
   for (int idx = blockIdx.x; idx < n1 + n2 + n3; idx += gridDim.x) {
     const bool whole = idx >= n1;  // fused or non-sequence-parallel: every query tile of the sequence
-    WorkItem it = idx < n1 ? p.items[p.all_heads ? idx / p.H : idx]
+    WorkItem it = idx < n1 ? p.items[kAllHeads ? idx / p.H : idx]
                            : idx < n1 + n2 ? p.items2[idx - n1] : p.items3[idx - n1 - n2];
-    if (p.all_heads) it.h = idx % p.H;
+    if (kAllHeads) it.h = idx % p.H;
     const int64_t qo = p.q_off[it.b];
     const int Lq = int(p.q_off[it.b + 1] - qo);
     const int64_t pad0 = int64_t(it.h) * p.qpad_cap + p.qpad[it.b];
@@ -253,70 +199,6 @@ __global__ void __launch_bounds__(256, 4) preprocess_kernel(const PreParams p) {
   }
 }
 
-template <int D>
-struct BwdCfg {
-  static constexpr int kTileBytes = 128 * D * 2;
-  static constexpr int kRingDkdv = D == 128 ? 4 : 8;  // single-tile ring entries
-  static constexpr int kRingDq = D == 128 ? 5 : 8;
-  static constexpr int kVecSlots = 4;                  // dK/dV: per-query-tile lse2 / D vectors
-  // dK/dV pass: S^T, dP^T, dK, dV.   dQ pass: S, dP (two buffers), dQ.
-  static constexpr uint32_t kColS = 0, kColP = 128, kColA0 = 256, kColA1 = 256 + D;
-  static constexpr uint32_t kColP1 = 256, kColDQ = 384;
-  // dK/dV pass: P^T and dS^T (bf16, keys x 128 queries, each compute warpgroup's 64 queries
-  // in 32 columns) over S^T / dP^T at d = 128, two 64-column halves apart; at d = 64 in the
-  // spare columns [384, 448) and [448, 512), so the next S^T / dP^T MMA does not write the
-  // columns the previous dV / dK MMA is still reading
-  static constexpr uint32_t kColPT = D == 64 ? 384 : kColS, kColDST = D == 64 ? 448 : kColP;
-  static constexpr uint32_t kXHalf = D == 64 ? 32 : 64;
-  // dQ pass at d = 64: the query tile's Q and dO rows copied into the free columns
-  // [448, 480) and [480, 512) by the compute warpgroups feed the S and dP MMAs from TMEM, and
-  // the shared-memory buffers are free for the next query tile once both copies are done
-  static constexpr bool kDqQTmem = D == 64;
-  static constexpr uint32_t kColDqQ = 448, kColDqDO = 480;
-  static constexpr int kSmemDkdv = 2 * kTileBytes + kRingDkdv * kTileBytes + kVecSlots * 1024 + 1024;
-  static constexpr int kSmemDq = 2 * kTileBytes + kRingDq * kTileBytes + 1024;
-  // Fused short-query pass: Q and dO resident, K/V ring, dS^T staging (keys x 128 queries,
-  // bf16), lse2 / D vectors.  TMEM: S^T [0,128), dP^T then dK [128,256), dV, dQ.
-  static constexpr int kRingFused = D == 128 ? 3 : 8;
-  static constexpr uint32_t kColFdV = 256, kColFdQ = 256 + D;
-  static constexpr int kSmemFused = 2 * kTileBytes + kRingFused * kTileBytes + 32768 + 1024 + 1024;
-  // Non-sequence-parallel pass: K, V resident, dO / Q ring, dS^T staging, lse2 / D vectors.
-  // dQ_ij over dP^T at d = 128, in the columns d = 64 leaves free otherwise.
-  static constexpr int kRingNsp = D == 128 ? 3 : 8;
-  static constexpr uint32_t kColNspDq = D == 128 ? kColP : 384;
-  static constexpr int kSmemNsp = 2 * kTileBytes + kRingNsp * kTileBytes + 32768 + kVecSlots * 1024 + 1024;
-  static_assert(kSmemDkdv <= 232448 && kSmemDq <= 232448 && kSmemFused + 1024 <= 232448 && kSmemNsp + 1024 <= 232448,
-                "shared memory per CTA");
-};
-
-// Load one row-tile (128 rows x D columns, D/64 boxes of 16 KB) through a tensor map.
-template <int D>
-__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int col0, int row0) {
-#pragma unroll
-  for (int c = 0; c < D / 64; ++c) tma_load_2d(dst + c * 16384, m, bar, col0 + c * 64, row0);
-}
-
-// 64 columns from TMEM -> floats, both loads in flight before one wait.
-__device__ __forceinline__ void ld_cols64(uint32_t taddr, float* x) {
-  uint32_t r0[32], r1[32];
-  tmem_ld32(taddr, r0);
-  tmem_ld32(taddr + 32, r1);
-  tmem_ld_wait();
-#pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    x[c] = __uint_as_float(r0[c]);
-    x[32 + c] = __uint_as_float(r1[c]);
-  }
-}
-
-// Store 64 fp32 values as 32 packed bf16x2 TMEM columns.
-__device__ __forceinline__ void st_bf16_64(uint32_t taddr, const float* v) {
-  uint32_t pk[32];
-#pragma unroll
-  for (int t = 0; t < 32; ++t) pk[t] = pack_bf16x2(v[2 * t], v[2 * t + 1]);
-  tmem_st32(taddr, pk);
-}
-
 // ---------------------------------------------------------------- bias-table gradient
 // Table entry (h, n) collects dS_ij over the pairs of bucket n = clamp(j - i + center, 0,
 // nb - 1).  A warp holds dS^T for its 32 key rows j = j0 + lane against 64 query columns
@@ -354,156 +236,12 @@ __device__ __forceinline__ void dbias_warp_tile(const float* ds, float* grad_row
   dbias_flush(s0, w0 + s1, w1, grad_row, nb, rel0, lane);
 }
 
-// Write NC (32 or 64) accumulator columns of this thread's TMEM lane, times `mul`, as bf16
-// to global (or zeros when `zero`), one thread per row.
-template <int NC>
-__device__ __forceinline__ void store_acc_row_own(uint32_t taddr, float mul, __nv_bfloat16* dst, bool valid,
-                                                  bool zero) {
-#pragma unroll
-  for (int cc = 0; cc < NC / 32; ++cc) {
-    uint32_t r[32];
-    if (!zero) {
-      tmem_ld32(taddr + cc * 32, r);
-      tmem_ld_wait();
-    }
-    uint32_t pk[16];
-#pragma unroll
-    for (int t = 0; t < 16; ++t)
-      pk[t] = zero ? 0u : pack_bf16x2(__uint_as_float(r[2 * t]) * mul, __uint_as_float(r[2 * t + 1]) * mul);
-    if (valid) {
-      st_global_v8(dst + cc * 32, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
-      st_global_v8(dst + cc * 32 + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
-    }
-  }
-}
-// All D accumulator columns of this thread's TMEM lane, times `mul`, as bf16 to its own row,
-// 32 columns at a time; arrives on `empty` as soon as the last columns are in registers.
-template <int D>
-__device__ __forceinline__ void drain_row_own(uint32_t taddr, float mul, __nv_bfloat16* dst, bool valid,
-                                              uint64_t* empty) {
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t r[32];
-    tmem_ld32(taddr + c0, r);
-    tmem_ld_wait();
-    if (c0 + 32 == D) {
-      tc_fence_before();
-      mbar_arrive(empty);
-    }
-    uint32_t pk[16];
-#pragma unroll
-    for (int t = 0; t < 16; ++t) pk[t] = pack_bf16x2(__uint_as_float(r[2 * t]) * mul, __uint_as_float(r[2 * t + 1]) * mul);
-    if (valid) {
-      st_global_v8(dst + c0, pk[0], pk[1], pk[2], pk[3], pk[4], pk[5], pk[6], pk[7]);
-      st_global_v8(dst + c0 + 16, pk[8], pk[9], pk[10], pk[11], pk[12], pk[13], pk[14], pk[15]);
-    }
-  }
-}
-
-// The D accumulator columns of this thread's TMEM lane as fp32 to its own row (16-byte
-// aligned); arrives on `empty` as soon as the last columns are in registers.
-template <int D>
-__device__ __forceinline__ void drain_row_f32(uint32_t taddr, float* dst, bool valid, uint64_t* empty) {
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t r[32];
-    tmem_ld32(taddr + c0, r);
-    tmem_ld_wait();
-    if (c0 + 32 == D) {
-      tc_fence_before();
-      mbar_arrive(empty);
-    }
-    if (valid) {
-#pragma unroll
-      for (int c = 0; c < 32; c += 4)
-        *reinterpret_cast<uint4*>(dst + c0 + c) = make_uint4(r[c], r[c + 1], r[c + 2], r[c + 3]);
-    }
-  }
-}
-
-// Write NC (32 or 64) accumulator columns of this thread's TMEM lane, times `mul`, as bf16
-// to global (or zeros when `zero`).  All 32 lanes of the warp call it together: the rows'
-// stores are shared across lanes so that each store instruction writes whole row segments.
-template <int NC>
-__device__ __forceinline__ void store_acc_row(uint32_t taddr, float mul, __nv_bfloat16* dst, bool valid, bool zero) {
-  uint4 c[NC / 8];  // the row's NC bf16 values as 16-byte chunks
-#pragma unroll
-  for (int cc = 0; cc < NC / 32; ++cc) {
-    uint32_t r[32];
-    if (!zero) {
-      tmem_ld32(taddr + cc * 32, r);
-      tmem_ld_wait();
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint32_t w4[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int e = 8 * q + 2 * t;
-        w4[t] = zero ? 0u : pack_bf16x2(__uint_as_float(r[e]) * mul, __uint_as_float(r[e + 1]) * mul);
-      }
-      c[4 * cc + q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
-    }
-  }
-  st_rows_coalesced<NC * 2>(c, valid ? static_cast<void*>(dst) : nullptr);
-}
-
-// Writes the D accumulator columns of this thread's TMEM lane, times `mul`, as bf16 to the
-// row at `dst`, 32 columns at a time (coalesced across the warp), and arrives on `empty`
-// once the last columns are in registers: the accumulator may be overwritten from then on.
-// All 32 lanes of the warp call it together.
-template <int D>
-__device__ __forceinline__ void drain_acc_rows(uint32_t taddr, float mul, __nv_bfloat16* dst, bool valid,
-                                               uint64_t* empty) {
-#pragma unroll 1
-  for (int c0 = 0; c0 < D; c0 += 32) {
-    uint32_t r[32];
-    tmem_ld32(taddr + c0, r);
-    tmem_ld_wait();
-    if (c0 + 32 == D) {
-      tc_fence_before();
-      mbar_arrive(empty);
-    }
-    uint4 c[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      c[q] = make_uint4(pack_bf16x2(__uint_as_float(r[8 * q]) * mul, __uint_as_float(r[8 * q + 1]) * mul),
-                        pack_bf16x2(__uint_as_float(r[8 * q + 2]) * mul, __uint_as_float(r[8 * q + 3]) * mul),
-                        pack_bf16x2(__uint_as_float(r[8 * q + 4]) * mul, __uint_as_float(r[8 * q + 5]) * mul),
-                        pack_bf16x2(__uint_as_float(r[8 * q + 6]) * mul, __uint_as_float(r[8 * q + 7]) * mul));
-    st_rows_coalesced<64>(c, valid ? static_cast<void*>(dst + c0) : nullptr);
-  }
-}
-
 // ================================================================== dK / dV pass
 // Ring of single tiles, filled in the order dO_i, Q_i for the query tiles i of each key
 // tile: dO_i is released after dV(i) and Q_i after dK(i), i.e. in fill order.  Each Q_i
 // brings its tile's lse2 and D vectors (vector slot = query tile count mod kVecSlots; a
 // slot is refilled only after dK of its previous tile completed).
-//
-// kWin (sliding window with sinks, shared key/value heads): an item's head is a key/value head,
-// whose tile sums over the query tiles that its keys' windows reach, of every query head of the
-// group.  The units behind the key tiles are chunks of the sinks' pairs (win_key_unit): K and V
-// are then the sinks, and the epilogue writes fp32 partial sums for join_kernel.
-struct KeyUnit {
-  int first, n, r0, count, chunk;  // see WinKeyUnit
-};
-template <bool kWin>
-__device__ __forceinline__ KeyUnit key_unit(const BwdParams& p, const ItemMeta& m, int kt) {
-  KeyUnit u;
-  if (kWin) {
-    const WinKeyUnit w = win_key_unit(kt, m.Lq, meta_win(m), p.win.window, p.group);
-    u = KeyUnit{w.first, w.n, w.r0, w.r1 - w.r0, w.chunk};
-  } else {
-    u.r0 = 0;
-    u.chunk = -1;
-    q_tiles_for_kv_tile(kt, m.Lq, m.Lk, p.causal != 0, &u.first, &u.count);
-    u.n = u.count;
-  }
-  return u;
-}
-
-template <int D, bool kBias, bool kJBias = false, bool kWin = false>
+template <int D, bool kBias, bool kJBias = false>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p) {
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDkdv;
@@ -570,49 +308,35 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
     // dP^T MMA frees the buffers, whatever the ring producer is waiting on.
     if (lane == 0) {
       uint32_t item_n = 0, tn = 0;
-      int acq_b = -1, acq_s = -1;  // sequences whose maps (sink maps) this thread has acquired
+      int acq_b = -1;  // sequence whose maps this thread has acquired
       bool ok = true;
       uint32_t item_k = 0;
       for (; ok; ++item_k) {
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
+        const int Lq = wi.Lq, Lk = wi.Lk;
         const int64_t k0 = wi.ko;
         acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
-        if (kWin && p.win.sinks > 0 && acq_s != wi.b) {
-          tmap_acquire(p.smaps + size_t(wi.b) * kNumMapSlots + kMapK);
-          tmap_acquire(p.smaps + size_t(wi.b) * kNumMapSlots + kMapV);
-          acq_s = wi.b;
-        }
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-          const KeyUnit ku = key_unit<kWin>(p, wi, kt);
-          if (ku.count == 0) continue;
-          const bool sink = kWin && ku.chunk >= 0;
-          const CUtensorMap* maps = sink ? p.smaps : p.maps;
-          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
-          const int skip = kWin && !sink ? meta_win(wi).skip : 0;
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
+          int first, count;
+          q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
+          if (count == 0) continue;
+          const TileMap mk = tile_map(p.maps, p.B, kMapK, wi.b, k0, kt, p.total_kv);
+          const TileMap mv = tile_map(p.maps, p.B, kMapV, wi.b, k0, kt, p.total_kv);
           if (mk.tail) {
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
           }
           if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
-          mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
+          mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
           load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
           load_tile<D>(sV, mv.map, &kv_full, wi.h * D, mv.y);
           ++item_n;
           // pull the next key tile into L2 meanwhile: the next of this range, else the first
           // of this CTA's next item
-          if (kWin) {  // items are single units
-            const ItemMeta* wn = meta_peek_next(meta, item_k);
-            if (wn && wn->u0 * kBN < wn->Lk) {
-              acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapK, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapV, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
-            }
-          } else {
+          {
             int nb = -1, nh = 0, nt = 0;
             if (kt + 1 < wi.u1) {
               nb = wi.b, nh = wi.h, nt = kt + 1;
@@ -660,22 +384,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
+        const int Lq = wi.Lq, Lk = wi.Lk;
         const int64_t q0 = wi.qo;
         acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
+        const int64_t vec0 = int64_t(wi.h) * p.qpad_cap + wi.qp;
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-          const KeyUnit ku = key_unit<kWin>(p, wi, kt);
-          if (const ItemMeta* wnp = kWin ? meta_peek_next(meta, item_k) : nullptr) {
-            // the first query tiles of this CTA's next item into L2 meanwhile
-            const KeyUnit nu = key_unit<kWin>(p, *wnp, wnp->u0);
-            const int64_t nqo = wnp->qo;
-            acquire_seq_maps(p.maps, wnp->b, kMapQ, kMapDO, acq_b, true);
-            for (int r = 0; r < min(nu.count, 2); ++r) {
-              const int t = nu.first + (nu.r0 + r) % nu.n, col = (wnp->h * p.group + (nu.r0 + r) / nu.n) * D;
-              prefetch_tile<D / 64>(p.maps, p.B, kMapDO, wnp->b, nqo, t, p.total_q, col);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapQ, wnp->b, nqo, t, p.total_q, col);
-            }
-          }
-          if (const ItemMeta* wnp = !kWin && kt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
+          int first, count;
+          q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
+          if (const ItemMeta* wnp = kt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
             // pull the first query tiles of this CTA's next item into L2 meanwhile
             const ItemMeta& wn = *wnp;
             int nLq, nLk, nfirst, ncount;
@@ -688,14 +404,12 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
               prefetch_tile<D / 64>(p.maps, p.B, kMapQ, wn.b, nqo, t, p.total_q, wn.h * D);
             }
           }
-          for (int i = 0; i < ku.count && ok; ++i) {
-            const int qt = kWin ? ku.first + (ku.r0 + i) % ku.n : ku.first + i;
-            const int qh = kWin ? wi.h * p.group + (ku.r0 + i) / ku.n : wi.h;  // query head
-            const int64_t vec0 = int64_t(qh) * p.qpad_cap + wi.qp;
+          for (int i = 0; i < count && ok; ++i) {
+            const int qt = first + i;
             const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
             const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
-            if (!fill(mdo, qh * D, nullptr, nullptr)) { ok = false; break; }
-            if (!fill(mq, qh * D, p.lse2 + vec0 + qt * kBM, p.delta + vec0 + qt * kBM)) {
+            if (!fill(mdo, wi.h * D, nullptr, nullptr)) { ok = false; break; }
+            if (!fill(mq, wi.h * D, p.lse2 + vec0 + qt * kBM, p.delta + vec0 + qt * kBM)) {
               ok = false;
               break;
             }
@@ -745,8 +459,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
+       const int Lq = wi.Lq, Lk = wi.Lk;
        for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
-        const int count = key_unit<kWin>(p, wi, kt).count;
+        int first, count;
+        q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
         if (count == 0) continue;
         if (!wait(&kv_full, item_n & 1)) { ok = false; break; }
         ++item_n;
@@ -804,8 +520,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
     }
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
-                                         p.win.window, p.win.sinks, p.win.H_kv))
+    if (lane == 0 && !meta_publish(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -830,15 +545,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
      if (it.b < 0) break;  // end of this CTA's items
      const int Lq = it.Lq, Lk = it.Lk;
      for (int kt = it.u0; kt < it.u1 && ok; ++kt) {
-      const KeyUnit ku = key_unit<kWin>(p, it, kt);
-      const int count = ku.count;
-      const bool sink = kWin && ku.chunk >= 0;
-      const int j = sink ? row - meta_win(it).org : kt * kBN + row;  // local key index (sinks: behind org)
+      int first, count;
+      q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
+      const int j = kt * kBN + row;  // local key index
       if (count == 0) continue;  // rows of zeros: written by the epilogue warpgroup
       const int diag = Lk - Lq;  // key j visible to query i iff i >= j - diag
       const float* brow = kBias ? p.bias2 + size_t(it.h) * p.num_buckets : nullptr;
       for (int i = 0; i < count && ok; ++i) {
-        const int qt = kWin ? ku.first + (ku.r0 + i) % ku.n : ku.first + i;
+        const int qt = first + i;
         uint4 jbw[8];  // general bias for this tile (row order), loaded before the waits
         if (kJBias) {
           const int64_t pitch = (Lk + 7) / 8 * 8;  // rows of the sequence's block: bias[i][j] at i * pitch + j
@@ -876,32 +590,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         if (!mbar_wait(&st_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 20);
-        const int i0 = qt * kBM + 64 * w;  // local query index of column 0 of this half
-        if (kWin && D == 64) {
-          // the warp's 32 keys against these 64 queries: none sees any -> nothing to compute (d = 64:
-          // 130 -> 127 us on the ragged step; at d = 128 the products set the pace, 334 -> 338 us)
-          const int j0 = j - lane, w_hi = sink ? Lq : j0 + 31 - diag + p.win.window - 1;  // last query that may see one
-          if (i0 + 63 < j0 - diag || i0 > w_hi || i0 >= Lq ||
-              quarter * 32 >= (sink ? meta_win(it).ns : Lk - kt * kBN)) {
-            uint32_t z[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) z[c] = 0u;
-            tmem_st32(tPT, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full);
-            if (!mbar_wait(&dpt_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-            ++tile_n;
-            tc_fence_after();
-            tmem_st32(tDST, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&ds_full);
-            continue;
-          }
-        }
         float x[64];
         ld_cols64(tS, x);
+        const int i0 = qt * kBM + 64 * w;  // local query index of column 0 of this half
         if (kJBias) {
           uint32_t jbk[32];
           jbias_col_transpose(jbk, jbw, jb_scratch + (warp - kFirstComputeWarp) * 128, j < Lk, lane);
@@ -928,14 +619,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c < lim) x[c] = -INFINITY;
-          }
-          if (kWin && !sink) {
-            const int hi = lim + p.win.window - 1;  // columns c > hi have moved past the key
-            if (hi < 63) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (c > hi) x[c] = -INFINITY;
-            }
           }
         }
 #pragma unroll
@@ -1007,27 +690,12 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
      const int64_t ko = it.ko;
      const int Lq = it.Lq, Lk = it.Lk;
      for (int kt = it.u0; kt < it.u1 && ok; ++kt) {
-      const KeyUnit ku = key_unit<kWin>(p, it, kt);
-      const int count = ku.count;
+      int first, count;
+      q_tiles_for_kv_tile(kt, Lq, Lk, causal, &first, &count);
       const int j = kt * kBN + row;  // local key index
-      const bool valid = j < Lk && (!kWin || j >= meta_win(it).pad);
-      const int heads = kWin ? p.win.H_kv : p.H;
-      __nv_bfloat16* dk_row = p.g0 + ((ko + j) * heads + it.h) * int64_t(D);
-      __nv_bfloat16* dv_row = p.g1 + ((ko + j) * heads + it.h) * int64_t(D);
-      if (kWin && ku.chunk >= 0) {  // a chunk of the sinks: fp32 partial sums
-        const WinSeq ws = meta_win(it);
-        const int64_t slot = sink_slot0(it.qp / kBM, it.b, p.group) * p.win.H_kv +
-                             int64_t(it.h) * win_sink_chunks(Lq, ws, p.group) + ku.chunk;
-        float* part = p.spart + (slot * 2 * p.win.sinks + row) * int64_t(D);
-        if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-        tc_fence_after();
-        drain_row_f32<D>(tmem + lane_addr + C::kColA1, part + p.win.sinks * int64_t(D), row < ws.ns, &dv_empty);
-        if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-        ++acc_n;
-        tc_fence_after();
-        drain_row_f32<D>(tmem + lane_addr + C::kColA0, part, row < ws.ns, &dk_empty);
-        continue;
-      }
+      const bool valid = j < Lk;
+      __nv_bfloat16* dk_row = p.g0 + ((ko + j) * p.H + it.h) * int64_t(D);
+      __nv_bfloat16* dv_row = p.g1 + ((ko + j) * p.H + it.h) * int64_t(D);
       if (count == 0) {  // no query sees these keys
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -1059,27 +727,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
 // Ring of single tiles, filled V_j, K_j per key tile: V_j is released after dP(j), K_j
 // after dQ(j), i.e. in fill order.  S and dP of the next key tile are issued as soon as
 // the warpgroups hold S in registers, so the dP/dS buffer alternates by tile parity.
-//
-// kWin: a query tile's steps are the sinks (nz = 1 if any of its rows sees them), then the
-// window-part key tiles from a on.  The sinks' products have sink_rows keys.
-struct QueryUnit {
-  int a, nz, nkv;
-};
-template <bool kWin>
-__device__ __forceinline__ QueryUnit query_unit(const BwdParams& p, const ItemMeta& m, int qt) {
-  QueryUnit u = {0, 0, 0};
-  if (kWin) {
-    int e;
-    win_kv_tiles(qt, m.Lq, meta_win(m), p.win.window, &u.a, &e);
-    u.nz = win_sees_sinks(qt, m.Lq, meta_win(m)) ? 1 : 0;
-    u.nkv = e - u.a + u.nz;
-  } else {
-    u.nkv = kv_tiles_for_q_tile(qt, m.Lq, m.Lk, p.causal != 0);
-  }
-  return u;
-}
-
-template <int D, bool kBias, bool kJBias = false, bool kWin = false>
+template <int D, bool kBias, bool kJBias = false>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) {
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDq;
@@ -1154,10 +802,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
+       const int Lq = wi.Lq, Lk = wi.Lk;
        const int64_t q0 = wi.qo;
        acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        if (query_unit<kWin>(p, wi, qt).nkv == 0) continue;
+        if (kv_tiles_for_q_tile(qt, Lq, Lk, causal) == 0) continue;
         const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
         const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
         if (mq.tail) {
@@ -1198,14 +847,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
     // ------------------------------------------------------------ V / K ring producer
     if (lane == 0) {
       uint32_t ring_n = 0, tn = 0;
-      int acq_b = -1, acq_s = -1;  // sequences whose maps (sink maps) this thread has acquired
+      int acq_b = -1;  // sequence whose maps this thread has acquired
       bool ok = true;
-      auto fill = [&](const TileMap& m, int col, uint32_t bytes) {
+      auto fill = [&](const TileMap& m, int col) {
         const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
         if (m.tail) tmap_acquire(m.map);
         if (!mbar_wait(&ring_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
         trace_event(p.trace, kTraceProducer, tn, 2);
-        mbar_arrive_expect_tx(&ring_full[e], bytes);
+        mbar_arrive_expect_tx(&ring_full[e], C::kTileBytes);
         load_tile<D>(sRing + e * C::kTileBytes, m.map, &ring_full[e], col, m.y);
         ++ring_n;
         return true;
@@ -1215,24 +864,12 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
+       const int Lq = wi.Lq, Lk = wi.Lk;
        const int64_t k0 = wi.ko;
-       const int col = (kWin ? wi.h / p.group : wi.h) * D;  // first column of the key/value head
        acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
-       if (kWin && p.win.sinks > 0) acquire_seq_maps(p.smaps, wi.b, kMapK, kMapV, acq_s, false);
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        const QueryUnit qu = query_unit<kWin>(p, wi, qt);
-        const int nkv = qu.nkv;
-        if (const ItemMeta* wnp = kWin && D == 128 ? meta_peek_next(meta, item_k) : nullptr) {
-          // the first key tiles of this CTA's next item into L2 meanwhile
-          const QueryUnit nu = query_unit<kWin>(p, *wnp, wnp->u0);
-          const int skip = meta_win(*wnp).skip;
-          acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
-          for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
-            prefetch_tile<D / 64>(p.maps, p.B, kMapV, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
-            prefetch_tile<D / 64>(p.maps, p.B, kMapK, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
-          }
-        }
-        if (const ItemMeta* wnp = !kWin && qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
+        const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
+        if (const ItemMeta* wnp = qt + 1 == wi.u1 ? meta_peek_next(meta, item_k) : nullptr) {
           // pull the first key tiles of this CTA's next item into L2 meanwhile
           const ItemMeta& wn = *wnp;
           const int64_t nko = p.kv_off[wn.b];
@@ -1244,15 +881,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           }
         }
         for (int jt = 0; jt < nkv && ok; ++jt) {
-          const bool sink = kWin && jt < qu.nz;
-          const CUtensorMap* maps = sink ? p.smaps : p.maps;
-          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
-          const int kt = kWin ? (sink ? 0 : qu.a + jt - qu.nz) : jt;
-          const int skip = kWin && !sink ? meta_win(wi).skip : 0;
-          const TileMap mv = tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv, kBN, skip);
-          const TileMap mk = tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv, kBN, skip);
-          const uint32_t bytes = sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes);
-          if (!fill(mv, col, bytes) || !fill(mk, col, bytes)) { ok = false; break; }
+          const TileMap mv = tile_map(p.maps, p.B, kMapV, wi.b, k0, jt, p.total_kv);
+          const TileMap mk = tile_map(p.maps, p.B, kMapK, wi.b, k0, jt, p.total_kv);
+          if (!fill(mv, wi.h * D) || !fill(mk, wi.h * D)) { ok = false; break; }
         }
        }
        if (ok) meta_release(meta, item_k);
@@ -1276,15 +907,15 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
       auto wait_ring = [&](uint32_t n) { return wait(&ring_full[n % R], (n / R) & 1); };
       auto ra = [&](uint32_t n) { return aR + (n % R) * C::kTileBytes; };
       // S (dp = false: Q K^T) or dP (dp = true: dO V^T) of a query tile and the key tile at b
-      auto mma_nt = [&](uint32_t dcol, bool dp, uint32_t b, uint32_t id) {
+      auto mma_nt = [&](uint32_t dcol, bool dp, uint32_t b) {
         const uint64_t ad = sdesc_sw128(dp ? aDO : aQ, 16, 1024), bd = sdesc_sw128(b, 16, 1024);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
           if (C::kDqQTmem)
-            umma_ts(tmem + dcol, tmem + (dp ? C::kColDqDO : C::kColDqQ) + kk * 8, bd + o, id, kk > 0);
+            umma_ts(tmem + dcol, tmem + (dp ? C::kColDqDO : C::kColDqQ) + kk * 8, bd + o, kIdS, kk > 0);
           else
-            umma_ss(tmem + dcol, ad + o, bd + o, id, kk > 0);
+            umma_ss(tmem + dcol, ad + o, bd + o, kIdS, kk > 0);
         }
       };
       uint32_t item_k = 0;
@@ -1292,20 +923,19 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
+       const int Lq = wi.Lq, Lk = wi.Lk;
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
-        const QueryUnit qu = query_unit<kWin>(p, wi, qt);
-        const int nkv = qu.nkv;
+        const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
         if (nkv == 0) continue;
-        const uint32_t id0 = kWin && qu.nz ? idesc_bf16_f32(128, p.sink_rows, false, false) : kIdS;  // the first step's
         if (!wait(C::kDqQTmem ? &qt_full : &qdo_full, item_n & 1)) { ok = false; break; }
         ++item_n;
         trace_event(p.trace, kTraceMma, tn, 10);
         const uint32_t n0 = ring_n;  // V_j at n0 + 2j, K_j at n0 + 2j + 1
         if (!wait_ring(n0 + 1)) { ok = false; break; }
-        mma_nt(C::kColS, false, ra(n0 + 1), id0);
+        mma_nt(C::kColS, false, ra(n0 + 1));
         umma_commit(&s_full);
         if (!wait_ring(n0)) { ok = false; break; }
-        mma_nt(colP(tile_n), true, ra(n0), id0);
+        mma_nt(colP(tile_n), true, ra(n0));
         umma_commit(&dp_full[tile_n & 1]);
         umma_commit(&ring_empty[n0 % R]);
         // Q and dO are read only by S and dP: once the last dP is issued the loader may
@@ -1321,11 +951,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
             if (!wait(&s_free, g & 1)) { ok = false; break; }
             trace_event(p.trace, kTraceMma, tn, 11);
             if (!wait_ring(nk + 2)) { ok = false; break; }
-            mma_nt(C::kColS, false, ra(nk + 2), kIdS);
+            mma_nt(C::kColS, false, ra(nk + 2));
             umma_commit(&s_full);
             trace_event(p.trace, kTraceMma, tn, 12);
             if (!wait_ring(nv + 2)) { ok = false; break; }
-            mma_nt(colP(g + 1), true, ra(nv + 2), kIdS);
+            mma_nt(colP(g + 1), true, ra(nv + 2));
             umma_commit(&dp_full[(g + 1) & 1]);
             umma_commit(&ring_empty[(nv + 2) % R]);
             if (jt + 2 == nkv && !C::kDqQTmem) umma_commit(&qdo_empty);
@@ -1337,12 +967,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           if (jt == 0 && !wait(&acc_empty, (acc_n & 1) ^ 1)) { ok = false; break; }
           // dQ += dS (TMEM, queries x keys) * K (keys x D, MN-major)
           const uint64_t kd = sdesc_sw128(ra(nk), 16384, 1024);
-          if (kWin && jt < qu.nz) {
-#pragma unroll 1
-            for (int kk = 0; kk < p.sink_rows / 16; ++kk)
-              umma_ts(tmem + C::kColDQ, tmem + colP(g) + (kk >> 2) * 64 + (kk & 3) * 8, kd + uint32_t(kk * 2048 >> 4),
-                      kIdAcc, kk > 0 ? 1u : 0u);
-          } else
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
             umma_ts(tmem + C::kColDQ, tmem + colP(g) + (kk >> 2) * 64 + (kk & 3) * 8, kd + uint32_t(kk * 2048 >> 4),
@@ -1365,8 +989,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
     }
    } else if (warp == 3) {
     // ------------------------------------------------------------ scheduler
-    if (lane == 0 && !meta_publish<kWin>(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag,
-                                         p.win.window, p.win.sinks, p.H))
+    if (lane == 0 && !meta_publish(meta, p.items, n_items, p.claim, p.q_off, p.kv_off, p.qpad, p.jb_off, abort_flag))
       raise_status(p.status, JFA_ERR_TIMEOUT);
    }
   } else if (warp < kFirstEpilogueWarp) {
@@ -1388,8 +1011,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
      const int Lq = it.Lq, Lk = it.Lk;
      const int64_t vec0 = int64_t(it.h) * p.qpad_cap + it.qp;
      for (int qt = it.u0; qt < it.u1 && ok; ++qt) {
-      const QueryUnit qu = query_unit<kWin>(p, it, qt);
-      const int nkv = qu.nkv;
+      const int nkv = kv_tiles_for_q_tile(qt, Lq, Lk, causal);
       const int i = qt * kBM + row;
       const bool valid = i < Lq;
       if (nkv == 0) continue;  // rows of zeros: written by the epilogue warpgroup
@@ -1462,35 +1084,13 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
         if (!mbar_wait(&s_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 20);
-        const bool sink = kWin && jt < qu.nz;
-        // local key index of column 0 of this half (sinks: behind org)
-        const int j0 = (kWin ? (sink ? -meta_win(it).org : (qu.a + jt - qu.nz) * kBN) : jt * kBN) + 64 * w;
-        const int n_real = sink ? meta_win(it).ns - 64 * w : Lk - j0;  // columns >= n_real hold no key
-        if (kWin && D == 64) {
-          // the warp's 32 queries against these 64 keys: none is seen -> nothing to compute (d = 64:
-          // 106 -> 101 us on the ragged step; no gain at d = 128)
-          const int r0 = i - lane;
-          if (r0 >= Lq || n_real <= 0 || r0 + 31 + diag < j0 || (!sink && r0 + diag - p.win.window + 1 > j0 + 63)) {
-            mbar_arrive(&s_free);
-            const uint32_t g = tile_n;
-            if (!mbar_wait(&dp_full[g & 1], (g >> 1) & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-            ++tile_n;
-            tc_fence_after();
-            uint32_t z[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) z[c] = 0u;
-            tmem_st32(tmem + lane_addr + colP(g) + 64 * w, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&ds_full[g & 1]);
-            continue;
-          }
-        }
         float x[64];
         ld_cols64(tS, x);
         tc_fence_before();
         mbar_arrive(&s_free);
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 21);
+        const int j0 = jt * kBN + 64 * w;  // local key index of column 0 of this half
+        const int n_real = Lk - j0;        // columns >= n_real are past the sequence end
         if (kJBias) {
           jbias_apply<64>(x, jbk, sl2, kLog2e);
 #pragma unroll
@@ -1515,15 +1115,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
 #pragma unroll
             for (int c = 0; c < 64; ++c)
               if (c > lim) x[c] = -INFINITY;
-          }
-          if (kWin && !sink) {
-            // columns c < clo are behind the window, or hold no key
-            const int clo = max(lim - p.win.window + 1, meta_win(it).pad - j0);
-            if (clo > 0) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (c < clo) x[c] = -INFINITY;
-            }
           }
         }
         if (n_real < 64) {
@@ -1573,12 +1164,12 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
      if (!meta_wait_warp(meta, item_k, abort_flag)) { ok = false; break; }
      const ItemMeta& it = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
      if (it.b < 0) break;  // end of this CTA's items
-     const int Lq = it.Lq;
+     const int Lq = it.Lq, Lk = it.Lk;
      for (int qt = it.u0; qt < it.u1 && ok; ++qt) {
       const int i = qt * kBM + row;
       const bool valid = i < Lq;
       __nv_bfloat16* dq_row = p.g0 + ((it.qo + i) * p.H + it.h) * int64_t(D);
-      if (query_unit<kWin>(p, it, qt).nkv == 0) {  // the query tile sees no key
+      if (kv_tiles_for_q_tile(qt, Lq, Lk, causal) == 0) {  // the query tile sees no key
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) store_acc_row<32>(0, 0.f, dq_row + c0, valid, true);
         continue;
@@ -2634,126 +2225,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) nsp_kernel(const BwdParams p)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-enum BwdPass { kPassDkdv = 0, kPassDq = 1, kPassFused = 2, kPassNsp = 3 };
-
-BwdParams make_params(const Problem& pr, const float* lse, void* ws, const WsLayout& L, int pass) {
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  BwdParams bp;
-  bp.q_off = pr.q_off;
-  bp.kv_off = pr.kv_off;
-  bp.B = pr.B;
-  bp.H = pr.H;
-  bp.total_q = pr.total_q;
-  bp.total_kv = pr.total_kv;
-  bp.scale = pr.scale;
-  bp.scale_log2 = pr.scale * kLog2e;
-  bp.causal = pr.causal;
-  bp.bias2 = pr.bias_table ? reinterpret_cast<const float*>(w + L.bias2) : nullptr;
-  // the dK/dV, fused and non-sequence-parallel passes together see every visible pair once:
-  // they add the bias gradient
-  bp.bias_grad = (pr.bias_table && pass != kPassDq) ? pr.bias_grad : nullptr;
-  bp.num_buckets = pr.num_buckets;
-  bp.center = pr.center;
-  bp.jbias = static_cast<const __nv_bfloat16*>(pr.jbias);
-  bp.jb_off = pr.jb_off;
-  bp.jb_plane = pr.jb_plane;
-  bp.jb_grad = pass != kPassDq ? static_cast<__nv_bfloat16*>(pr.jb_grad) : nullptr;
-  bp.maps = reinterpret_cast<const CUtensorMap*>(w + L.maps);
-  bp.items = reinterpret_cast<const WorkItem*>(
-      w + (pass == kPassDq ? L.dq : pass == kPassFused ? L.fused : pass == kPassNsp ? L.nsp : L.dkv));
-  const WsHeader* hdr = reinterpret_cast<const WsHeader*>(w);
-  bp.n_items = pass == kPassDq ? &hdr->n_dq : pass == kPassFused ? &hdr->n_fused
-                                           : pass == kPassNsp ? &hdr->n_nsp : &hdr->n_dkv;
-  WsHeader* mh = reinterpret_cast<WsHeader*>(w);
-  bp.claim = pass == kPassDq ? &mh->claim_dq : pass == kPassFused ? &mh->claim_fused
-                                             : pass == kPassNsp ? &mh->claim_nsp : &mh->claim_dkv;
-  bp.status = &reinterpret_cast<WsHeader*>(w)->status;
-  // list kinds of the planner: forward 0, dQ 1, dK/dV 2, fused 3, non-sequence-parallel 4
-  bp.wait_ns = &hdr->wait_ns[pass == kPassDq ? 1 : pass == kPassFused ? 3 : pass == kPassNsp ? 4 : 2];
-  bp.dqacc = reinterpret_cast<float*>(w + L.dqacc);
-  (void)lse;
-  bp.lse2 = reinterpret_cast<const float*>(w + L.lse2);
-  bp.delta = reinterpret_cast<const float*>(w + L.delta);
-  bp.qpad = reinterpret_cast<const int64_t*>(w + L.qpad);
-  bp.qpad_cap = L.qpad_cap;
-  bp.g0 = nullptr;
-  bp.g1 = nullptr;
-  bp.g2 = nullptr;
-  bp.win = pr.win;
-  bp.group = pr.win.window > 0 ? pr.H / pr.win.H_kv : 1;
-  bp.smaps = reinterpret_cast<const CUtensorMap*>(static_cast<uint8_t*>(ws) + L.smaps);
-  bp.sink_rows = sink_rows(pr.win.sinks);
-  bp.spart = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + L.spart);
-  bp.trace = pr.trace[pass == kPassDq ? JFA_KERNEL_BWD_DQ : pass == kPassFused ? JFA_KERNEL_BWD_FUSED
-                     : pass == kPassNsp ? JFA_KERNEL_BWD_NSP : JFA_KERNEL_BWD_DKDV];
-  return bp;
-}
-
-// ================================================================== the sinks' gradients (window)
-// dK and dV of each sequence's sinks from the dK/dV pass's partial sums, added in chunk order,
-// and zero rows for the keys between the sinks and the window part, which no query sees.
-// Memory bound and small: the partials are sinks x d x 2 floats per 16 query tiles.  Every
-// sequence gets the same number of warps.
-struct JoinParams {
-  const int64_t *q_off, *kv_off, *qpad;
-  const int* planned;  // 0 with malformed offsets: nothing to do
-  const float* spart;
-  int B, group;
-  WindowSpec win;
-  float scale;
-  __nv_bfloat16 *dk, *dv;
-};
-
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  if (*p.planned == 0) return;
-  const int lane = threadIdx.x & 31;
-  const int warps = int(gridDim.x * blockDim.x) >> 5, warp = int(blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int per_seq = warps / p.B > 0 ? warps / p.B : 1;
-  const int Hkv = p.win.H_kv;
-  for (int b = warp / per_seq; b < p.B; b += warps / per_seq) {
-    const int Lq = int(p.q_off[b + 1] - p.q_off[b]);
-    const int64_t ko = p.kv_off[b];
-    const WinSeq ws = win_seq(Lq, int(p.kv_off[b + 1] - ko), p.win.window, p.win.sinks, kBN);
-    const int chunks = win_sink_chunks(Lq, ws, p.group);
-    const int64_t slot0 = sink_slot0(p.qpad[b] / kBM, b, p.group) * Hkv;
-    const int64_t row_vecs = int64_t(Hkv) * D / 8;  // 16-byte pieces of a key row, all heads
-    const int64_t first = int64_t(warp % per_seq) * 32 + lane, step = int64_t(per_seq) * 32;
-    uint4* dk = reinterpret_cast<uint4*>(p.dk + ko * Hkv * D);
-    uint4* dv = reinterpret_cast<uint4*>(p.dv + ko * Hkv * D);
-    for (int64_t i = first; i < ws.ns * row_vecs; i += step) {
-      const int j = int(i / row_vecs), h = int(i % row_vecs) / (D / 8), c = int(i % (D / 8)) * 8;
-      const float* part = p.spart + ((slot0 + int64_t(h) * chunks) * 2 * p.win.sinks + j) * D + c;
-      float sk[8] = {}, sv[8] = {};
-      for (int k = 0; k < chunks; ++k, part += int64_t(2) * p.win.sinks * D) {
-        const float* pv = part + int64_t(p.win.sinks) * D;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(part) + q), v = __ldg(reinterpret_cast<const float4*>(pv) + q);
-          sk[4 * q] += a.x;
-          sk[4 * q + 1] += a.y;
-          sk[4 * q + 2] += a.z;
-          sk[4 * q + 3] += a.w;
-          sv[4 * q] += v.x;
-          sv[4 * q + 1] += v.y;
-          sv[4 * q + 2] += v.z;
-          sv[4 * q + 3] += v.w;
-        }
-      }
-      dk[i] = make_uint4(pack_bf16x2(sk[0] * p.scale, sk[1] * p.scale), pack_bf16x2(sk[2] * p.scale, sk[3] * p.scale),
-                         pack_bf16x2(sk[4] * p.scale, sk[5] * p.scale), pack_bf16x2(sk[6] * p.scale, sk[7] * p.scale));
-      dv[i] = make_uint4(pack_bf16x2(sv[0], sv[1]), pack_bf16x2(sv[2], sv[3]), pack_bf16x2(sv[4], sv[5]),
-                         pack_bf16x2(sv[6], sv[7]));
-    }
-    for (int64_t i = ws.ns * row_vecs + first; i < (ws.org + ws.pad) * row_vecs; i += step) {
-      dk[i] = make_uint4(0, 0, 0, 0);
-      dv[i] = make_uint4(0, 0, 0, 0);
-    }
-  }
-}
-
 }  // namespace
 
 cudaError_t launch_bwd_preprocess(const Problem& pr, const void* dout, const void* out, const float* lse,
@@ -2766,7 +2237,6 @@ cudaError_t launch_bwd_preprocess(const Problem& pr, const void* dout, const voi
   pp.total_q = pr.total_q;
   pp.items = reinterpret_cast<const WorkItem*>(w + L.dq);
   pp.n_items = &reinterpret_cast<const WsHeader*>(w)->n_dq;
-  pp.all_heads = pr.win.window > 0;
   pp.items2 = reinterpret_cast<const WorkItem*>(w + L.fused);
   pp.n_items2 = &reinterpret_cast<const WsHeader*>(w)->n_fused;
   pp.items3 = reinterpret_cast<const WorkItem*>(w + L.nsp);
@@ -2782,20 +2252,13 @@ cudaError_t launch_bwd_preprocess(const Problem& pr, const void* dout, const voi
   // row-parallel for wide token rows (every block resident at once, 4 per SM at <= 64
   // registers); per item otherwise
   const bool wide = int64_t(pr.H) * pr.d >= 1024;
+  const auto items128 = pr.win.window > 0 ? preprocess_items_kernel<128, true> : preprocess_items_kernel<128, false>;
+  const auto items64 = pr.win.window > 0 ? preprocess_items_kernel<64, true> : preprocess_items_kernel<64, false>;
   if (pr.d == 128)
     return wide ? launch_pdl(preprocess_kernel<128>, dim3(4 * num_sms), dim3(256), 0, stream, pp)
-                : launch_pdl(preprocess_items_kernel<128>, dim3(8 * num_sms), dim3(256), 0, stream, pp);
+                : launch_pdl(items128, dim3(8 * num_sms), dim3(256), 0, stream, pp);
   return wide ? launch_pdl(preprocess_kernel<64>, dim3(4 * num_sms), dim3(256), 0, stream, pp)
-              : launch_pdl(preprocess_items_kernel<64>, dim3(8 * num_sms), dim3(256), 0, stream, pp);
-}
-
-template <typename K>
-cudaError_t launch_dkdv_k(K kern, int smem, int grid, const BwdParams& bp, cudaStream_t stream) {
-  cudaError_t e = check_launch_registers(kern, kLaunchRegsDkdv);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(grid), dim3(kThreadsDkdv), smem, stream, bp);
+              : launch_pdl(items64, dim3(8 * num_sms), dim3(256), 0, stream, pp);
 }
 
 cudaError_t launch_bwd_dkdv(const Problem& pr, const float* lse, void* ws, const WsLayout& L, void* dk, void* dv,
@@ -2803,10 +2266,6 @@ cudaError_t launch_bwd_dkdv(const Problem& pr, const float* lse, void* ws, const
   BwdParams bp = make_params(pr, lse, ws, L, kPassDkdv);
   bp.g0 = static_cast<__nv_bfloat16*>(dk);
   bp.g1 = static_cast<__nv_bfloat16*>(dv);
-  if (pr.win.window > 0)
-    return pr.d == 128
-               ? launch_dkdv_k(dkdv_kernel<128, false, false, true>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream)
-               : launch_dkdv_k(dkdv_kernel<64, false, false, true>, BwdCfg<64>::kSmemDkdv, num_sms, bp, stream);
   const bool bias = pr.bias_table != nullptr, jb = pr.jbias != nullptr;
   if (pr.d == 128)
     return bias ? launch_dkdv_k(dkdv_kernel<128, true>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream)
@@ -2837,9 +2296,6 @@ cudaError_t launch_bwd_dq(const Problem& pr, const float* lse, void* ws, const W
                           cudaStream_t stream) {
   BwdParams bp = make_params(pr, lse, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
-  if (pr.win.window > 0)
-    return pr.d == 128 ? launch_dkdv_k(dq_kernel<128, false, false, true>, BwdCfg<128>::kSmemDq, num_sms, bp, stream)
-                       : launch_dkdv_k(dq_kernel<64, false, false, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream);
   const bool bias = pr.bias_table != nullptr, jb = pr.jbias != nullptr;
   if (pr.d == 128)
     return bias ? launch_dkdv_k(dq_kernel<128, true>, BwdCfg<128>::kSmemDq, num_sms, bp, stream)
@@ -2848,25 +2304,6 @@ cudaError_t launch_bwd_dq(const Problem& pr, const float* lse, void* ws, const W
   return bias ? launch_dkdv_k(dq_kernel<64, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream)
               : jb ? launch_dkdv_k(dq_kernel<64, false, true>, BwdCfg<64>::kSmemDq, num_sms, bp, stream)
                    : launch_dkdv_k(dq_kernel<64, false>, BwdCfg<64>::kSmemDq, num_sms, bp, stream);
-}
-
-cudaError_t launch_bwd_join(const Problem& pr, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
-                            cudaStream_t stream) {
-  uint8_t* w = static_cast<uint8_t*>(ws);
-  JoinParams jp;
-  jp.q_off = pr.q_off;
-  jp.kv_off = pr.kv_off;
-  jp.qpad = reinterpret_cast<const int64_t*>(w + L.qpad);
-  jp.planned = &reinterpret_cast<const WsHeader*>(w)->planned;
-  jp.spart = reinterpret_cast<const float*>(w + L.spart);
-  jp.B = pr.B;
-  jp.group = pr.H / pr.win.H_kv;
-  jp.win = pr.win;
-  jp.scale = pr.scale;
-  jp.dk = static_cast<__nv_bfloat16*>(dk);
-  jp.dv = static_cast<__nv_bfloat16*>(dv);
-  return pr.d == 128 ? launch_pdl(join_kernel<128>, dim3(2 * num_sms), dim3(256), 0, stream, jp)
-                     : launch_pdl(join_kernel<64>, dim3(2 * num_sms), dim3(256), 0, stream, jp);
 }
 
 cudaError_t launch_bwd_nsp(const Problem& pr, const float* lse, void* ws, const WsLayout& L, void* dq, void* dk,

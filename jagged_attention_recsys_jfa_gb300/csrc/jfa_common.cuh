@@ -375,11 +375,34 @@ struct TileMap {
   int y;
   bool tail;  // to be acquired before the load
 };
-// Windowed key tiles may have `skip` empty rows in front of the first (see WinSeq): row0 is then the
-// grid's start, the maps start at the first real row (of the tile, for a tail map), and a tile with
-// empty rows is loaded from a negative coordinate.
 __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                            int64_t total, int rows = kBM, int skip = 0) {
+                                            int64_t total) {
+  const int64_t g0 = row0 + int64_t(t) * kBM;
+  if (g0 + kBM > total)
+    return {maps + size_t(B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total), 0, true};
+  return {maps + size_t(b) * kNumMapSlots + slot, t * kBM, false};
+}
+
+// Pull row tile `t` of a sequence (boxes of 64 columns from column col0) into L2 ahead of
+// its load.  Tiles whose box would reach past the tensor's last row are skipped.
+template <int kBoxes>
+__device__ __forceinline__ void prefetch_tile(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
+                                              int64_t total, int col0) {
+  const TileMap m = tile_map(maps, B, slot, b, row0, t, total);
+  if (m.tail) return;
+#pragma unroll
+  for (int c = 0; c < kBoxes; ++c)
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m.map), "r"(col0 + c * 64),
+                 "r"(m.y)
+                 : "memory");
+}
+
+// Windowed key tiles (of `rows` rows) may have `skip` empty rows in front of the first (see WinSeq):
+// row0 is then the grid's start, the maps start at the first real row (of the tile, for a tail map),
+// and a tile with empty rows is loaded from a negative coordinate.  (A function of its own: with
+// these two tests in tile_map the plain backward's passes ran 1 to 2% slower.)
+__device__ __forceinline__ TileMap win_tile_map(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
+                                                int64_t total, int rows, int skip) {
   const int64_t g0 = row0 + int64_t(t) * rows;
   const int empty = t * rows < skip ? skip - t * rows : 0;  // empty rows of this tile
   if (g0 + rows > total)
@@ -392,20 +415,20 @@ __device__ __forceinline__ TileMap tile_map(const CUtensorMap* maps, int B, int 
 // (switching to another sequence's map costs a load about a microsecond).  Only a sequence's last,
 // partial tile goes through a map of its own.  `whole` is nullptr when row numbers need more than
 // 31 bits.
-__device__ __forceinline__ TileMap tile_map(const CUtensorMap* whole, const CUtensorMap* maps, int B, int slot, int b,
-                                            int64_t row0, int t, int len, int64_t total, int rows = kBM, int skip = 0) {
+__device__ __forceinline__ TileMap win_tile_map(const CUtensorMap* whole, const CUtensorMap* maps, int B, int slot, int b,
+                                                int64_t row0, int t, int len, int64_t total, int rows = kBM,
+                                                int skip = 0) {
   if (whole != nullptr && (t + 1) * rows <= len && t * rows >= skip) return {whole, int(row0) + t * rows, false};
-  TileMap m = tile_map(maps, B, slot, b, row0, t, total, rows, skip);
+  TileMap m = win_tile_map(maps, B, slot, b, row0, t, total, rows, skip);
   m.tail = true;  // not acquired yet
   return m;
 }
 
-// Pull row tile `t` of a sequence (boxes of 64 columns from column col0) into L2 ahead of
-// its load.  Tiles whose box would reach past the tensor's last row are skipped.
+// prefetch_tile for windowed key tiles (of kBN rows); tiles with empty rows are skipped too.
 template <int kBoxes>
-__device__ __forceinline__ void prefetch_tile(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
-                                              int64_t total, int col0, int skip = 0) {
-  const TileMap m = tile_map(maps, B, slot, b, row0, t, total, kBM, skip);
+__device__ __forceinline__ void win_prefetch_tile(const CUtensorMap* maps, int B, int slot, int b, int64_t row0, int t,
+                                                  int64_t total, int col0, int skip) {
+  const TileMap m = win_tile_map(maps, B, slot, b, row0, t, total, kBN, skip);
   if (m.tail || m.y < 0) return;
 #pragma unroll
   for (int c = 0; c < kBoxes; ++c)

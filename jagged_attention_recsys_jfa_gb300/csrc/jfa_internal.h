@@ -85,8 +85,17 @@ cudaError_t launch_wait_timeout_selftest(void* ws, uint64_t timeout_ns, cudaStre
 cudaError_t launch_forward(const Problem& p, void* ws, const WsLayout& L, void* out, float* lse,
                            int num_sms, cudaStream_t stream);
 
+// ---- windowed call (jfa_win_plan.cu, jfa_win.cu, jfa_win_bwd.cu; its preprocess is launch_bwd_preprocess)
+cudaError_t launch_win_plan(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, bool backward,
+                            int num_sms, cudaStream_t stream);
 cudaError_t launch_win_forward(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse,
                                int num_sms, cudaStream_t stream);
+cudaError_t launch_win_dkdv(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+                            cudaStream_t stream);
+cudaError_t launch_win_dq(const Problem& p, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream);
+// The sinks' dK and dV from their partial sums, and zeros for keys that no query sees.
+cudaError_t launch_win_join(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+                            cudaStream_t stream);
 
 cudaError_t launch_bwd_preprocess(const Problem& p, const void* dout, const void* out, const float* lse,
                                   void* ws, const WsLayout& L, int num_sms, cudaStream_t stream);
@@ -94,9 +103,6 @@ cudaError_t launch_bwd_dkdv(const Problem& p, const float* lse, void* ws, const 
                             void* dv, int num_sms, cudaStream_t stream);
 cudaError_t launch_bwd_dq(const Problem& p, const float* lse, void* ws, const WsLayout& L, void* dq,
                           int num_sms, cudaStream_t stream);
-// Window: the sinks' dK and dV from their partial sums, and zeros for keys that no query sees.
-cudaError_t launch_bwd_join(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
-                            cudaStream_t stream);
 // Sequences of 2 .. kNspMaxTiles query tiles: one CTA per sequence and head, every tile
 // pair once, dQ summed over key tiles in the workspace.
 cudaError_t launch_bwd_nsp(const Problem& p, const float* lse, void* ws, const WsLayout& L, void* dq, void* dk,
