@@ -178,7 +178,7 @@ jfa_status jfa_forward_noalloc(const void* q, const void* k, const void* v, cons
  * k, v: bf16 [num_pages][H_kv][page_size][d], the caller's, 16-byte aligned; token p of
  * sequence b lives in row p % page_size of page page_table[b * max_pages + p / page_size].
  * page_size in {16, 32, 64, 128}; d in {64, 128}; num_pages * H_kv * page_size < 2^31 and
- * max_pages * page_size < 2^31.  page_table: device int32 [B][max_pages]; entries that a
+ * max_pages * page_size <= 2^31 - 128.  page_table: device int32 [B][max_pages]; entries that a
  * call does not need may hold anything.  lengths: device int32 [B], tokens of each
  * sequence.  Pages may be shared by sequences for reading. */
 typedef struct {
@@ -215,7 +215,8 @@ size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
  *
  * q (may be NULL) is rotated into q_out, contiguous [total][H][d]; with k_out non-NULL the
  * rotated keys are also written there, contiguous [total][H_kv][d] (for the prompt's own
- * attention).  q_out may be q and k_out may be k when those are contiguous.  lengths_out (may
+ * attention).  q_out may be q and k_out may be k when those are contiguous;
+ * other overlaps of outputs with inputs or one another are not allowed (equal pointers are refused).  lengths_out (may
  * be NULL): device int32 [B], overwritten with lengths[b] + the number of appended tokens; it
  * may be `lengths` itself.  Each cache row must be written by one token only.
  *

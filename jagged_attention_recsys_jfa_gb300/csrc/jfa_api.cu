@@ -207,9 +207,9 @@ jfa_status check_cache(const jfa_cache* c) {
   if (!c->k || !c->v || !aligned16(c->k) || !aligned16(c->v) || !c->page_table || !c->lengths) return JFA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(c->page_table) & 3u) != 0 || (reinterpret_cast<uintptr_t>(c->lengths) & 3u) != 0)
     return JFA_ERR_INVALID_ARG;
-  const int64_t limit = int64_t(1) << 31;
+  const int64_t limit = int64_t(1) << 31;  // positions leave room to round up to a tile
   if (c->num_pages >= limit || c->num_pages * c->H_kv >= limit || c->num_pages * c->H_kv * c->page_size >= limit ||
-      int64_t(c->max_pages) * c->page_size >= limit)
+      int64_t(c->max_pages) * c->page_size > limit - 128)
     return JFA_ERR_INVALID_ARG;
   return JFA_OK;
 }
@@ -503,6 +503,9 @@ jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_str
     return JFA_ERR_INVALID_ARG;
   if (k_out && !aligned16(k_out)) return JFA_ERR_INVALID_ARG;
   if ((q && q_out == q && total > 1 && q_stride != int64_t(H) * d) || (k_out && k_out == k && total > 1 && k_stride != kv_row))
+    return JFA_ERR_INVALID_ARG;
+  // rows are read and written in any order: an output that is another argument's memory would change it
+  if (total > 0 && ((k_out && (k_out == v || k_out == q || k_out == q_out)) || (q && (q_out == k || q_out == v))))
     return JFA_ERR_INVALID_ARG;
   if (rot_dim < 0 || rot_dim > d || (rot_dim > 0 && !frequencies)) return JFA_ERR_INVALID_ARG;
   if (rot_dim % 16 != 0) return JFA_ERR_UNSUPPORTED;

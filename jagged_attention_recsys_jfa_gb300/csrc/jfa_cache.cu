@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
       if (page >= 0 && page < p.num_pages)
         at = (int64_t(page) * p.Hkv * p.page_size + (pos - pg * p.page_size)) * D;
     }
-    if (at < 0 && lane == 0) raise_status(p.status, JFA_ERR_BAD_PAGES);
+    if (at < 0 && lane == 0) raise_status(p.status, pos < 0 ? JFA_ERR_BAD_OFFSETS : JFA_ERR_BAD_PAGES);
     float2* cs = cs_all[warp];
     for (int i = lane; i < p.rot / 2; i += 32) {
       const uint64_t turns = uint64_t(pos) * p.turn[i];

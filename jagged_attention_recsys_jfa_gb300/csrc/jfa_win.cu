@@ -68,6 +68,7 @@ struct WinFwdParams {
   const uint64_t* wait_ns;
   __nv_bfloat16* out;
   float* lse;
+  bool wide_out;  // out is 32-byte aligned
   TraceBuf trace;
 };
 
@@ -547,7 +548,14 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           for (int e = 0; e < 8; ++e)
             w8[e] = pack_bf16x2(__uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e]) * inv_l,
                                 __uint_as_float(r[q >> 1][(q & 1) * 16 + 2 * e + 1]) * inv_l);
-          if (valid) st_global_v8(orow + c0 + q * 16, w8[0], w8[1], w8[2], w8[3], w8[4], w8[5], w8[6], w8[7]);
+          if (!valid) continue;
+          if (p.wide_out) {
+            st_global_v8(orow + c0 + q * 16, w8[0], w8[1], w8[2], w8[3], w8[4], w8[5], w8[6], w8[7]);
+          } else {
+            uint4* o = reinterpret_cast<uint4*>(orow + c0 + q * 16);
+            o[0] = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+            o[1] = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+          }
         }
       }
       tc_fence_before();
@@ -597,6 +605,7 @@ cudaError_t launch_win_forward(const Problem& pr, const PlanMaps& maps, void* ws
   fp.wait_ns = &reinterpret_cast<const WsHeader*>(w)->wait_ns[0];
   fp.out = static_cast<__nv_bfloat16*>(out);
   fp.lse = lse;
+  fp.wide_out = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
   fp.trace = pr.trace[JFA_KERNEL_FORWARD];
   const int grid = kWinCtasPerSm * num_sms;
   return pr.d == 128 ? launch_win_fwd_t<128>(maps, fp, grid, stream) : launch_win_fwd_t<64>(maps, fp, grid, stream);

@@ -331,8 +331,11 @@ _BF16, _F32, _I32, _I64 = torch.bfloat16, torch.float32, torch.int32, torch.int6
 
 def _call(device, stream, run):
     """run(stream handle) with `stream` current (so that what the call allocates and clears is
-    ordered with its kernels), else on `device`'s current stream."""
+    ordered with its kernels), else on `device`'s current stream.  As with any work on a stream of
+    one's own, the inputs have to be ready on `stream` and alive until it has passed the call."""
     if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
         with torch.cuda.stream(stream):
             return run(int(stream.cuda_stream))
     if device.index == torch.cuda.current_device():
@@ -751,18 +754,44 @@ def jagged_attention(q, k, v, q_offsets, kv_offsets, bias=None, bias_center=0, s
                                  jb_offsets)
 
 
+def _check_capture(*inputs):
+    """Refuses to capture a step whose gradients would be accumulated outside the capture.
+
+    While an eager graph of a leaf lives, the leaf's gradient is accumulated on the stream that
+    this graph was made on.  Made on the default stream, that is work which a capture cannot hold,
+    and a backward pass captured then ends the process.  So an eager call there marks its leaves'
+    accumulators, and a captured call refuses a marked one.  (A graph made on a side stream joins
+    the capture, and a mark is gone with its graph.)"""
+    leaves = [t for t in inputs if t.requires_grad and t.is_leaf]
+    if not leaves:
+        return
+    capturing = torch.cuda.is_current_stream_capturing()
+    if not capturing and torch.cuda.current_stream(leaves[0].device).cuda_stream != 0:
+        return
+    for t in leaves:
+        node = torch.autograd.graph.get_gradient_edge(t).node
+        if not capturing:
+            node.metadata["jfa_default_stream"] = True
+        elif node.metadata.get("jfa_default_stream"):
+            raise RuntimeError("cannot capture this call: an eager graph of the same leaf tensors, made on the default "
+                               "stream, is alive; drop its outputs first, or run eager steps on a side stream")
+
+
 class WindowAttention(torch.autograd.Function):
     """Differentiable windowed attention: out = WindowAttention.apply(q, k, v, q_offsets,
-    kv_offsets, window, sinks, scale).  lse is saved for the backward."""
+    kv_offsets, window, sinks, scale).  lse is saved for the backward, which cannot be
+    differentiated again.  A step may be captured in a CUDA graph (see _check_capture)."""
 
     @staticmethod
     def forward(ctx, q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None):
+        _check_capture(q, k, v)
         out, lse, _ = jfa_window_forward(q, k, v, q_offsets, kv_offsets, window, sinks, scale)
         ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets)
         ctx.cfg = (window, sinks, scale)
         return out
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, q_offsets, kv_offsets = ctx.saved_tensors
         dq, dk, dv, _ = jfa_window_backward(dout.contiguous(), q, k, v, out, lse, q_offsets, kv_offsets, *ctx.cfg)

@@ -43,7 +43,7 @@ def attend(c=None, **over):
     (dict(v=8200), INVALID), (dict(page_table=None), INVALID), (dict(page_table=66), INVALID),
     (dict(lengths=None), INVALID), (dict(lengths=130), INVALID),
     (dict(num_pages=1 << 27), INVALID),   # 2^27 pages x 2 heads x 16 rows: row numbers past 31 bits
-    (dict(num_pages=1 << 62), INVALID), (dict(max_pages=1 << 27), INVALID),
+    (dict(num_pages=1 << 62), INVALID), (dict(max_pages=1 << 27), INVALID), (dict(max_pages=(1 << 27) - 7), INVALID),
 ])
 def test_cache_is_checked(call, over, status):
     assert call(cache(**over)) == status
@@ -57,6 +57,9 @@ def test_cache_is_checked(call, over, status):
     (dict(q=16, qs=128, H=4, q_out=16), INVALID),     # q rows overlap
     (dict(q=16, qs=264, H=4, q_out=16), INVALID),     # in place, but strided
     (dict(k_out=16, ks=136), INVALID),
+    (dict(k_out=32), INVALID),                        # k_out is v
+    (dict(q=48, qs=256, H=4, q_out=16), INVALID), (dict(q=48, qs=256, H=4, q_out=32), INVALID),
+    (dict(q=48, qs=256, H=4, q_out=64, k_out=64), INVALID), (dict(q=48, qs=256, H=4, q_out=64, k_out=48), INVALID),
     (dict(rot=66), INVALID), (dict(rot=-16), INVALID), (dict(rot=24), UNSUPPORTED), (dict(ws=None), WORKSPACE),
     (dict(ws=128), WORKSPACE), (dict(wsb=255), WORKSPACE),
 ])

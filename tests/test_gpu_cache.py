@@ -347,6 +347,49 @@ def test_decoding_steps_in_a_graph():
     assert jfa.jfa_check_status(ws) == 0
 
 
+def test_pages_beyond_4_billion_elements():
+    """The last pages of caches of 2^32 elements and more."""
+    g, G, d, page, B = gen(14), 2, 128, 128, 3
+    P = (1 << 32) // (G * page * d) + 8
+    kc = torch.empty(P, G, page, d, dtype=BF16, device=DEV)
+    vc = torch.empty_like(kc)
+    table = (P - 1 - torch.arange(2 * B, device=DEV, dtype=torch.int32)).view(B, 2)
+    n = torch.tensor([0, 100, 255], dtype=torch.int32, device=DEV)
+    for b in range(B):
+        for t in (kc, vc):
+            if n[b]:
+                fill(t, table, b, range(int(n[b])), normal(g, int(n[b]), G, d))
+    k, v, q, off = normal(g, B, G, d), normal(g, B, G, d), normal(g, B, 4, d), torch.arange(B + 1, device=DEV)
+    f = jfa.rotary_frequencies(d)
+    k_out = torch.empty_like(k)
+    q2, _, n2, ws = jfa.jfa_cache_append(k, v, off, kc, vc, table, n, q=q, frequencies=f, k_out=k_out)
+    assert jfa.jfa_check_status(ws) == 0 and n2.tolist() == [1, 101, 256]
+    close(k_out, orc.rotate(k, n.cpu().numpy(), f), "k_out")
+    for b in range(B):
+        at = table[b, int(n[b]) // page].long(), slice(None), int(n[b]) % page
+        assert torch.equal(kc[at], k_out[b]) and torch.equal(vc[at], v[b])
+    check_attention(q2, kc, vc, table, n2, None, 0)
+
+
+def test_two_calls_at_once():
+    g = gen(15)
+    calls = []
+    for lens, H, G in (([9000, 300, 0, 5000], 4, 2), ([200] * 150 + [7000], 8, 1)):
+        k, v, table, n = filled(g, lens, G, 128, 64)
+        q = normal(g, len(lens), H, 128)
+        ws = jfa.new_cache_workspace(len(lens), H, G, 128, DEV)
+        calls.append(((q, k, v, table, n, 4000, 9), ws, torch.cuda.Stream(), jfa.jfa_cache_attention(q, k, v, table, n, 4000, 9)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (args, ws, side, _) in enumerate(calls):
+            got[i].append(jfa.jfa_cache_attention(*args, workspace=ws, stream=side))
+    torch.cuda.synchronize()
+    for (_, ws, side, want), results in zip(calls, got):
+        assert jfa.jfa_check_status(ws, side) == 0
+        assert all(torch.equal(r[0], want[0]) and torch.equal(r[1], want[1]) for r in results)
+
+
 def test_calls_on_a_side_stream():
     g = gen(12)
     k, v, table, n = filled(g, [300, 70], 2, 64, 16)

@@ -1,6 +1,6 @@
 """Windowed jagged attention with sinks on the GPU, both directions, against float64 with
 elementwise bounds (oracle/window_oracle.py)."""
-import math
+import types
 
 import numpy as np
 import pytest
@@ -177,6 +177,67 @@ def test_autograd_with_shared_heads():
     assert torch.equal(g, x["q"].grad)
 
 
+def test_gradients_are_not_differentiable():
+    x, dout = make([40], [40], 1, 1, 64, 14)
+    q = x["q"].requires_grad_()
+    out = jfa.window_attention(*x.values(), 8, 1)
+    (g,) = torch.autograd.grad(out, q, dout.requires_grad_(), create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        g.float().sum().backward()
+
+
+def test_autograd_in_a_graph():
+    """A captured forward and backward pass of leaf tensors; refused while an eager graph of them,
+    made on the default stream, is alive (its accumulators would run outside the capture)."""
+    lens = [140, 33]
+    x, dout = make(lens, lens, 2, 2, 64, 15)
+    for n in ("q", "k", "v"):
+        x[n].requires_grad_()
+    out = jfa.window_attention(*x.values(), 20, 2)
+    graph = torch.cuda.CUDAGraph()
+    with pytest.raises(RuntimeError, match="eager graph"):
+        with torch.cuda.graph(graph):
+            jfa.window_attention(*x.values(), 20, 2)
+    del out, graph
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        jfa.window_attention(*x.values(), 20, 2).backward(dout)
+    torch.cuda.current_stream().wait_stream(side)
+    for n in ("q", "k", "v"):
+        x[n].grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = jfa.window_attention(*x.values(), 20, 2)
+        out.backward(dout)
+    y, do = make(lens, lens, 2, 2, 64, 16)
+    with torch.no_grad():
+        for n in ("q", "k", "v"):
+            x[n].copy_(y[n])
+        dout.copy_(do)
+    graph.replay()
+    ref = orc.window_attention(*(t.detach() for t in x.values()), 20, 2, 0.125, dout)
+    close(out, ref["out"], "out")
+    for n in ("q", "k", "v"):
+        close(x[n].grad, ref["d" + n], "d" + n)
+
+
+def test_outputs_aligned_to_16_bytes():
+    """Outputs that start on an odd multiple of 16 bytes."""
+    lens, H, G, d = [130, 5], 2, 1, 128
+    x, dout = make(lens, lens, H, G, d, 17)
+    like = lambda t: torch.empty(t.numel() + 8, dtype=t.dtype, device=DEV)[8:].view(t.shape)
+    lse = torch.empty(H * sum(lens) + 4, device=DEV)[4:].view(H, sum(lens))
+    out, _, _ = jfa.jfa_window_forward(**x, window=50, sinks=3, out=like(x["q"]), lse=lse)
+    assert out.data_ptr() % 32 == 16
+    want, wl, _ = jfa.jfa_window_forward(**x, window=50, sinks=3)
+    assert torch.equal(out, want) and torch.equal(lse, wl)
+    args = (dout, x["q"], x["k"], x["v"], out, lse, x["q_offsets"], x["kv_offsets"], 50, 3)
+    got = jfa.jfa_window_backward(*args, dq=like(x["q"]), dk=like(x["k"]), dv=like(x["v"]))
+    for a, b in zip(got[:3], jfa.jfa_window_backward(*args)[:3]):
+        assert torch.equal(a, b)
+
+
 def test_training_step_in_a_graph():
     lens = [200, 129, 7]
     x, dout = make(lens, lens, 2, 1, 128, 13)
@@ -224,6 +285,39 @@ def test_malformed_offsets_are_reported():
     assert jfa.jfa_check_status(ws) == 0 and torch.equal(again, out)
 
 
+def test_rows_beyond_2_billion_elements():
+    """A short sequence behind one whose rows fill 2^31 elements: as if it were alone."""
+    H, G, d, W, S = 16, 1, 128, 16, 2
+    lens = [(1 << 31) // (H * d) + 77, 40, 0, 130]
+    x, dout = make(lens, lens, H, G, d, 18)
+    out, lse, _ = jfa.jfa_window_forward(**x, window=W, sinks=S)
+    dq, dk, dv, ws = jfa.jfa_window_backward(dout, x["q"], x["k"], x["v"], out, lse, x["q_offsets"], x["kv_offsets"], W, S)
+    assert jfa.jfa_check_status(ws) == 0
+    r = slice(lens[0], None)
+    off = offsets(lens[1:])
+    ref = orc.window_attention(x["q"][r], x["k"][r], x["v"][r], off, off, W, S, d ** -0.5, dout[r])
+    for n, t in (("out", out[r]), ("lse", lse[:, r]), ("dq", dq[r]), ("dk", dk[r]), ("dv", dv[r])):
+        close(t, ref[n], n)
+
+
+def test_two_calls_at_once():
+    calls = []
+    for i, (lens, H, G, d) in enumerate([([700, 1, 300, 0, 1290], 4, 2, 64), ([513] * 9, 2, 2, 128)]):
+        x, dout = make(lens, lens, H, G, d, 30 + i)
+        want = check(x, None, 100, 7)
+        grads = jfa.jfa_window_backward(dout, x["q"], x["k"], x["v"], *want, x["q_offsets"], x["kv_offsets"], 100, 7)[:3]
+        calls.append((x, dout, (*want, *grads), torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for x, dout, _, side, got in calls:
+            out, lse, _ = jfa.jfa_window_forward(**x, window=100, sinks=7, stream=side)
+            got.append((out, lse, *jfa.jfa_window_backward(dout, x["q"], x["k"], x["v"], out, lse, x["q_offsets"],
+                                                           x["kv_offsets"], 100, 7, stream=side)[:3]))
+    torch.cuda.synchronize()
+    for _, _, want, _, got in calls:
+        assert all(torch.equal(a, b) for r in got for a, b in zip(r, want))
+
+
 def test_side_stream():
     x, dout = make([300], [300], 2, 1, 64, 15)
     want = jfa.jfa_window_forward(**x, window=64, sinks=2)
@@ -238,7 +332,8 @@ def test_refusals_of_the_binding():
     for bad in (dict(q=x["q"].float()), dict(k=x["k"][:, :1].expand(20, 3, 64).contiguous()), dict(v=x["v"][:10]),
                 dict(q=x["q"][:, ::2]), dict(window=0), dict(sinks=-1), dict(kv_offsets=offsets([10, 10])),
                 dict(q_offsets=x["q_offsets"].int()), dict(out=x["k"]), dict(lse=torch.empty(4, 4, device=DEV)),
-                dict(workspace=torch.zeros(256, dtype=torch.uint8, device=DEV))):
+                dict(workspace=torch.zeros(256, dtype=torch.uint8, device=DEV)),
+                dict(stream=types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0))):
         with pytest.raises(ValueError):
             jfa.jfa_window_forward(**{**dict(x, window=4, sinks=0), **bad})
     with pytest.raises(jfa.JfaError):
