@@ -240,7 +240,6 @@ jfa_status window_maps(PlanMaps* maps, const Problem& pr, const void* q, const v
     jfa_status st = encode_template(&maps->tmpl[i], base[i], rows, heads, pr.d, kv ? keys : kBM);
     if (st == JFA_OK && kv) st = encode_template(&maps->sink_tmpl[i - kMapK], base[i], rows, heads, pr.d, sink_box);
     if (st != JFA_OK) return st;
-    maps->tile_rows[i] = kv ? keys : kBM;
     maps->base[i] = base[i];
     maps->row_bytes[i] = uint32_t(heads) * uint32_t(pr.d) * 2;
     maps->used[i] = 1;
@@ -300,7 +299,6 @@ jfa_status jfa_forward(const void* q, const void* k, const void* v, const int64_
   maps.base[kMapV] = vbase;
   for (int i = 0; i < 3; ++i) {
     maps.row_bytes[i] = uint32_t(H) * uint32_t(d) * 2;
-    maps.tile_rows[i] = kBM;
     maps.used[i] = 1;
   }
   {
@@ -355,7 +353,6 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
   maps.base[kMapDO] = dobase;
   for (int i = 0; i < kNumMapSlots; ++i) {
     maps.row_bytes[i] = uint32_t(H) * uint32_t(d) * 2;
-    maps.tile_rows[i] = kBM;
     maps.used[i] = 1;
   }
   if (pr.jb_grad)  // pairs no pass visits (hidden by the causal mask) and the row padding read as 0

@@ -31,7 +31,6 @@ struct PlanMaps {
   CUtensorMap sink_tmpl[2];        // window: K and V again, with boxes for the sinks
   const void* base[kNumMapSlots];  // tensor base pointers (row 0)
   uint32_t row_bytes[kNumMapSlots];
-  int tile_rows[kNumMapSlots];         // rows of the tiles that the kernels load through each map
   int used[kNumMapSlots];
 };
 

@@ -261,9 +261,9 @@ __global__ void __launch_bounds__(kWinThreads, 2)
         auto fill = [&](int slot, int j, Ring<R>& r, uint64_t* full, uint64_t* empty, uint8_t* smem_tiles) {
           const bool sink = j < w.nz;
           const TileMap m =
-              sink ? win_tile_map(nullptr, p.smaps, p.B, slot, w.b, w.ko - w.org, j, w.ns, p.total_kv, kWinKeys)
-                   : win_tile_map(slot == kMapK ? whole_k : whole_v, p.maps, p.B, slot, w.b, w.ko, w.a + j - w.nz, w.Lk,
-                                  p.total_kv, kWinKeys, w.skip);
+              sink ? win_tile_map(nullptr, p.smaps, slot, w.b, 0, j, 0, kWinKeys, 0)
+                   : win_tile_map(slot == kMapK ? whole_k : whole_v, p.maps, slot, w.b, w.ko, w.a + j - w.nz, w.Lk,
+                                  kWinKeys, w.skip);
           if (m.tail) tmap_acquire(m.map);
           if (!mbar_wait(&empty[r.e], r.ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
           trace_event(p.trace, kTraceProducer, tn, slot);
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       // the last scores of the previous tile have read the buffer
       if (!warp_wait(&q_empty, (n_q & 1) ^ 1, abort_flag)) { ok = false; break; }
       if (lane == 0) {
-        const TileMap m = win_tile_map(p.whole ? &q_map : nullptr, p.maps, p.B, kMapQ, w.b, w.qo, w.t, w.Lq, p.total_q);
+        const TileMap m = win_tile_map(p.whole ? &q_map : nullptr, p.maps, kMapQ, w.b, w.qo, w.t, w.Lq, kBM, 0);
         if (m.tail) tmap_acquire(m.map);
         trace_event(p.trace, kTraceLoader, tn, 1);
         mbar_arrive_expect_tx(&q_full, C::kQBytes);

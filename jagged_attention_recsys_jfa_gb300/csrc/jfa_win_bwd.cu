@@ -119,7 +119,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
-        const int64_t k0 = wi.ko;
         acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
         if (p.win.sinks > 0) acquire_seq_maps(p.smaps, wi.b, kMapK, kMapV, acq_s, false);
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
@@ -127,14 +126,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
           if (count_of(ku) == 0) continue;
           const bool sink = ku.chunk >= 0;
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
-          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
           const int skip = !sink ? meta_win(wi).skip : 0;
-          const TileMap mk = win_tile_map(maps, p.B, kMapK, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
-          const TileMap mv = win_tile_map(maps, p.B, kMapV, wi.b, row0, sink ? 0 : kt, p.total_kv, kBN, skip);
-          if (mk.tail) {
-            tmap_acquire(mk.map);
-            tmap_acquire(mv.map);
-          }
+          const TileMap mk = win_tile_map(maps, kMapK, wi.b, sink ? 0 : kt, kBN, skip);
+          const TileMap mv = win_tile_map(maps, kMapV, wi.b, sink ? 0 : kt, kBN, skip);
           if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
           mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
@@ -147,8 +141,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
             const ItemMeta* wn = meta_peek_next(meta, item_k);
             if (wn && wn->u0 * kBN < wn->Lk) {
               acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
-              win_prefetch_tile<D / 64>(p.maps, p.B, kMapK, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
-              win_prefetch_tile<D / 64>(p.maps, p.B, kMapV, wn->b, wn->ko, wn->u0, p.total_kv, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64>(p.maps, kMapK, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64>(p.maps, kMapV, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
             }
           }
         }
@@ -165,7 +159,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
       bool ok = true;
       auto fill = [&](const TileMap& m, int col, const float* l2src, const float* dsrc) {
         const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
-        if (m.tail) tmap_acquire(m.map);
         if (!mbar_wait(&ring_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
         trace_event(p.trace, kTraceProducer, tn, 2);
         mbar_arrive_expect_tx(&ring_full[e], C::kTileBytes + (l2src ? 2 * kBM * 4 : 0));
@@ -183,26 +176,24 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
         if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
         const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
-        const int64_t q0 = wi.qo;
         acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
         for (int kt = wi.u0; kt < wi.u1 && ok; ++kt) {
           const WinKeyUnit ku = key_unit(p, wi, kt);
           if (const ItemMeta* wnp = meta_peek_next(meta, item_k)) {
             // the first query tiles of this CTA's next item into L2 meanwhile
             const WinKeyUnit nu = key_unit(p, *wnp, wnp->u0);
-            const int64_t nqo = wnp->qo;
             acquire_seq_maps(p.maps, wnp->b, kMapQ, kMapDO, acq_b, true);
             for (int r = 0; r < min(count_of(nu), 2); ++r) {
               const int t = nu.first + (nu.r0 + r) % nu.n, col = (wnp->h * p.group + (nu.r0 + r) / nu.n) * D;
-              prefetch_tile<D / 64>(p.maps, p.B, kMapDO, wnp->b, nqo, t, p.total_q, col);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapQ, wnp->b, nqo, t, p.total_q, col);
+              win_prefetch_tile<D / 64>(p.maps, kMapDO, wnp->b, t, col, 0);
+              win_prefetch_tile<D / 64>(p.maps, kMapQ, wnp->b, t, col, 0);
             }
           }
           for (int i = 0; i < count_of(ku) && ok; ++i) {
             const int qt = ku.first + (ku.r0 + i) % ku.n, qh = wi.h * p.group + (ku.r0 + i) / ku.n;
             const int64_t vec0 = int64_t(qh) * p.qpad_cap + wi.qp;
-            const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
-            const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
+            const TileMap mdo = win_tile_map(p.maps, kMapDO, wi.b, qt, kBM, 0);
+            const TileMap mq = win_tile_map(p.maps, kMapQ, wi.b, qt, kBM, 0);
             if (!fill(mdo, qh * D, nullptr, nullptr)) { ok = false; break; }
             if (!fill(mq, qh * D, p.lse2 + vec0 + qt * kBM, p.delta + vec0 + qt * kBM)) {
               ok = false;
@@ -583,16 +574,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int64_t q0 = wi.qo;
        acquire_seq_maps(p.maps, wi.b, kMapQ, kMapDO, acq_b, false);
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
         if (query_unit(p, wi, qt).nkv == 0) continue;
-        const TileMap mq = tile_map(p.maps, p.B, kMapQ, wi.b, q0, qt, p.total_q);
-        const TileMap mdo = tile_map(p.maps, p.B, kMapDO, wi.b, q0, qt, p.total_q);
-        if (mq.tail) {
-          tmap_acquire(mq.map);
-          tmap_acquire(mdo.map);
-        }
+        const TileMap mq = win_tile_map(p.maps, kMapQ, wi.b, qt, kBM, 0);
+        const TileMap mdo = win_tile_map(p.maps, kMapDO, wi.b, qt, kBM, 0);
         if (!mbar_wait(&qdo_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
         trace_event(p.trace, kTraceLoader, tn, 1);
         mbar_arrive_expect_tx(&qdo_full, 2 * C::kTileBytes);
@@ -612,8 +598,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
             const int64_t nqo = p.q_off[nb];
             acquire_seq_maps(p.maps, nb, kMapQ, kMapDO, acq_b, true);
             if (nt * kBM < int(p.q_off[nb + 1] - nqo)) {
-              prefetch_tile<D / 64>(p.maps, p.B, kMapQ, nb, nqo, nt, p.total_q, nh * D);
-              prefetch_tile<D / 64>(p.maps, p.B, kMapDO, nb, nqo, nt, p.total_q, nh * D);
+              win_prefetch_tile<D / 64>(p.maps, kMapQ, nb, nt, nh * D, 0);
+              win_prefetch_tile<D / 64>(p.maps, kMapDO, nb, nt, nh * D, 0);
             }
           }
         }
@@ -631,7 +617,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
       bool ok = true;
       auto fill = [&](const TileMap& m, int col, uint32_t bytes) {
         const uint32_t e = ring_n % R, ph = (ring_n / R) & 1;
-        if (m.tail) tmap_acquire(m.map);
         if (!mbar_wait(&ring_empty[e], ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
         trace_event(p.trace, kTraceProducer, tn, 2);
         mbar_arrive_expect_tx(&ring_full[e], bytes);
@@ -644,7 +629,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
        if (!meta_wait(meta, item_k, abort_flag)) { ok = false; break; }
        const ItemMeta& wi = meta.e[item_k % kMetaSlots];  // read in place, freed after the item
        if (wi.b < 0) break;  // end of this CTA's items
-       const int64_t k0 = wi.ko;
        const int col = wi.h / p.group * D;  // first column of the key/value head
        acquire_seq_maps(p.maps, wi.b, kMapK, kMapV, acq_b, false);
        if (p.win.sinks > 0) acquire_seq_maps(p.smaps, wi.b, kMapK, kMapV, acq_s, false);
@@ -657,18 +641,17 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
           const int skip = meta_win(*wnp).skip;
           acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
           for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
-            win_prefetch_tile<D / 64>(p.maps, p.B, kMapV, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
-            win_prefetch_tile<D / 64>(p.maps, p.B, kMapK, wnp->b, wnp->ko, t, p.total_kv, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64>(p.maps, kMapV, wnp->b, t, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64>(p.maps, kMapK, wnp->b, t, wnp->h / p.group * D, skip);
           }
         }
         for (int jt = 0; jt < nkv && ok; ++jt) {
           const bool sink = jt < qu.nz;
           const CUtensorMap* maps = sink ? p.smaps : p.maps;
-          const int64_t row0 = sink ? k0 - meta_win(wi).org : k0;
           const int kt = sink ? 0 : qu.a + jt - qu.nz;
           const int skip = !sink ? meta_win(wi).skip : 0;
-          const TileMap mv = win_tile_map(maps, p.B, kMapV, wi.b, row0, kt, p.total_kv, kBN, skip);
-          const TileMap mk = win_tile_map(maps, p.B, kMapK, wi.b, row0, kt, p.total_kv, kBN, skip);
+          const TileMap mv = win_tile_map(maps, kMapV, wi.b, kt, kBN, skip);
+          const TileMap mk = win_tile_map(maps, kMapK, wi.b, kt, kBN, skip);
           const uint32_t bytes = sink ? uint32_t(p.sink_rows) * D * 2 : uint32_t(C::kTileBytes);
           if (!fill(mv, col, bytes) || !fill(mk, col, bytes)) { ok = false; break; }
         }

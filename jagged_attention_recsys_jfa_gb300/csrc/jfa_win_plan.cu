@@ -145,66 +145,49 @@ __global__ void __launch_bounds__(1024, 1) win_plan_kernel(const __grid_constant
   if (int(blockIdx.x) >= list_ctas) {
     const size_t gt = size_t(blockIdx.x - list_ctas) * blockDim.x + tid;
     const size_t gstride = size_t(gridDim.x - list_ctas) * blockDim.x;
-    // ---- tail copies: the last min(128, total) rows of each tensor, which the boxes that
-    //      would otherwise read past the tensor's last row load from instead
+    // ---- the tensors' last rows, which maps that start close to their end load from (zone_bytes)
+    const size_t stride = zone_stride(p.L.row_bytes);
     for (int slot = 0; slot < kNumMapSlots; ++slot) {
       if (!maps.used[slot]) continue;
       const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
       if (total <= 0) continue;
-      const int64_t n = total < kBM ? total : kBM;
       const size_t rb = maps.row_bytes[slot];
+      const int64_t n = zone_rows(total, rb);
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(maps.base[slot]) +
                                                         size_t(total - n) * rb);
-      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes);
+      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * stride);
       const size_t nvec = size_t(n) * rb / 16;
       for (size_t i = gt; i < nvec; i += gstride) dst[i] = src[i];
     }
-    // ---- per-sequence tensor maps: copy the template, point it at the sequence's first
-    //      row and clip its row extent to the sequence length.  A sequence whose last tile
-    //      would reach past the tensor's last row also gets a tail map over the tail copy,
-    //      pointed at that tile's first row and clipped to the tile's rows.  (With invalid
-    //      offsets CTA 0 leaves every list empty, so no map is used; a tail map is only
-    //      written for a sequence inside its tensor, which keeps its index in range.)
+    // ---- per-sequence tensor maps: copy the template, point it at the sequence's first row (of its
+    //      window part, of its sinks) and clip its row extent.  (With invalid offsets CTA 0 leaves
+    //      every list empty, so no map is used.)
     //      One warp per map: the replaces of a warp's lanes are done one after another, so lanes
     //      that each wrote a map would be what the planner waits for.
     const int sets = p.win.sinks > 0 ? 2 : 1;  // maps, and the sinks' maps
     const int lane = tid & 31;
-    for (size_t job = gt / 32; job < size_t(p.B) * kNumMapSlots * 2 * sets; job += gstride / 32) {
-      const bool tail = job & 1, sink = sets == 2 && ((job >> 1) & 1);
-      const size_t idx = job / (2 * sets);
+    for (size_t job = gt / 32; job < size_t(p.B) * kNumMapSlots * sets; job += gstride / 32) {
+      const bool sink = sets == 2 && (job & 1);
+      const size_t idx = job / sets;
       const int b = int(idx / kNumMapSlots), slot = int(idx % kNumMapSlots);
       if (!maps.used[slot]) continue;
       const bool is_q_side = (slot == kMapQ || slot == kMapDO);
       int64_t row0 = is_q_side ? p.q_off[b] : p.kv_off[b];
       int64_t len = (is_q_side ? p.q_off[b + 1] : p.kv_off[b + 1]) - row0;
-      int skip = 0;  // empty rows in front of the first key's tile
       if (is_q_side && sink) continue;
       if (!is_q_side) {  // the sinks, or the window part
         const int64_t lq = p.q_off[b + 1] - p.q_off[b];
         if (lq < 0 || len < 0 || lq > (int64_t(1) << 30) || len > (int64_t(1) << 30)) continue;
         const WinSeq ws = plan_seq(p, int(lq), int(len));
-        skip = sink ? 0 : ws.skip;
         if (!sink) row0 += ws.org + ws.skip;
         len = sink ? ws.ns : ws.Lk - ws.skip;
       }
       const size_t rb = maps.row_bytes[slot];
-      const int rows = maps.tile_rows[slot];
       const int64_t total = is_q_side ? p.total_q : p.total_kv;
-      CUtensorMap* dst = reinterpret_cast<CUtensorMap*>(p.ws + (sink ? p.L.smaps : p.L.maps));
-      const void* base;
-      if (!tail) {
-        dst += idx;
-        base = static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb);
-      } else {
-        if (len <= 0 || row0 < 0 || row0 + len > total) continue;
-        // the sequence's last tile: its box's first row, and its first row that holds something
-        const int64_t g0 = row0 - skip + (skip + len - 1) / rows * rows, r0 = g0 > row0 ? g0 : row0;
-        if (g0 + rows <= total) continue;
-        const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
-        dst += size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(r0 + rows - total);
-        base = p.ws + p.L.tail + size_t(slot) * kTailRows * p.L.row_bytes + size_t(r0 - (total - n)) * rb;
-        len = row0 + len - r0;
-      }
+      const void* base = static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb);
+      if (in_zone(row0, total, rb))
+        base = p.ws + p.L.tail + size_t(slot) * stride + (row0 - (total - zone_rows(total, rb))) * int64_t(rb);
+      CUtensorMap* dst = reinterpret_cast<CUtensorMap*>(p.ws + (sink ? p.L.smaps : p.L.maps)) + idx;
       const uint4* src = reinterpret_cast<const uint4*>(sink ? &maps.sink_tmpl[slot - kMapK] : &maps.tmpl[slot]);
       if (lane < 8) reinterpret_cast<uint4*>(dst)[lane] = src[lane];
       __syncwarp();
@@ -260,7 +243,7 @@ cudaError_t launch_win_plan(const Problem& pr, const PlanMaps& maps, void* ws, c
   const PlanParams p = plan_params(pr, ws, L, backward, backward ? num_sms : kWinCtasPerSm * num_sms);
   // one CTA per list; helpers for the maps (one warp each) and tail copies
   const int sets = pr.win.sinks > 0 ? 2 : 1;
-  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots * 2 * sets + 31) / 32;
+  const long long map_ctas = (static_cast<long long>(pr.B) * kNumMapSlots * sets + 31) / 32;
   const int helpers = int(map_ctas < 8 ? 8 : map_ctas > 120 ? 120 : map_ctas);
   return launch_pdl(win_plan_kernel, dim3((backward ? 2 : 1) + helpers), dim3(1024), 0, stream, maps, p);
 }

@@ -285,6 +285,28 @@ def test_malformed_offsets_are_reported():
     assert jfa.jfa_check_status(ws) == 0 and torch.equal(again, out)
 
 
+@pytest.mark.parametrize("S", [0, 3, 16, 40])
+def test_tensors_that_fill_their_memory(S):
+    """Short sequences at the end of tensors that end with their allocation: loads of partial tiles
+    must not touch what lies behind.  (A key row of 128 bytes; the sizes are whole 2 MB pages.)"""
+    H, G, d, W = 8, 1, 64, 64
+    lens = np.random.RandomState(3).randint(0, 21, 20000)
+    lens = lens[:np.searchsorted(np.cumsum(lens), 163840)]
+    lens = [int(x) for x in lens] + [163840 - int(lens.sum())]
+    torch.cuda.empty_cache()
+    x, dout = make(lens, lens, H, G, d, 19)
+    out, lse, ws = jfa.jfa_window_forward(**x, window=W, sinks=S)
+    dq, dk, dv, wb = jfa.jfa_window_backward(dout, x["q"], x["k"], x["v"], out, lse, x["q_offsets"], x["kv_offsets"], W, S)
+    assert jfa.jfa_check_status(ws) == 0 and jfa.jfa_check_status(wb) == 0
+    for part in (slice(0, 120), slice(len(lens) - 120, None)):
+        first = sum(lens[:part.start])
+        n = sum(lens[part])
+        r, off = slice(first, first + n), offsets(lens[part])
+        ref = orc.window_attention(x["q"][r], x["k"][r], x["v"][r], off, off, W, S, d ** -0.5, dout[r])
+        for name, t in (("out", out[r]), ("lse", lse[:, r]), ("dq", dq[r]), ("dk", dk[r]), ("dv", dv[r])):
+            close(t, ref[name], name)
+
+
 def test_rows_beyond_2_billion_elements():
     """A short sequence behind one whose rows fill 2^31 elements: as if it were alone."""
     H, G, d, W, S = 16, 1, 128, 16, 2
