@@ -144,7 +144,7 @@ static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 struct WsLayout {
   size_t maps = 0;       // CUtensorMap[B][kNumMapSlots], then CUtensorMap[kNumMapSlots][kTailMaps]
   size_t tail = 0;       // per used slot: kTailRows rows of the tensor's row pitch (tail copies);
-                         // windowed: its last zone_rows
+                         // windowed calls and narrow rows: its last zone_rows
   size_t row_bytes = 0;  // H * d * 2, the row pitch of q, k, v, dout
   size_t fwd = 0;      // WorkItem[cap_fwd]
   size_t dq = 0;       // WorkItem[cap_dq]
@@ -178,6 +178,9 @@ __host__ __device__ inline int64_t zone_rows(int64_t total, int64_t row_bytes) {
 __host__ __device__ inline bool in_zone(int64_t row0, int64_t total, int64_t row_bytes) {
   return (total - row0) * row_bytes < zone_bytes(row_bytes);
 }
+// The plain call's tail maps (tiles whose box reaches past the tensor's last row) leave a box 128 rows
+// or more, which is enough unless rows are this narrow; then its maps point into the copy as well.
+__host__ __device__ inline bool narrow_rows(int64_t row_bytes) { return row_bytes <= 1024; }
 // The copies lie one behind the other, a tensor of fewer heads in the space of the queries'.
 __host__ __device__ inline size_t zone_stride(size_t row_bytes) {
   return align_up(size_t(zone_bytes(int64_t(row_bytes))) + row_bytes, 1024);
@@ -230,8 +233,9 @@ __host__ __device__ inline WsLayout make_layout(int B, int H, int d, int64_t tot
   off = L.maps + (size_t(B) + (windowed ? 0 : kTailMaps)) * kNumMapSlots * 128;
   L.row_bytes = size_t(H) * size_t(d) * 2;
   L.tail = align_up(off, 1024);
-  off = L.tail + (windowed ? size_t(backward ? 4 : 3) * zone_stride(L.row_bytes) + size_t(zone_bytes(int64_t(L.row_bytes)))
-                           : size_t(backward ? 4 : 3) * kTailRows * L.row_bytes);
+  off = L.tail + (windowed || narrow_rows(L.row_bytes)
+                      ? size_t(backward ? 4 : 3) * zone_stride(L.row_bytes) + size_t(zone_bytes(int64_t(L.row_bytes)))
+                      : size_t(backward ? 4 : 3) * kTailRows * L.row_bytes);
   // windowed lists: one entry per query tile (key tile, chunk of the sinks) for all heads
   L.cap_fwd = windowed ? total_q / 128 + B + 1 : int64_t(H) * (total_q / 256 + B + 1);
   L.fwd = align_up(off, 16);

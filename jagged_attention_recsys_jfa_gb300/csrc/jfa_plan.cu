@@ -184,16 +184,19 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
     if (p.bias_grad)
       for (size_t i = gt; i < size_t(p.H) * p.nb; i += gstride) p.bias_grad[i] = 0.f;
     // ---- tail copies: the last min(128, total) rows of each tensor, which the boxes that
-    //      would otherwise read past the tensor's last row load from instead
+    //      would otherwise read past the tensor's last row load from instead (narrow rows: the
+    //      last zone_rows, which the maps of the last sequences point into)
     const size_t rb = p.L.row_bytes;
+    const bool narrow = narrow_rows(rb);
+    const size_t stride = narrow ? zone_stride(rb) : size_t(kTailRows) * rb;  // between the tensors' copies
     for (int slot = 0; slot < kNumMapSlots; ++slot) {
       if (!maps.used[slot]) continue;
       const int64_t total = (slot == kMapQ || slot == kMapDO) ? p.total_q : p.total_kv;
       if (total <= 0) continue;
-      const int64_t n = total < kBM ? total : kBM;
+      const int64_t n = narrow ? zone_rows(total, rb) : total < kBM ? total : kBM;
       const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(maps.base[slot]) +
                                                         size_t(total - n) * rb);
-      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * kTailRows * rb);
+      uint4* dst = reinterpret_cast<uint4*>(p.ws + p.L.tail + size_t(slot) * stride);
       const size_t nvec = size_t(n) * rb / 16;
       for (size_t i = gt; i < nvec; i += gstride) dst[i] = src[i];
     }
@@ -215,19 +218,22 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       uint4* d4 = reinterpret_cast<uint4*>(dst);
 #pragma unroll
       for (int i = 0; i < 8; ++i) d4[i] = src[i];
-      tmap_replace_address(dst, static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb));
-      tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
       const int64_t total = is_q_side ? p.total_q : p.total_kv;
+      const int64_t n = narrow ? zone_rows(total, rb) : total < kBM ? total : kBM;  // the copy starts at row total - n
+      const uint8_t* copy = p.ws + p.L.tail + size_t(slot) * stride;
+      tmap_replace_address(dst, narrow && in_zone(row0, total, rb)
+                                    ? copy + (row0 - (total - n)) * int64_t(rb)
+                                    : static_cast<const uint8_t*>(maps.base[slot]) + row0 * int64_t(rb));
+      tmap_replace_dim1(dst, uint32_t(len > 0 ? len : 1));
       if (len <= 0 || row0 < 0 || row0 + len > total) continue;
       const int64_t g0 = row0 + (len - 1) / kBM * kBM;  // first row of the sequence's last tile
       if (g0 + kBM > total) {
-        const int64_t n = total < kBM ? total : kBM;  // rows in the tail copy; it starts at row total - n
         CUtensorMap* tdst =
             out_maps + size_t(p.B) * kNumMapSlots + size_t(slot) * kTailMaps + size_t(g0 + kBM - total);
         uint4* t4 = reinterpret_cast<uint4*>(tdst);
 #pragma unroll
         for (int i = 0; i < 8; ++i) t4[i] = src[i];
-        tmap_replace_address(tdst, p.ws + p.L.tail + size_t(slot) * kTailRows * rb + size_t(g0 - (total - n)) * rb);
+        tmap_replace_address(tdst, copy + size_t(g0 - (total - n)) * rb);
         tmap_replace_dim1(tdst, uint32_t(row0 + len - g0));
       }
     }
