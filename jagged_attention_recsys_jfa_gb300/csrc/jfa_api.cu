@@ -223,7 +223,7 @@ jfa_status check_window(int H, int H_kv, int d, int64_t total_kv, int window, in
 
 // The templates of a windowed call: K and V have H_kv heads, and maps of their own for the sinks.
 // The forward loads them in tiles of kWinKeys rows, the backward of kBN.
-jfa_status window_maps(PlanMaps* maps, const Problem& pr, const void* q, const void* k, const void* v, const void* dout,
+jfa_status window_maps(WinPlanMaps* maps, const Problem& pr, const void* q, const void* k, const void* v, const void* dout,
                        bool backward) {
   std::memset(maps, 0, sizeof(*maps));
   const int G = pr.win.H_kv;
@@ -412,7 +412,7 @@ jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  PlanMaps maps;
+  WinPlanMaps maps;
   if ((st = window_maps(&maps, pr, q, k, v, nullptr, false)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);
@@ -449,7 +449,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  PlanMaps maps;
+  WinPlanMaps maps;
   if ((st = window_maps(&maps, pr, q, k, v, dout, true)) != JFA_OK) return st;
   {
     KernelTimer t(JFA_KERNEL_PLAN, s);

@@ -28,10 +28,14 @@ struct Problem {
 
 struct PlanMaps {
   CUtensorMap tmpl[kNumMapSlots];  // whole-tensor templates; the planner patches per-sequence copies
-  CUtensorMap sink_tmpl[2];        // window: K and V again, with boxes for the sinks
   const void* base[kNumMapSlots];  // tensor base pointers (row 0)
   uint32_t row_bytes[kNumMapSlots];
   int used[kNumMapSlots];
+};
+
+// A windowed call's: K and V again, with boxes for the sinks.
+struct WinPlanMaps : PlanMaps {
+  CUtensorMap sink_tmpl[2];
 };
 
 // Record which CUDA call failed (what jfa_last_error then returns, for the calling thread)
@@ -85,7 +89,7 @@ cudaError_t launch_forward(const Problem& p, void* ws, const WsLayout& L, void* 
                            int num_sms, cudaStream_t stream);
 
 // ---- windowed call (jfa_win_plan.cu, jfa_win.cu, jfa_win_bwd.cu; its preprocess is launch_bwd_preprocess)
-cudaError_t launch_win_plan(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, bool backward,
+cudaError_t launch_win_plan(const Problem& p, const WinPlanMaps& maps, void* ws, const WsLayout& L, bool backward,
                             int num_sms, cudaStream_t stream);
 cudaError_t launch_win_forward(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse,
                                int num_sms, cudaStream_t stream);

@@ -133,7 +133,7 @@ __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items,
 // The first CTAs validate the offsets and write one work list each: the forward list, or the
 // dK/dV list (with the padded query offsets) and the dQ list.  The other CTAs write the tail
 // copies and the tensor maps in parallel.
-__global__ void __launch_bounds__(1024, 1) win_plan_kernel(const __grid_constant__ PlanMaps maps, PlanParams p) {
+__global__ void __launch_bounds__(1024, 1) win_plan_kernel(const __grid_constant__ WinPlanMaps maps, PlanParams p) {
   __shared__ int hist[kCostBuckets];
   __shared__ int base[kCostBuckets];
   const int tid = threadIdx.x;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(1024, 1) win_plan_kernel(const __grid_constant
 
 }  // namespace
 
-cudaError_t launch_win_plan(const Problem& pr, const PlanMaps& maps, void* ws, const WsLayout& L, bool backward,
+cudaError_t launch_win_plan(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, bool backward,
                             int num_sms, cudaStream_t stream) {
   const PlanParams p = plan_params(pr, ws, L, backward, backward ? num_sms : kWinCtasPerSm * num_sms);
   // one CTA per list; helpers for the maps (one warp each) and tail copies
