@@ -480,14 +480,17 @@ def _check_int32(name, t, shape, device):
 
 
 def _check_tokens(name, t, rows, heads, d, device):
-    """Token rows [T, heads, d], each row contiguous; tokens may be strided."""
+    """Token rows [T, heads, d], each row contiguous; tokens may be strided.  Returns the rows, the
+    address and the elements between tokens."""
     try:
         n, h, w = t.shape
+        step, *inner = t.stride()
+        ptr = t.data_ptr()
         if (t.dtype is _BF16 and w == d and t.device == device and (rows is None or n == rows)
-                and (heads is None or h == heads) and n > 1 and h > 0 and t.stride() == (t.stride(0), d, 1)
-                and t.stride(0) % 8 == 0 and t.stride(0) >= h * d and t.data_ptr() % 16 == 0):
-            return
-    except (AttributeError, ValueError):
+                and (heads is None or h == heads) and n > 1 and h > 0 and inner == [d, 1]
+                and step % 8 == 0 and step >= h * d and ptr % 16 == 0):
+            return n, ptr, step
+    except (AttributeError, ValueError, RuntimeError):
         pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA tensor on {device} (the library has no CPU path)")
@@ -499,6 +502,7 @@ def _check_tokens(name, t, rows, heads, d, device):
     if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or
                       (t.shape[0] > 1 and (t.stride(0) % 8 or t.stride(0) < t.shape[1] * d)) or t.data_ptr() % 16):
         raise ValueError(f"{name} needs contiguous 16-byte aligned rows, tokens a multiple of 8 elements apart")
+    return t.shape[0], t.data_ptr(), t.stride(0)
 
 
 def _cache_struct(k_cache, v_cache, page_table, lengths):
@@ -571,15 +575,14 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
     lib = load_library()
     cache = _cache_struct(k_cache, v_cache, page_table, lengths)
     device, G, d, B = k_cache.device, cache.H_kv, cache.d, cache.B
-    _check_tokens("k", k, None, G, d, device)
-    T = k.shape[0]
-    _check_tokens("v", v, T, G, d, device)
+    T, k_ptr, k_step = _check_tokens("k", k, None, G, d, device)
+    _, v_ptr, v_step = _check_tokens("v", v, T, G, d, device)
     if not (offsets.dtype is _I64 and offsets.shape == (B + 1,) and offsets.is_contiguous() and offsets.device == device):
         _check_offsets("offsets", offsets)
         raise ValueError(f"offsets must have {B + 1} entries on {device}")
-    H = 0
+    H, q_ptr, q_step = 0, None, 0
     if q is not None:
-        _check_tokens("q", q, T, None, d, device)
+        _, q_ptr, q_step = _check_tokens("q", q, T, None, d, device)
         H = q.shape[1]
     elif q_out is not None:
         raise ValueError("q_out needs q")
@@ -605,8 +608,8 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
             _check_int32("lengths_out", n, (B,), device)
         if ws is None:
             ws = _workspace(256, device)
-        st = lib.jfa_cache_append(ctypes.byref(cache), k.data_ptr(), k.stride(0), v.data_ptr(), v.stride(0),
-                                  q.data_ptr() if H else None, q.stride(0) if H else 0, H, offsets.data_ptr(), T,
+        st = lib.jfa_cache_append(ctypes.byref(cache), k_ptr, k_step, v_ptr, v_step, q_ptr if H else None,
+                                  q_step if H else 0, H, offsets.data_ptr(), T,
                                   freq_ptr, rot, 1 if interleaved else 0, qo.data_ptr() if H else None,
                                   k_out.data_ptr() if k_out is not None else None, n.data_ptr(), ws.data_ptr(),
                                   _check_workspace(ws, 256, device), handle)

@@ -322,6 +322,23 @@ def test_rows_beyond_2_billion_elements():
         close(t, ref[n], n)
 
 
+def test_one_workspace_for_calls_of_different_sizes():
+    """A workspace made for the largest call serves every smaller one, forward and backward in turn."""
+    ws = jfa.new_window_workspace(300, 8, 4, 128, 60000, 60000, 128, True, DEV)
+    calls = []
+    for i, (lens, H, G, d, W, S) in enumerate([([700, 1, 300, 0, 1290], 4, 2, 64, 100, 7), ([20] * 300, 8, 4, 128, 9, 128),
+                                               ([5000, 3, 8000], 2, 1, 128, 999, 0), ([1], 1, 1, 64, 1, 1)]):
+        x, dout = make(lens, lens, H, G, d, 40 + i)
+        o = jfa.jfa_window_forward(**x, window=W, sinks=S)[:2]
+        b = lambda ws, x=x, dout=dout, o=o, W=W, S=S: jfa.jfa_window_backward(
+            dout, x["q"], x["k"], x["v"], *o, x["q_offsets"], x["kv_offsets"], W, S, workspace=ws)[:3]
+        calls.append((lambda ws, x=x, W=W, S=S: jfa.jfa_window_forward(**x, window=W, sinks=S, workspace=ws)[:2], b, o, b(None)))
+    for i in (0, 1, 2, 3, 1, 0, 3, 2, 0):
+        f, b, o, g = calls[i]
+        assert all(torch.equal(p, r) for p, r in zip(f(ws), o)) and all(torch.equal(p, r) for p, r in zip(b(ws), g))
+    assert jfa.jfa_check_status(ws) == 0
+
+
 def test_two_calls_at_once():
     calls = []
     for i, (lens, H, G, d) in enumerate([([700, 1, 300, 0, 1290], 4, 2, 64), ([513] * 9, 2, 2, 128)]):
