@@ -33,69 +33,55 @@ __device__ __forceinline__ int win_unit_cost(const PlanParams& p, int kind, int 
 }
 
 // The windowed lists.  A window bounds what a unit can cost, so every unit is an item of its own
-// and the units, not the sequences, are dealt out to the threads: a thread finds its unit's
-// sequence in the running sums of the threads' runs of sequences (1024 of them) and walks its run
-// to it.  Long sequences then cost no more time than short ones (long-tail batch of 64 sequences:
-// 31 -> 10 us against emit_list).  Costliest first by the same counting sort.  One entry stands
+// and the units, not the sequences, are dealt out to the threads: 1024 sequences at a time, a thread
+// finds its unit's sequence in the running sums of their units.  Long sequences then cost no more
+// time than short ones (long-tail batch of 64 sequences: 31 -> 10 us against a thread per sequence).
+// Costliest first by a counting sort.  One entry stands
 // for a unit of all `heads` heads: item i of the launch is entry i / heads, head i % heads, so that
 // heads which share keys read them at the same time (and the list is written in a tenth of the time
 // that one entry per head took).
 __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items, int64_t cap, int* count_out, int* hist,
                                  int* base) {
-  __shared__ long long run_end[1024];
-  __shared__ int run_q[1024], run_k[1024];  // lengths, when a run is one sequence
-  __shared__ long long units_total, cost_total;
+  __shared__ long long seq_end[1024];       // units up to the end of each of these sequences
+  __shared__ int seq_q[1024], seq_k[1024];  // their lengths
+  __shared__ long long units, cost_total;
   __shared__ int cost_max;
   const int tid = threadIdx.x;
   const int heads = kind == kListDkv ? p.win.H_kv : p.H;
-  const int run = (p.B + 1023) / 1024;
-  auto len_q = [&](int b) { return int(p.q_off[b + 1] - p.q_off[b]); };
-  auto len_k = [&](int b) { return int(p.kv_off[b + 1] - p.kv_off[b]); };
   for (int c = tid; c < kCostBuckets; c += blockDim.x) hist[c] = 0;
   if (tid == 0) cost_max = 0;
-  long long mine = 0;
-  for (int b = tid * run; b < min(p.B, (tid + 1) * run); ++b) {
-    run_q[tid] = len_q(b);
-    run_k[tid] = len_k(b);
-    mine += win_units(p, kind, run_q[tid], run_k[tid]);
-  }
-  run_end[tid] = block_scan_incl(mine, &units_total);
-  __syncthreads();
-  const long long n = units_total;
-  if (n > cap) {  // cannot happen for valid offsets (capacities are upper bounds)
-    if (tid == 0) {
-      atomicCAS(&reinterpret_cast<WsHeader*>(p.ws)->status, 0, int(JFA_ERR_WORKSPACE));
-      *count_out = 0;
-    }
-    return;
-  }
+  int loaded = -1;  // first of the sequences in shared memory
   // calls f(active, b, unit, cost) for this thread's units, all lanes of a warp together
   auto for_units = [&](auto&& f) {
-    for (long long i = tid; i - tid < n; i += blockDim.x) {
-      int b = 0, u = 0, cost = 0;
-      if (i < n) {
-        int lo = 0, hi = 1023;  // the first run that ends behind unit i
-        while (lo < hi) {
-          const int mid = (lo + hi) >> 1;
-          if (run_end[mid] > i) hi = mid;
-          else lo = mid + 1;
+    for (int b0 = 0; b0 < p.B; b0 += 1024) {
+      if (loaded != b0) {
+        const int b = b0 + tid;
+        long long mine = 0;
+        __syncthreads();  // the sequences before have been read
+        if (b < p.B) {
+          seq_q[tid] = int(p.q_off[b + 1] - p.q_off[b]);
+          seq_k[tid] = int(p.kv_off[b + 1] - p.kv_off[b]);
+          mine = win_units(p, kind, seq_q[tid], seq_k[tid]);
         }
-        long long at = lo ? run_end[lo - 1] : 0;
-        int lq = run_q[lo], lk = run_k[lo];
-        b = lo * run;
-        if (run > 1) {
-          for (;; ++b) {
-            lq = len_q(b);
-            lk = len_k(b);
-            const int m = win_units(p, kind, lq, lk);
-            if (at + m > i) break;
-            at += m;
-          }
-        }
-        u = int(i - at);
-        cost = win_unit_cost(p, kind, u, lq, lk);
+        seq_end[tid] = block_scan_incl(mine, &units);
+        __syncthreads();
+        loaded = b0;
       }
-      f(i < n, b, u, cost);
+      const long long n = units;
+      for (long long i = tid; i - tid < n; i += blockDim.x) {
+        int lo = 0, u = 0, cost = 0;
+        if (i < n) {
+          int hi = 1023;  // the first sequence that ends behind unit i
+          while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (seq_end[mid] > i) hi = mid;
+            else lo = mid + 1;
+          }
+          u = int(i - (lo ? seq_end[lo - 1] : 0));
+          cost = win_unit_cost(p, kind, u, seq_q[lo], seq_k[lo]);
+        }
+        f(i < n, b0 + lo, u, cost);
+      }
     }
   };
   // Position of this lane's entry in its bucket.  Most units cost the same, so lanes of
@@ -119,6 +105,13 @@ __device__ void emit_window_list(const PlanParams& p, int kind, WorkItem* items,
   if ((tid & 31) == 0) atomicMax(&cost_max, mx);
   block_scan_incl(sum, &cost_total);
   const int total = scan_desc(hist, base);
+  if (total > cap) {  // cannot happen for valid offsets (capacities are upper bounds)
+    if (tid == 0) {
+      atomicCAS(&reinterpret_cast<WsHeader*>(p.ws)->status, 0, int(JFA_ERR_WORKSPACE));
+      *count_out = 0;
+    }
+    return;
+  }
   for_units([&](bool active, int b, int u, int cost) {
     const int pos = claim(base, active, bucket(cost));
     if (active) *reinterpret_cast<int4*>(items + pos) = make_int4(b, 0, u, u + 1);
