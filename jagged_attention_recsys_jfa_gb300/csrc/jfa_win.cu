@@ -27,8 +27,12 @@
 // metadata worked out by the scheduler take 115 (128 sequences of 1 to 2048 tokens, d = 64, 4 query
 // and 2 key/value heads, window 255, 4 sinks), and 172 where they take 159 (64 long-tailed sequences
 // of up to 16384 tokens, d = 128, 8 heads, window 1024, 4 sinks).  With the window's grid aligned
-// (win_seq) the two take 106 and 158.  Left to gain, by timing copies that leave work out: the
-// softmax arithmetic about 35 us of the first, half of the score products 5.
+// (win_seq) and a sequence's partial tiles through its own maps the two take 103 and 153 (floors 30
+// and 64): neither memory (16% and 46%) nor the tensor pipe (17% and 41%) sets the pace, but the
+// steps' hand-offs.  By timing copies that leave work out, the softmax arithmetic is about 35 us of
+// the first, half of the score products 5.
+//
+// P is rounded to bf16 for its product (2^-9 relative a term); scores, maximum, sum and O are fp32.
 #include <cuda_bf16.h>
 
 #include "jfa_internal.h"
