@@ -156,9 +156,9 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
  * plugins and services on a fixed, pre-planned memory arena give a kernel library
  * only its inputs and outputs and must not call cudaMalloc on their hot path (it can
  * synchronise the device and breaks the arena's budget); this call runs jfa_forward
- * with its scratch in a file-scope device array of 8 MiB that every GPU loading the
+ * with its scratch in a file-scope device array of 9 MiB that every GPU loading the
  * library holds until exit.  Arguments and results are those of jfa_forward.
- * - Sizes whose workspace (jfa_workspace_size(..., 0)) exceeds 8 MiB are rejected with
+ * - Sizes whose workspace (jfa_workspace_size(..., 0)) exceeds 9 MiB are rejected with
  *   JFA_ERR_WORKSPACE before anything is enqueued.
  * - The first call on a device looks up the array's device address (cudaGetSymbolAddress)
  *   with that device current; make that first call before any stream capture.

@@ -439,10 +439,12 @@ __device__ __forceinline__ TileMap win_tile_map(const CUtensorMap* whole, const 
   m.tail = true;  // not acquired yet
   return m;
 }
-// Pull a tile of 128 rows (boxes of 64 columns from column col0) into L2 ahead of its load.
+// Pull a tile of 128 rows (boxes of 64 columns from column col0) into L2 ahead of its load; one with
+// empty rows in front is left to its load.
 template <int kBoxes>
 __device__ __forceinline__ void win_prefetch_tile(const CUtensorMap* maps, int slot, int b, int t, int col0, int skip) {
   const TileMap m = win_tile_map(maps, slot, b, t, kBN, skip);
+  if (m.y < 0) return;
 #pragma unroll
   for (int c = 0; c < kBoxes; ++c)
     asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m.map), "r"(col0 + c * 64),

@@ -17,8 +17,8 @@ namespace {
 
 // Fixed scratch for the no-allocation forward.  Every GPU that loads this library holds
 // it until the process exits.  Its size bounds the problems this entry point accepts
-// (jfa_workspace_size(..., 0) <= 8 MiB, e.g. B = 4096 sequences, H = 8, 1M query rows).
-constexpr size_t kNoAllocScratchBytes = size_t(8) << 20;
+// (jfa_workspace_size(..., 0) <= 9 MiB, e.g. B = 4096 sequences, H = 8, 1M query rows).
+constexpr size_t kNoAllocScratchBytes = size_t(9) << 20;
 static __device__ __align__(256) unsigned char g_noalloc_scratch[kNoAllocScratchBytes];
 
 constexpr int kMaxDevices = 64;
