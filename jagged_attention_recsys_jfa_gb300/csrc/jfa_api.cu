@@ -227,7 +227,7 @@ jfa_status window_maps(WinPlanMaps* maps, const Problem& pr, const void* q, cons
                        bool backward) {
   std::memset(maps, 0, sizeof(*maps));
   const int G = pr.win.H_kv;
-  const int keys = backward ? kBN : kWinKeys, sink_box = backward ? sink_rows(pr.win.sinks) : win_sink_box(pr.win.sinks);
+  const int keys = win_key_box(pr.d, backward), sink_box = keys == kBN ? sink_rows(pr.win.sinks) : win_sink_box(pr.win.sinks);
   const void* kbase = pr.total_kv > 0 ? k : q;  // maps of a side without rows are never read
   const void* vbase = pr.total_kv > 0 ? v : kbase;
   const void* qbase = pr.total_q > 0 ? q : kbase;

@@ -52,6 +52,16 @@ __device__ __forceinline__ WinKeyUnit key_unit(const BwdParams& p, const ItemMet
   return win_key_unit(kt, m.Lq, meta_win(m), p.win.window, p.group);
 }
 __device__ __forceinline__ int count_of(const WinKeyUnit& u) { return u.r1 - u.r0; }
+// A tile of keys or values: d / 64 boxes of 128 rows, at d = 64 two (`half`: one) of 64 (win_key_box).
+template <int D>
+__device__ __forceinline__ void load_keys(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int col, int y, bool half) {
+  if (D == 128) {
+    load_tile<D>(dst, m, bar, col, y);
+  } else {
+    tma_load_2d(dst, m, bar, col, y);
+    if (!half) tma_load_2d(dst + kWinKeys * 128, m, bar, col, y + kWinKeys);
+  }
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdParams p) {
@@ -133,9 +143,11 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
           const TileMap mv = win_tile_map(maps, kMapV, wi.b, sink ? 0 : kt, kBN, skip);
           if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
-          mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
-          load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
-          load_tile<D>(sV, mv.map, &kv_full, wi.h * D, mv.y);
+          const bool half = sink && p.sink_rows <= kWinKeys;  // at d = 64, one box of the two
+          mbar_arrive_expect_tx(&kv_full, D == 128 ? sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes
+                                                   : half ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
+          load_keys<D>(sK, mk.map, &kv_full, wi.h * D, mk.y, half);
+          load_keys<D>(sV, mv.map, &kv_full, wi.h * D, mv.y, half);
           ++item_n;
           // the key tile of this CTA's next item into L2 meanwhile (at d = 128, long-tailed batch:
           // 342 -> 334 us)
@@ -143,8 +155,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
             const ItemMeta* wn = meta_peek_next(meta, item_k);
             if (wn && wn->u0 * kBN < wn->Lk) {
               acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
-              win_prefetch_tile<D / 64>(p.maps, kMapK, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
-              win_prefetch_tile<D / 64>(p.maps, kMapV, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapK, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapV, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
             }
           }
         }
@@ -643,8 +655,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
           const int skip = meta_win(*wnp).skip;
           acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
           for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
-            win_prefetch_tile<D / 64>(p.maps, kMapV, wnp->b, t, wnp->h / p.group * D, skip);
-            win_prefetch_tile<D / 64>(p.maps, kMapK, wnp->b, t, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapV, wnp->b, t, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapK, wnp->b, t, wnp->h / p.group * D, skip);
           }
         }
         for (int jt = 0; jt < nkv && ok; ++jt) {
@@ -1027,10 +1039,10 @@ cudaError_t launch_win_dkdv(const Problem& pr, void* ws, const WsLayout& L, void
 }
 
 cudaError_t launch_win_dq(const Problem& pr, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
+  if (pr.d == 64) return launch_win_dq64(pr, ws, L, dq, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
-  return pr.d == 128 ? launch_dkdv_k(win_dq_kernel<128>, BwdCfg<128>::kSmemDq, num_sms, bp, stream)
-                     : launch_dkdv_k(win_dq_kernel<64>, BwdCfg<64>::kSmemDq, num_sms, bp, stream);
+  return launch_dkdv_k(win_dq_kernel<128>, BwdCfg<128>::kSmemDq, num_sms, bp, stream);
 }
 
 cudaError_t launch_win_join(const Problem& pr, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
