@@ -465,7 +465,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_DQ, s);
-    JFA_CHECK_LAUNCH(launch_win_dq(pr, workspace, L, dq, nsm, s), "dQ launch");
+    JFA_CHECK_LAUNCH(launch_win_dq(pr, maps, workspace, L, dq, nsm, s), "dQ launch");
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_JOIN, s);

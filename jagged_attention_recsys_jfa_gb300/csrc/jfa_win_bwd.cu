@@ -1038,8 +1038,8 @@ cudaError_t launch_win_dkdv(const Problem& pr, void* ws, const WsLayout& L, void
                      : launch_dkdv_k(win_dkdv_kernel<64>, BwdCfg<64>::kSmemDkdv, num_sms, bp, stream);
 }
 
-cudaError_t launch_win_dq(const Problem& pr, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
-  if (pr.d == 64) return launch_win_dq64(pr, ws, L, dq, num_sms, stream);
+cudaError_t launch_win_dq(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
+  if (pr.d == 64) return launch_win_dq64(pr, maps, ws, L, dq, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
   return launch_dkdv_k(win_dq_kernel<128>, BwdCfg<128>::kSmemDq, num_sms, bp, stream);

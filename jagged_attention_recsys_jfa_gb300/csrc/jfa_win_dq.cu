@@ -24,6 +24,7 @@ struct WinDqParams {
   int B, H, group;
   float scale, scale_log2;
   WindowSpec win;
+  bool whole;  // the tensors' own maps serve whole tiles (row numbers fit 31 bits)
   const CUtensorMap *maps, *smaps;
   int sink_box;
   const WorkItem* items;
@@ -46,7 +47,10 @@ constexpr uint32_t kColDq = 0, kColBuf = kD;
 static_assert(kColBuf + 3 * kWinKeys <= kWinTmemCols, "TMEM columns");
 static_assert(2 * (kDqSmemBytes + 2048) <= 233472, "two CTAs per SM");
 
-__global__ void __launch_bounds__(kWinThreads, 2) win_dq64_kernel(const __grid_constant__ WinDqParams p) {
+__global__ void __launch_bounds__(kWinThreads, 2)
+    win_dq64_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap do_map,
+                    const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                    const __grid_constant__ WinDqParams p) {
   constexpr int R = kStages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -107,6 +111,12 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_dq64_kernel(const __grid_c
       Ring<R> kr, vr;
       uint32_t n = 0;  // tiles loaded into each ring
       bool ok = true;
+      if (p.whole) {
+        tmap_prefetch(&k_map);
+        tmap_prefetch(&v_map);
+      }
+      const CUtensorMap* const whole_k = p.whole ? &k_map : nullptr;
+      const CUtensorMap* const whole_v = p.whole ? &v_map : nullptr;
       for (uint32_t k = 0; ok; ++k) {
         if (!tile_wait(tiles, k, abort_flag)) { ok = false; break; }
         const WinTile& w = tiles.e[k % kMetaSlots];
@@ -115,8 +125,9 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_dq64_kernel(const __grid_c
         auto fill = [&](int slot, int j, Ring<R>& r, uint64_t* full, uint64_t* empty, uint8_t* smem_tiles) {
           const bool sink = j < w.nz;
           const TileMap m = sink ? win_tile_map(p.smaps, slot, w.b, j, kWinKeys, 0)
-                                 : win_tile_map(p.maps, slot, w.b, w.a + j - w.nz, kWinKeys, w.skip);
-          tmap_acquire(m.map);
+                                 : win_tile_map(slot == kMapK ? whole_k : whole_v, p.maps, slot, w.b, w.ko,
+                                                w.a + j - w.nz, w.Lk, kWinKeys, w.skip);
+          if (sink || m.tail) tmap_acquire(m.map);
           if (!mbar_wait(&empty[r.e], r.ph ^ 1, abort_flag, kWaitTimeoutNs)) return false;
           mbar_arrive_expect_tx(&full[r.e], uint32_t(sink ? p.sink_box : kWinKeys) * kD * 2);
           tma_load_2d(smem_tiles + r.e * kKeyBytes, m.map, &full[r.e], col, m.y);
@@ -203,12 +214,24 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_dq64_kernel(const __grid_c
       // the last products of the previous tile have read the buffers
       if (!warp_wait(&q_empty, (n_q & 1) ^ 1, abort_flag)) { ok = false; break; }
       if (lane == 0) {
-        const TileMap mq = win_tile_map(p.maps, kMapQ, w.b, w.t, kBM, 0), md = win_tile_map(p.maps, kMapDO, w.b, w.t, kBM, 0);
-        tmap_acquire(mq.map);
-        tmap_acquire(md.map);
+        const TileMap mq = win_tile_map(p.whole ? &q_map : nullptr, p.maps, kMapQ, w.b, w.qo, w.t, w.Lq, kBM, 0);
+        const TileMap md = win_tile_map(p.whole ? &do_map : nullptr, p.maps, kMapDO, w.b, w.qo, w.t, w.Lq, kBM, 0);
+        if (mq.tail) {
+          tmap_acquire(mq.map);
+          tmap_acquire(md.map);
+        }
         mbar_arrive_expect_tx(&q_full, 2 * kQBytes);
         tma_load_2d(sQ, mq.map, &q_full, w.h * kD, mq.y);
         tma_load_2d(sDO, md.map, &q_full, w.h * kD, md.y);
+        // pull the CTA's next query tile into L2 meanwhile, if the scheduler has it already
+        const uint32_t kn = k + 1;
+        if (p.whole && mbar_test_wait(&tiles.full[kn % kMetaSlots], (kn / kMetaSlots) & 1)) {
+          const WinTile& x = tiles.e[kn % kMetaSlots];
+          if (x.b >= 0 && x.rows == kBM) {
+            tma_prefetch_2d(&q_map, x.h * kD, int(x.qo) + x.t * kBM);
+            tma_prefetch_2d(&do_map, x.h * kD, int(x.qo) + x.t * kBM);
+          }
+        }
       }
       tile_release_warp(tiles, k);
       ++n_q;
@@ -397,7 +420,8 @@ __global__ void __launch_bounds__(kWinThreads, 2) win_dq64_kernel(const __grid_c
 
 }  // namespace
 
-cudaError_t launch_win_dq64(const Problem& pr, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
+cudaError_t launch_win_dq64(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq,
+                            int num_sms, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   WsHeader* hdr = reinterpret_cast<WsHeader*>(w);
   WinDqParams p;
@@ -410,6 +434,7 @@ cudaError_t launch_win_dq64(const Problem& pr, void* ws, const WsLayout& L, void
   p.scale = pr.scale;
   p.scale_log2 = pr.scale * kLog2e;
   p.win = pr.win;
+  p.whole = pr.total_q < (int64_t(1) << 31) && pr.total_kv < (int64_t(1) << 31);
   p.maps = reinterpret_cast<const CUtensorMap*>(w + L.maps);
   p.smaps = reinterpret_cast<const CUtensorMap*>(w + L.smaps);
   p.sink_box = win_sink_box(pr.win.sinks);
@@ -426,7 +451,8 @@ cudaError_t launch_win_dq64(const Problem& pr, void* ws, const WsLayout& L, void
   p.trace = pr.trace[JFA_KERNEL_BWD_DQ];
   const cudaError_t e = cudaFuncSetAttribute(win_dq64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmemBytes);
   if (e != cudaSuccess) return e;
-  return launch_pdl(win_dq64_kernel, dim3(kWinCtasPerSm * num_sms), dim3(kWinThreads), kDqSmemBytes, stream, p);
+  return launch_pdl(win_dq64_kernel, dim3(kWinCtasPerSm * num_sms), dim3(kWinThreads), kDqSmemBytes, stream, maps.tmpl[kMapQ],
+                    maps.tmpl[kMapDO], maps.tmpl[kMapK], maps.tmpl[kMapV], p);
 }
 
 }  // namespace jfa
