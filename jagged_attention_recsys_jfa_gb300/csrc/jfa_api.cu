@@ -461,7 +461,7 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_DKDV, s);
-    JFA_CHECK_LAUNCH(launch_win_dkdv(pr, workspace, L, dk, dv, nsm, s), "dK/dV launch");
+    JFA_CHECK_LAUNCH(launch_win_dkdv(pr, maps, workspace, L, dk, dv, nsm, s), "dK/dV launch");
   }
   {
     KernelTimer t(JFA_KERNEL_BWD_DQ, s);

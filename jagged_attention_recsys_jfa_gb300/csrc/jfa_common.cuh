@@ -361,7 +361,8 @@ __host__ __device__ inline bool win_sees_sinks(int t, int Lq, const WinSeq& s) {
 // tiles; the ones behind are chunks of the sinks' pairs.
 struct WinKeyUnit {
   int first, n, r0, r1;
-  int chunk;  // -1: a key tile
+  int chunk;   // -1: a key tile
+  int lo, hi;  // queries outside [lo, hi] see none of its keys
 };
 __host__ __device__ inline int win_sink_chunks(int Lq, const WinSeq& s, int group) {
   if (s.ns <= 0 || Lq <= 0) return 0;
@@ -370,11 +371,12 @@ __host__ __device__ inline int win_sink_chunks(int Lq, const WinSeq& s, int grou
   return (group * (nq - i_min / kBM) + kSinkChunk - 1) / kSinkChunk;
 }
 __host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq& s, int W, int group) {
-  WinKeyUnit u = {0, 1, 0, 0, -1};
+  WinKeyUnit u = {0, 1, 0, 0, -1, 0, Lq - 1};
   const int nk = (s.Lk + kBN - 1) / kBN, nq = (Lq + kBM - 1) / kBM;
   if (kt >= nk) {
     u.chunk = kt - nk;
     const int i_min = Lq - s.org - s.Lk > 0 ? Lq - s.org - s.Lk : 0;
+    u.lo = i_min;
     u.first = i_min / kBM;
     u.n = nq - u.first;
     u.r0 = u.chunk * kSinkChunk;
@@ -387,6 +389,8 @@ __host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq&
   const int lo = j0 - diag > 0 ? j0 - diag : 0;
   const int hi = j1 - diag > Lq - W ? Lq - 1 : j1 - diag + W - 1;  // min(Lq - 1, j1 - diag + W - 1)
   if (hi < lo) return u;
+  u.lo = lo;
+  u.hi = hi;
   u.first = lo / kBM;
   u.n = hi / kBM - u.first + 1;
   u.r1 = group * u.n;

@@ -93,12 +93,14 @@ cudaError_t launch_win_plan(const Problem& p, const WinPlanMaps& maps, void* ws,
                             int num_sms, cudaStream_t stream);
 cudaError_t launch_win_forward(const Problem& p, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse,
                                int num_sms, cudaStream_t stream);
-cudaError_t launch_win_dkdv(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+cudaError_t launch_win_dkdv(const Problem& p, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
                             cudaStream_t stream);
 cudaError_t launch_win_dq(const Problem& p, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms,
                           cudaStream_t stream);
 cudaError_t launch_win_dq64(const Problem& p, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq,
                             int num_sms, cudaStream_t stream);
+cudaError_t launch_win_dkdv64(const Problem& p, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dk, void* dv,
+                              int num_sms, cudaStream_t stream);
 // The sinks' dK and dV from their partial sums, and zeros for keys that no query sees.
 cudaError_t launch_win_join(const Problem& p, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
                             cudaStream_t stream);

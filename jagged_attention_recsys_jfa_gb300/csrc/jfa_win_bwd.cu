@@ -1029,13 +1029,13 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 
 }  // namespace
 
-cudaError_t launch_win_dkdv(const Problem& pr, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
+cudaError_t launch_win_dkdv(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
                             cudaStream_t stream) {
+  if (pr.d == 64) return launch_win_dkdv64(pr, maps, ws, L, dk, dv, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDkdv);
   bp.g0 = static_cast<__nv_bfloat16*>(dk);
   bp.g1 = static_cast<__nv_bfloat16*>(dv);
-  return pr.d == 128 ? launch_dkdv_k(win_dkdv_kernel<128>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream)
-                     : launch_dkdv_k(win_dkdv_kernel<64>, BwdCfg<64>::kSmemDkdv, num_sms, bp, stream);
+  return launch_dkdv_k(win_dkdv_kernel<128>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream);
 }
 
 cudaError_t launch_win_dq(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
