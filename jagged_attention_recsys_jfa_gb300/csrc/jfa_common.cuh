@@ -204,7 +204,7 @@ __host__ __device__ inline int win_sink_box(int sinks) {
   return sink_rows(sinks) < kWinKeys ? sink_rows(sinks) : kWinKeys;
 }
 // Rows of the boxes that load keys and values: the dQ pass at d = 64 takes steps of kWinKeys as the
-// forward does (the dK/dV pass then loads a tile as two boxes).
+// forward does (the dK/dV pass there loads a tile as two boxes).
 __host__ __device__ inline int win_key_box(int d, bool backward) { return backward && d == 128 ? kBN : kWinKeys; }
 // Query tiles of one chunk of the sinks' gradient.  Every query tile of a sequence sees its
 // sinks, so their dK / dV are summed chunk by chunk in fp32 partials, which join_kernel adds up
@@ -446,16 +446,16 @@ __device__ __forceinline__ TileMap win_tile_map(const CUtensorMap* whole, const 
   m.tail = true;  // not acquired yet
   return m;
 }
-// Pull a tile of 128 rows (boxes of 64 columns from column col0, and of 128 / kRowBoxes rows) into L2
-// ahead of its load; one with empty rows in front is left to its load.
-template <int kBoxes, int kRowBoxes = 1>
+// Pull a tile of 128 rows (boxes of 64 columns from column col0) into L2 ahead of its load; one with
+// empty rows in front is left to its load.
+template <int kBoxes>
 __device__ __forceinline__ void win_prefetch_tile(const CUtensorMap* maps, int slot, int b, int t, int col0, int skip) {
   const TileMap m = win_tile_map(maps, slot, b, t, kBN, skip);
   if (m.y < 0) return;
 #pragma unroll
-  for (int c = 0; c < kBoxes * kRowBoxes; ++c)
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m.map),
-                 "r"(col0 + c / kRowBoxes * 64), "r"(m.y + c % kRowBoxes * (kBN / kRowBoxes))
+  for (int c = 0; c < kBoxes; ++c)
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(m.map), "r"(col0 + c * 64),
+                 "r"(m.y)
                  : "memory");
 }
 #endif

@@ -1,5 +1,6 @@
-// What the windowed kernels with two CTAs per SM share (jfa_win.cu: forward, jfa_win_dq.cu: dQ at
-// d = 64): the query tiles that a CTA's scheduler hands to its warps, and their waits.
+// What the windowed kernels with two CTAs per SM share (jfa_win.cu: forward; jfa_win_dq.cu and
+// jfa_win_dkdv.cu: the backward passes at d = 64): the query tiles that a CTA's scheduler hands to
+// its warps, and their waits.
 #pragma once
 #include <cuda_bf16.h>
 

@@ -1,6 +1,7 @@
 // Windowed jagged attention backward for sm_103a: the gradients of the windowed call (jfa_win.cu,
 // include/jfa.h) in the split scheme of the plain call's (jfa_bwd.cu), whose formulas, warp roles,
-// memory plan and pipelines the two passes here share:
+// memory plan and pipelines the two passes here share (d = 128; the passes for d = 64, with the same
+// items, are kernels of two CTAs per SM: jfa_win_dkdv.cu, jfa_win_dq.cu):
 //
 //   dK/dV pass   one item per (sequence, key/value head, key tile of the window part), summed over
 //                the query tiles that its keys' windows reach, of every query head of the group;
@@ -15,8 +16,8 @@
 // the window's branches in the code it shared).  Of the 773 the dK/dV pass is 298, dQ 235, forward
 // 154, preprocess 50, join 10; the floor of the step's products is 190.
 // P and dS are rounded to bf16 as operands (2^-9 relative a term); sums are fp32.
-// Bound by the tensor pipe with its operands and results in TMEM at d = 128, by the steps'
-// hand-offs at d = 64; an item's few steps leave both partly idle between items.
+// Bound by the tensor pipe with its operands and results in TMEM (4150 cycles per 128 x 128 pair of
+// the dK/dV pass, as in the plain call).
 #include <cuda_bf16.h>
 
 #include "jfa_bwd.cuh"
@@ -52,19 +53,8 @@ __device__ __forceinline__ WinKeyUnit key_unit(const BwdParams& p, const ItemMet
   return win_key_unit(kt, m.Lq, meta_win(m), p.win.window, p.group);
 }
 __device__ __forceinline__ int count_of(const WinKeyUnit& u) { return u.r1 - u.r0; }
-// A tile of keys or values: d / 64 boxes of 128 rows, at d = 64 two (`half`: one) of 64 (win_key_box).
-template <int D>
-__device__ __forceinline__ void load_keys(uint8_t* dst, const CUtensorMap* m, uint64_t* bar, int col, int y, bool half) {
-  if (D == 128) {
-    load_tile<D>(dst, m, bar, col, y);
-  } else {
-    tma_load_2d(dst, m, bar, col, y);
-    if (!half) tma_load_2d(dst + kWinKeys * 128, m, bar, col, y + kWinKeys);
-  }
-}
-
-template <int D>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdParams p) {
+  constexpr int D = 128;
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDkdv;
   extern __shared__ uint8_t smem_raw[];
@@ -143,11 +133,9 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
           const TileMap mv = win_tile_map(maps, kMapV, wi.b, sink ? 0 : kt, kBN, skip);
           if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
-          const bool half = sink && p.sink_rows <= kWinKeys;  // at d = 64, one box of the two
-          mbar_arrive_expect_tx(&kv_full, D == 128 ? sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes
-                                                   : half ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
-          load_keys<D>(sK, mk.map, &kv_full, wi.h * D, mk.y, half);
-          load_keys<D>(sV, mv.map, &kv_full, wi.h * D, mv.y, half);
+          mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
+          load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
+          load_tile<D>(sV, mv.map, &kv_full, wi.h * D, mv.y);
           ++item_n;
           // the key tile of this CTA's next item into L2 meanwhile (at d = 128, long-tailed batch:
           // 342 -> 334 us)
@@ -155,8 +143,8 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
             const ItemMeta* wn = meta_peek_next(meta, item_k);
             if (wn && wn->u0 * kBN < wn->Lk) {
               acquire_seq_maps(p.maps, wn->b, kMapK, kMapV, acq_b, true);
-              win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapK, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
-              win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapV, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64>(p.maps, kMapK, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
+              win_prefetch_tile<D / 64>(p.maps, kMapV, wn->b, wn->u0, wn->h * D, meta_win(*wn).skip);
             }
           }
         }
@@ -364,29 +352,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceCompute0 + w, tn, 20);
         const int i0 = qt * kBM + 64 * w;  // local query index of column 0 of this half
-        if (D == 64) {
-          // the warp's 32 keys against these 64 queries: none sees any -> nothing to compute (d = 64:
-          // 130 -> 127 us on the ragged step; at d = 128 the products set the pace, 334 -> 338 us)
-          const int j0 = j - lane, w_hi = sink ? Lq : j0 + 31 - diag + p.win.window - 1;  // last query that may see one
-          if (i0 + 63 < j0 - diag || i0 > w_hi || i0 >= Lq ||
-              quarter * 32 >= (sink ? meta_win(it).ns : Lk - kt * kBN)) {
-            uint32_t z[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) z[c] = 0u;
-            tmem_st32(tPT, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&p_full);
-            if (!mbar_wait(&dpt_full, tile_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-            ++tile_n;
-            tc_fence_after();
-            tmem_st32(tDST, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&ds_full);
-            continue;
-          }
-        }
         float x[64];
         ld_cols64(tS, x);
         {
@@ -519,8 +484,8 @@ __device__ __forceinline__ QueryUnit query_unit(const BwdParams& p, const ItemMe
   return u;
 }
 
-template <int D>
 __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams p) {
+  constexpr int D = 128;
   using C = BwdCfg<D>;
   constexpr int R = C::kRingDq;
   extern __shared__ uint8_t smem_raw[];
@@ -529,7 +494,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
   uint8_t* sDO = smem + C::kTileBytes;
   uint8_t* sRing = smem + 2 * C::kTileBytes;
 
-  __shared__ uint64_t qdo_full, qdo_empty, qt_full, s_full, s_free, acc_full, acc_empty, mma_done;
+  __shared__ uint64_t qdo_full, qdo_empty, s_full, s_free, acc_full, acc_empty, mma_done;
   // dp_full / ds_full of global tile g live at index g & 1: dP(g+1) is issued before dQ(g)
   // waits for dS(g), so one warpgroup may finish tile g+1 while the other still works on
   // tile g (never further: S(g+2) waits for both warpgroups' s_free(g+1)); separate
@@ -544,8 +509,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
   if (threadIdx.x == 0) {
     abort_sh = 0;
     mbar_init(&qdo_full, 1);
-    mbar_init(&qdo_empty, C::kDqQTmem ? 256 : 1);  // both compute warpgroups, else the last dP MMA
-    mbar_init(&qt_full, 256);
+    mbar_init(&qdo_empty, 1);
     mbar_init(&s_full, 1);
     mbar_init(&s_free, 256);
     mbar_init(&dp_full[0], 1);
@@ -649,14 +613,14 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
        for (int qt = wi.u0; qt < wi.u1 && ok; ++qt) {
         const QueryUnit qu = query_unit(p, wi, qt);
         const int nkv = qu.nkv;
-        if (const ItemMeta* wnp = D == 128 ? meta_peek_next(meta, item_k) : nullptr) {
+        if (const ItemMeta* wnp = meta_peek_next(meta, item_k)) {
           // the first key tiles of this CTA's next item into L2 meanwhile
           const QueryUnit nu = query_unit(p, *wnp, wnp->u0);
           const int skip = meta_win(*wnp).skip;
           acquire_seq_maps(p.maps, wnp->b, kMapK, kMapV, acq_b, true);
           for (int t = nu.a; t < nu.a + 2 && t * kBN < wnp->Lk; ++t) {
-            win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapV, wnp->b, t, wnp->h / p.group * D, skip);
-            win_prefetch_tile<D / 64, 128 / D>(p.maps, kMapK, wnp->b, t, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64>(p.maps, kMapV, wnp->b, t, wnp->h / p.group * D, skip);
+            win_prefetch_tile<D / 64>(p.maps, kMapK, wnp->b, t, wnp->h / p.group * D, skip);
           }
         }
         for (int jt = 0; jt < nkv && ok; ++jt) {
@@ -696,10 +660,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t o = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          if (C::kDqQTmem)
-            umma_ts(tmem + dcol, tmem + (dp ? C::kColDqDO : C::kColDqQ) + kk * 8, bd + o, id, kk > 0);
-          else
-            umma_ss(tmem + dcol, ad + o, bd + o, id, kk > 0);
+          umma_ss(tmem + dcol, ad + o, bd + o, id, kk > 0);
         }
       };
       uint32_t item_k = 0;
@@ -712,7 +673,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
         const int nkv = qu.nkv;
         if (nkv == 0) continue;
         const uint32_t id0 = qu.nz ? idesc_bf16_f32(128, p.sink_rows, false, false) : kIdS;  // the first step's
-        if (!wait(C::kDqQTmem ? &qt_full : &qdo_full, item_n & 1)) { ok = false; break; }
+        if (!wait(&qdo_full, item_n & 1)) { ok = false; break; }
         ++item_n;
         trace_event(p.trace, kTraceMma, tn, 10);
         const uint32_t n0 = ring_n;  // V_j at n0 + 2j, K_j at n0 + 2j + 1
@@ -726,7 +687,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
         // Q and dO are read only by S and dP: once the last dP is issued the loader may
         // bring in the next query tile while dQ of this one still runs (at d = 64 the compute
         // warpgroups free them after copying them into TMEM)
-        if (nkv == 1 && !C::kDqQTmem) umma_commit(&qdo_empty);
+        if (nkv == 1) umma_commit(&qdo_empty);
         for (int jt = 0; jt < nkv && ok; ++jt) {
           const uint32_t g = tile_n;  // global tile index
           const uint32_t nv = n0 + 2 * jt, nk = nv + 1;
@@ -743,7 +704,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
             mma_nt(colP(g + 1), true, ra(nv + 2), kIdS);
             umma_commit(&dp_full[(g + 1) & 1]);
             umma_commit(&ring_empty[(nv + 2) % R]);
-            if (jt + 2 == nkv && !C::kDqQTmem) umma_commit(&qdo_empty);
+            if (jt + 2 == nkv) umma_commit(&qdo_empty);
             trace_event(p.trace, kTraceMma, tn, 13);
           }
           if (!wait(&ds_full[g & 1], (g >> 1) & 1)) { ok = false; break; }
@@ -792,7 +753,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
     const uint32_t lane_addr = uint32_t(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_addr + C::kColS + 64 * w;
     const float sl2 = p.scale_log2;
-    uint32_t tile_n = 0, q_n = 0, tn = 0;
+    uint32_t tile_n = 0, tn = 0;
     const bool leader = (warp & 3) == 0 && lane == 0;
     bool ok = true;
     uint32_t item_k = 0;
@@ -807,27 +768,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
       const int nkv = qu.nkv;
       const int i = qt * kBM + row;
       if (nkv == 0) continue;  // rows of zeros: written by the epilogue warpgroup
-      if (C::kDqQTmem) {
-        // this query tile's rows into TMEM: warpgroup 0 copies Q, warpgroup 1 dO (row `row`
-        // of a 128-byte-swizzled tile: 16-byte chunk c at chunk position c ^ (row & 7))
-        if (!mbar_wait(&qdo_full, q_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-        ++q_n;
-        const uint4* src = reinterpret_cast<const uint4*>((w ? sDO : sQ) + row * 128);
-        uint32_t cw[32];
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const uint4 v = src[c ^ (row & 7)];
-          cw[4 * c] = v.x;
-          cw[4 * c + 1] = v.y;
-          cw[4 * c + 2] = v.z;
-          cw[4 * c + 3] = v.w;
-        }
-        tmem_st32(tmem + lane_addr + (w ? C::kColDqDO : C::kColDqQ), cw);
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(&qt_full);
-        mbar_arrive(&qdo_empty);
-      }
       // padded per-query vectors (stored negated): 0 past the sequence end, -inf for rows
       // that see no key
       const float nl2 = __ldg(p.lse2 + vec0 + i);
@@ -843,26 +783,6 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
         // local key index of column 0 of this half (sinks: behind org)
         const int j0 = (sink ? -meta_win(it).org : (qu.a + jt - qu.nz) * kBN) + 64 * w;
         const int n_real = sink ? meta_win(it).ns - 64 * w : Lk - j0;  // columns >= n_real hold no key
-        if (D == 64) {
-          // the warp's 32 queries against these 64 keys: none is seen -> nothing to compute (d = 64:
-          // 106 -> 101 us on the ragged step; no gain at d = 128)
-          const int r0 = i - lane;
-          if (r0 >= Lq || n_real <= 0 || r0 + 31 + diag < j0 || (!sink && r0 + diag - p.win.window + 1 > j0 + 63)) {
-            mbar_arrive(&s_free);
-            const uint32_t g = tile_n;
-            if (!mbar_wait(&dp_full[g & 1], (g >> 1) & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
-            ++tile_n;
-            tc_fence_after();
-            uint32_t z[32];
-#pragma unroll
-            for (int c = 0; c < 32; ++c) z[c] = 0u;
-            tmem_st32(tmem + lane_addr + colP(g) + 64 * w, z);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(&ds_full[g & 1]);
-            continue;
-          }
-        }
         float x[64];
         ld_cols64(tS, x);
         tc_fence_before();
@@ -1035,14 +955,14 @@ cudaError_t launch_win_dkdv(const Problem& pr, const WinPlanMaps& maps, void* ws
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDkdv);
   bp.g0 = static_cast<__nv_bfloat16*>(dk);
   bp.g1 = static_cast<__nv_bfloat16*>(dv);
-  return launch_dkdv_k(win_dkdv_kernel<128>, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream);
+  return launch_dkdv_k(win_dkdv_kernel, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream);
 }
 
 cudaError_t launch_win_dq(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
   if (pr.d == 64) return launch_win_dq64(pr, maps, ws, L, dq, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
-  return launch_dkdv_k(win_dq_kernel<128>, BwdCfg<128>::kSmemDq, num_sms, bp, stream);
+  return launch_dkdv_k(win_dq_kernel, BwdCfg<128>::kSmemDq, num_sms, bp, stream);
 }
 
 cudaError_t launch_win_join(const Problem& pr, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
