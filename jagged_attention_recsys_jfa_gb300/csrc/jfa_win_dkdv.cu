@@ -54,22 +54,27 @@ static_assert(kColP + 64 <= kWinTmemCols, "TMEM columns");
 static_assert(2 * (kDkdvSmemBytes + 2048) <= 233472, "two CTAs per SM");
 
 // A unit's steps: its pairs of query head and query tile in order, and of each tile the halves that
-// see any of its keys.
+// see any of its keys.  (Counted on, not divided out of the pair's number, which costs every warp
+// some hundred instructions a step.)
 struct StepWalk {
-  WinKeyUnit u;
-  int r;     // pair
-  int half;  // of its tile
-  __device__ __forceinline__ StepWalk(const WinKeyUnit& unit) : u(unit), r(unit.r0), half(0) { half = first_half(); }
-  __device__ __forceinline__ bool live() const { return r < u.r1; }
-  __device__ __forceinline__ int tile() const { return u.first + r % u.n; }
-  __device__ __forceinline__ int first_half() const { return tile() * kBM + 63 >= u.lo ? 0 : 1; }
-  __device__ __forceinline__ bool last_half() const { return half == 1 || tile() * kBM + 64 > u.hi; }
+  int left;         // pairs not done yet
+  int t, half;      // query tile, its half
+  int first, end;   // tiles of one head
+  int lo, hi;       // queries outside [lo, hi] see no key
+  __device__ __forceinline__ StepWalk(const WinKeyUnit& u)
+      : left(u.r1 - u.r0), t(u.first + u.r0 % u.n), first(u.first), end(u.first + u.n), lo(u.lo), hi(u.hi) {
+    half = first_half();
+  }
+  __device__ __forceinline__ bool live() const { return left > 0; }
+  __device__ __forceinline__ int first_half() const { return t * kBM + 63 >= lo ? 0 : 1; }
+  __device__ __forceinline__ bool last_half() const { return half == 1 || t * kBM + 64 > hi; }
   __device__ __forceinline__ void next() {
     if (!last_half()) {
       half = 1;
     } else {
-      ++r;
-      half = live() ? first_half() : 0;
+      --left;
+      t = t + 1 == end ? first : t + 1;
+      half = first_half();
     }
   }
 };
@@ -149,8 +154,8 @@ __global__ void __launch_bounds__(kWinThreads, 2)
         const ItemMeta& wi = meta.e[k % kMetaSlots];  // read in place, freed after the item
         if (wi.b < 0) break;  // end of this CTA's items
         const WinKeyUnit u = unit_of(wi);
+        int t = u.first + u.r0 % u.n, h = wi.h * p.group + u.r0 / u.n;
         for (int i = u.r0; i < u.r1; ++i) {
-          const int t = u.first + i % u.n, h = wi.h * p.group + i / u.n;
           const TileMap mq = win_tile_map(p.whole ? &q_map : nullptr, p.maps, kMapQ, wi.b, wi.qo, t, wi.Lq, kBM, 0);
           const TileMap md = win_tile_map(p.whole ? &do_map : nullptr, p.maps, kMapDO, wi.b, wi.qo, t, wi.Lq, kBM, 0);
           if (mq.tail) {
@@ -167,6 +172,10 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           bulk_load(v + kBM, p.delta + vec, kBM * 4, &ring_full[r.e]);
           r.next();
           ++n;
+          if (++t == u.first + u.n) {  // the group's next query head
+            t = u.first;
+            ++h;
+          }
         }
         if (ok) meta_release(meta, k);
       }
@@ -348,7 +357,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       }
       const bool no_key = quarter * 32 >= (sink ? ws.ns : Lk - kt * kBN);  // of the warp's
       for (StepWalk w(u); w.live(); w.next(), ++g) {
-        const int i0 = w.tile() * kBM + 64 * w.half;  // local query index of column 0
+        const int i0 = w.t * kBM + 64 * w.half;  // local query index of column 0
         const bool pair_done = w.last_half();
         // the stage's vectors
         if (!warp_wait(&ring_full[cur.e], cur.ph, abort_flag)) { ok = false; break; }
