@@ -66,6 +66,7 @@ struct StepWalk {
     half = first_half();
   }
   __device__ __forceinline__ bool live() const { return left > 0; }
+  __device__ __forceinline__ bool final() const { return left == 1 && last_half(); }
   __device__ __forceinline__ int first_half() const { return t * kBM + 63 >= lo ? 0 : 1; }
   __device__ __forceinline__ bool last_half() const { return half == 1 || t * kBM + 64 > hi; }
   __device__ __forceinline__ void next() {
@@ -220,14 +221,12 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       tc_fence_after();
       {
         const uint32_t at = cur.e * kTileBytes + w.half * kHalfBytes;
-        StepWalk after = w;
-        after.next();
         if (elect_one()) {
           mma_nt(kColS, kd, aQ + at);
           umma_commit(&s_full);
           mma_nt(kColP, vd, aDO + at);
           umma_commit(&dp_full);
-          if (!after.live()) umma_commit(&kv_empty);
+          if (w.final()) umma_commit(&kv_empty);
         }
       }
       bool first = true;
@@ -239,8 +238,6 @@ __global__ void __launch_bounds__(kWinThreads, 2)
         const bool more = nx.live();
         if (pair_done) cur.next();
         const uint32_t at_next = cur.e * kTileBytes + nx.half * kHalfBytes;
-        StepWalk after = nx;
-        if (more) after.next();
         if (!warp_wait(&p_full, g & 1, abort_flag)) { ok = false; break; }
         if (more && pair_done && !warp_wait(&ring_full[cur.e], cur.ph, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -259,7 +256,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           if (more) {
             mma_nt(kColP, vd, aDO + at_next);
             umma_commit(&dp_full);
-            if (!after.live()) umma_commit(&kv_empty);  // the last to read K and V
+            if (nx.final()) umma_commit(&kv_empty);  // the last to read K and V
           } else {
             umma_commit(&acc_full);
           }
@@ -334,28 +331,27 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       if (!meta_wait_warp(meta, k, abort_flag)) { ok = false; break; }
       const ItemMeta& it = meta.e[k % kMetaSlots];
       if (it.b < 0) break;
-      const WinSeq ws = meta_win(it);
-      const int Lq = it.Lq, Lk = it.Lk, kt = it.u0, diag = Lk - Lq;
-      const int64_t ko = it.ko, qp = it.qp;
-      const int b = it.b, hk = it.h;
       const WinKeyUnit u = unit_of(it);
-      meta_release_warp(meta, k);  // the rest is in registers
       const bool sink = u.chunk >= 0;
-      const int j = sink ? row - ws.org : kt * kBN + row;  // local key index (sinks: behind org)
-      const bool valid = sink ? row < ws.ns : j < Lk && j >= ws.pad;
-      __nv_bfloat16* dk_row = p.dk + ((ko + j) * p.win.H_kv + hk) * int64_t(kD);
-      __nv_bfloat16* dv_row = p.dv + ((ko + j) * p.win.H_kv + hk) * int64_t(kD);
+      const int chunk = u.chunk;
+      const int j = sink ? row - meta_win(it).org : it.u0 * kBN + row;  // local key index (sinks: behind org)
+      // (the entry is read in place, also at the end: fewer values live through the steps)
+      auto valid = [&] { return sink ? row < meta_win(it).ns : j < it.Lk && j >= meta_win(it).pad; };
+      auto row_of = [&](__nv_bfloat16* base) { return base + ((it.ko + j) * p.win.H_kv + it.h) * int64_t(kD); };
       if (u.r1 <= u.r0) {  // no query sees these keys
-        if (valid) {
+        if (valid()) {
+          __nv_bfloat16 *dk_row = row_of(p.dk), *dv_row = row_of(p.dv);
 #pragma unroll
           for (int c = 0; c < kD / 8; ++c) {
             reinterpret_cast<uint4*>(dk_row)[c] = make_uint4(0, 0, 0, 0);
             reinterpret_cast<uint4*>(dv_row)[c] = make_uint4(0, 0, 0, 0);
           }
         }
+        meta_release_warp(meta, k);
         continue;
       }
-      const bool no_key = quarter * 32 >= (sink ? ws.ns : Lk - kt * kBN);  // of the warp's
+      const bool no_key = quarter * 32 >= (sink ? meta_win(it).ns : it.Lk - it.u0 * kBN);  // of the warp's
+      const int j_diag = j - (it.Lk - it.Lq);  // first query that sees this thread's key
       for (StepWalk w(u); w.live(); w.next(), ++g) {
         const int i0 = w.t * kBM + 64 * w.half;  // local query index of column 0
         const bool pair_done = w.last_half();
@@ -366,9 +362,9 @@ __global__ void __launch_bounds__(kWinThreads, 2)
         if (!warp_wait(&s_full, g & 1, abort_flag)) { ok = false; break; }
         tc_fence_after();
         // columns [clo, chi] see this thread's key; the warp's lanes move both by one each
-        const int clo = j - diag - i0, chi = sink ? 1 << 30 : clo + p.win.window - 1;
+        const int clo = j_diag - i0, chi = sink ? 1 << 30 : clo + p.win.window - 1;
         const int clo0 = clo - lane, chi0 = sink ? 1 << 30 : chi - lane;  // lane 0's
-        const bool hidden = no_key || clo0 > 63 || (!sink && chi0 + 31 < 0) || i0 >= Lq;
+        const bool hidden = no_key || clo0 > 63 || (!sink && chi0 + 31 < 0);
         uint32_t pk[32];
         if (!hidden) {
           float x[64];
@@ -436,10 +432,14 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       if (!warp_wait(&acc_full, acc_n & 1, abort_flag)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
+      const bool stored = valid();
       float* part = nullptr;
       if (sink)
-        part = p.spart + ((sink_slot0(qp / kBM, b, p.group) * p.win.H_kv +
-                           int64_t(hk) * win_sink_chunks(Lq, ws, p.group) + u.chunk) * 2 * p.win.sinks + row) * int64_t(kD);
+        part = p.spart + ((sink_slot0(it.qp / kBM, it.b, p.group) * p.win.H_kv +
+                           int64_t(it.h) * win_sink_chunks(it.Lq, meta_win(it), p.group) + chunk) *
+                              2 * p.win.sinks + row) * int64_t(kD);
+      __nv_bfloat16 *dk_row = row_of(p.dk), *dv_row = row_of(p.dv);
+      meta_release_warp(meta, k);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -447,7 +447,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
           uint32_t r[32];
           tmem_ld32(tmem + lane_addr + (t ? kColDk : kColDv) + c0, r);
           tmem_ld_wait();
-          if (!valid) continue;
+          if (!stored) continue;
           if (sink) {  // fp32 partial sums, dK in front of dV
             uint4* o = reinterpret_cast<uint4*>(part + (t ? 0 : p.win.sinks * kD) + c0);
 #pragma unroll
