@@ -2,10 +2,11 @@
 // jfa_win_bwd.cu).  Two CTAs per SM, each with half of its shared and tensor memory, as in the dQ pass
 // (jfa_win_dq.cu): while one waits for its next key tile, a product or its rows, the other computes.
 //
-// 95 us (64 sequences of up to 2048 tokens, 4 query and 2 key/value heads, window 256, 4 sinks); one
-// CTA per SM with 128-query steps took 108, and 333 instead of 276 on 2048 sequences of up to 96
-// tokens.  The products' 64 columns and the hand-offs set the pace: vectors read 16 bytes at a time
-// and the next key tile pulled into L2 changed nothing.
+// 88 us (64 sequences of up to 2048 tokens, 4 query and 2 key/value heads, window 256, 4 sinks); one
+// CTA per SM with 128-query steps took 108, and 333 instead of 249 on 2048 sequences of up to 96
+// tokens.  The tensor pipe is busy 27% of it, memory 17%: the hand-offs and every warp's own work
+// per step set the pace (eight warps of 32 queries each took 113; vectors read 16 bytes at a time and
+// the next key tile pulled into L2 changed nothing).
 //
 // A step takes 64 queries of one query head against the item's 128 keys; of a query tile's two
 // halves only those are taken that a key's window reaches.
