@@ -254,7 +254,8 @@ int jfa_last_launch_count(void);
 const char* jfa_last_error(void);
 
 /* Kernel kinds for per-kernel timing.  (A windowed call's kernels count as the plain call's of
- * their role; the join and cache kinds record no developer trace.) */
+ * their role; the join and cache kinds, and the windowed backward passes at d = 64, record no
+ * developer trace.) */
 enum { JFA_KERNEL_PLAN = 0, JFA_KERNEL_FORWARD = 1, JFA_KERNEL_BWD_PREPROCESS = 2, JFA_KERNEL_BWD_DKDV = 3,
        JFA_KERNEL_BWD_DQ = 4, JFA_KERNEL_BWD_FUSED = 5, JFA_KERNEL_BWD_NSP = 6, JFA_KERNEL_BWD_JOIN = 7,
        JFA_KERNEL_CACHE_APPEND = 8, JFA_KERNEL_CACHE_ATTENTION = 9, JFA_NUM_KERNEL_KINDS = 10 };

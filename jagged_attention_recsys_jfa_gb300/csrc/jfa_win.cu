@@ -47,8 +47,8 @@ constexpr float kRescaleThreshold = 16.0f;
 struct WinFwdParams {
   const int64_t* q_off;
   const int64_t* kv_off;
-  int B, H, group;  // group: query heads per key/value head
-  int64_t total_q, total_kv;
+  int H, group;  // group: query heads per key/value head
+  int64_t total_q;
   float scale_log2;  // scale * log2(e), > 0
   WindowSpec win;
   bool whole;                // the tensors' own maps serve whole tiles (row numbers fit 31 bits)
@@ -483,11 +483,9 @@ cudaError_t launch_win_forward(const Problem& pr, const PlanMaps& maps, void* ws
   WinFwdParams fp;
   fp.q_off = pr.q_off;
   fp.kv_off = pr.kv_off;
-  fp.B = pr.B;
   fp.H = pr.H;
   fp.group = pr.H / pr.win.H_kv;
   fp.total_q = pr.total_q;
-  fp.total_kv = pr.total_kv;
   fp.scale_log2 = pr.scale * kLog2e;
   fp.win = pr.win;
   fp.whole = pr.total_q < (int64_t(1) << 31) && pr.total_kv < (int64_t(1) << 31);

@@ -26,7 +26,7 @@ namespace {
 
 struct WinDkdvParams {
   const int64_t *q_off, *kv_off, *qpad;
-  int B, H, group;
+  int H, group;
   float scale, scale_log2;
   WindowSpec win;
   bool whole;  // the tensors' own maps serve whole tiles (row numbers fit 31 bits)
@@ -41,7 +41,6 @@ struct WinDkdvParams {
   int64_t qpad_cap;
   __nv_bfloat16 *dk, *dv;
   float* spart;  // partial dK, dV of the sinks: [slot][2][sinks][64]
-  TraceBuf trace;
 };
 
 constexpr int kD = 64;
@@ -479,7 +478,6 @@ cudaError_t launch_win_dkdv64(const Problem& pr, const WinPlanMaps& maps, void* 
   p.q_off = pr.q_off;
   p.kv_off = pr.kv_off;
   p.qpad = reinterpret_cast<const int64_t*>(w + L.qpad);
-  p.B = pr.B;
   p.H = pr.H;
   p.group = pr.H / pr.win.H_kv;
   p.scale = pr.scale;
@@ -500,7 +498,6 @@ cudaError_t launch_win_dkdv64(const Problem& pr, const WinPlanMaps& maps, void* 
   p.dk = static_cast<__nv_bfloat16*>(dk);
   p.dv = static_cast<__nv_bfloat16*>(dv);
   p.spart = reinterpret_cast<float*>(w + L.spart);
-  p.trace = pr.trace[JFA_KERNEL_BWD_DKDV];
   const cudaError_t e = cudaFuncSetAttribute(win_dkdv64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDkdvSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(win_dkdv64_kernel, dim3(kWinCtasPerSm * num_sms), dim3(kWinThreads), kDkdvSmemBytes, stream,

@@ -24,7 +24,7 @@ namespace {
 
 struct WinDqParams {
   const int64_t *q_off, *kv_off, *qpad;
-  int B, H, group;
+  int H, group;
   float scale, scale_log2;
   WindowSpec win;
   bool whole;  // the tensors' own maps serve whole tiles (row numbers fit 31 bits)
@@ -39,7 +39,6 @@ struct WinDqParams {
   int64_t qpad_cap;
   __nv_bfloat16* dq;
   bool wide_out;  // dq is 32-byte aligned
-  TraceBuf trace;
 };
 
 constexpr int kD = 64;
@@ -431,7 +430,6 @@ cudaError_t launch_win_dq64(const Problem& pr, const WinPlanMaps& maps, void* ws
   p.q_off = pr.q_off;
   p.kv_off = pr.kv_off;
   p.qpad = reinterpret_cast<const int64_t*>(w + L.qpad);
-  p.B = pr.B;
   p.H = pr.H;
   p.group = pr.H / pr.win.H_kv;
   p.scale = pr.scale;
@@ -451,7 +449,6 @@ cudaError_t launch_win_dq64(const Problem& pr, const WinPlanMaps& maps, void* ws
   p.qpad_cap = L.qpad_cap;
   p.dq = static_cast<__nv_bfloat16*>(dq);
   p.wide_out = (reinterpret_cast<uintptr_t>(dq) & 31u) == 0;
-  p.trace = pr.trace[JFA_KERNEL_BWD_DQ];
   const cudaError_t e = cudaFuncSetAttribute(win_dq64_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDqSmemBytes);
   if (e != cudaSuccess) return e;
   return launch_pdl(win_dq64_kernel, dim3(kWinCtasPerSm * num_sms), dim3(kWinThreads), kDqSmemBytes, stream, maps.tmpl[kMapQ],

@@ -307,9 +307,10 @@ def test_tensors_that_fill_their_memory(S):
             close(t, ref[name], name)
 
 
-def test_rows_beyond_2_billion_elements():
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_beyond_2_billion_elements(d):
     """A short sequence behind one whose rows fill 2^31 elements: as if it were alone."""
-    H, G, d, W, S = 16, 1, 128, 16, 2
+    H, G, W, S = 16, 1, 16, 2
     lens = [(1 << 31) // (H * d) + 77, 40, 0, 130]
     x, dout = make(lens, lens, H, G, d, 18)
     out, lse, _ = jfa.jfa_window_forward(**x, window=W, sinks=S)
