@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
 //
 // In a CTA a producer warp copies K and V tiles into a ring with TMA (one box per page and
 // 64 columns, 128-byte swizzle); four warps take 16 keys of each tile each, with the running
-// maximum, sum and output rows in registers (P rounded to bf16 as an operand):  S = Q K^T and O += P V on m16n8k16 products
-// whose 16 rows are the query heads (rows past G are zero).
+// maximum, sum and output rows in registers:  S = Q K^T and O += P V on m16n8k16 products whose
+// 16 rows are the query heads (rows past G are zero); P is rounded to bf16 as an operand (at most
+// 2^-8 relative a term).
 constexpr int kTileKeys = 64;
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * (kAttnWarps + 1);

@@ -385,7 +385,8 @@ __host__ __device__ inline WinKeyUnit win_key_unit(int kt, int Lq, const WinSeq&
   }
   if (Lq <= 0) return u;
   // key j' is seen by queries j' - diag .. j' - diag + W - 1
-  const int diag = s.Lk - Lq, j0 = kt * kBN > s.pad ? kt * kBN : s.pad, j1 = kt * kBN + kBN - 1 < s.Lk - 1 ? kt * kBN + kBN - 1 : s.Lk - 1;
+  const int diag = s.Lk - Lq, j0 = kt * kBN > s.pad ? kt * kBN : s.pad;
+  const int j1 = kt * kBN + kBN - 1 < s.Lk - 1 ? kt * kBN + kBN - 1 : s.Lk - 1;
   const int lo = j0 - diag > 0 ? j0 - diag : 0;
   const int hi = j1 - diag > Lq - W ? Lq - 1 : j1 - diag + W - 1;  // min(Lq - 1, j1 - diag + W - 1)
   if (hi < lo) return u;

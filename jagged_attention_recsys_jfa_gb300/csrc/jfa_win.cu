@@ -32,7 +32,7 @@
 // steps' hand-offs.  By timing copies that leave work out, the softmax arithmetic is about 35 us of
 // the first, half of the score products 5.
 //
-// P is rounded to bf16 for its product (2^-9 relative a term); scores, maximum, sum and O are fp32.
+// P is rounded to bf16 for its product (at most 2^-8 relative a term); scores, maximum, sum and O are fp32.
 #include "jfa_win.cuh"
 
 namespace jfa {
@@ -477,8 +477,8 @@ cudaError_t launch_win_fwd_t(const PlanMaps& maps, const WinFwdParams& fp, int g
 
 }  // namespace
 
-cudaError_t launch_win_forward(const Problem& pr, const PlanMaps& maps, void* ws, const WsLayout& L, void* out, float* lse, int num_sms,
-                               cudaStream_t stream) {
+cudaError_t launch_win_forward(const Problem& pr, const PlanMaps& maps, void* ws, const WsLayout& L, void* out,
+                               float* lse, int num_sms, cudaStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   WinFwdParams fp;
   fp.q_off = pr.q_off;

@@ -15,7 +15,7 @@
 // 4 key/value heads, window 512, 16 sinks) and the plain dK/dV pass keeps its 0.699 ms (0.714 with
 // the window's branches in the code it shared).  Of the 773 the dK/dV pass is 298, dQ 235, forward
 // 154, preprocess 50, join 10; the floor of the step's products is 190.
-// P and dS are rounded to bf16 as operands (2^-9 relative a term); sums are fp32.
+// P and dS are rounded to bf16 as operands (at most 2^-8 relative a term); sums are fp32.
 // Bound by the tensor pipe with its operands and results in TMEM (4150 cycles per 128 x 128 pair of
 // the dK/dV pass, as in the plain call).
 #include <cuda_bf16.h>
@@ -949,8 +949,8 @@ __global__ void __launch_bounds__(256) join_kernel(const JoinParams p) {
 
 }  // namespace
 
-cudaError_t launch_win_dkdv(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dk, void* dv, int num_sms,
-                            cudaStream_t stream) {
+cudaError_t launch_win_dkdv(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dk, void* dv,
+                            int num_sms, cudaStream_t stream) {
   if (pr.d == 64) return launch_win_dkdv64(pr, maps, ws, L, dk, dv, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDkdv);
   bp.g0 = static_cast<__nv_bfloat16*>(dk);
@@ -958,7 +958,8 @@ cudaError_t launch_win_dkdv(const Problem& pr, const WinPlanMaps& maps, void* ws
   return launch_dkdv_k(win_dkdv_kernel, BwdCfg<128>::kSmemDkdv, num_sms, bp, stream);
 }
 
-cudaError_t launch_win_dq(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms, cudaStream_t stream) {
+cudaError_t launch_win_dq(const Problem& pr, const WinPlanMaps& maps, void* ws, const WsLayout& L, void* dq, int num_sms,
+                          cudaStream_t stream) {
   if (pr.d == 64) return launch_win_dq64(pr, maps, ws, L, dq, num_sms, stream);
   BwdParams bp = make_params(pr, nullptr, ws, L, kPassDq);
   bp.g0 = static_cast<__nv_bfloat16*>(dq);
