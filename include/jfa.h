@@ -137,8 +137,10 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
  * with the visible key tiles, not with the sequence length squared.  Keys that no query of their
  * sequence sees (when queries follow a longer history) are not read: they may hold anything,
  * NaN included, and get zero gradients.  A non-finite value in a key or value that some query
- * sees may reach every row of that sequence and head.  dk and dv sum over the group's query heads
- * in fp32, in a fixed order (results are bit-reproducible). */
+ * sees may reach every row of that sequence and head, in out and in the gradients.  A row one of
+ * whose scores is NaN (or +inf) gets out = NaN and lse = NaN; lse = -inf means that it sees no key
+ * (or that all its scores are -inf).  dk and dv sum over the group's query heads in fp32, in a fixed
+ * order (results are bit-reproducible). */
 size_t jfa_window_workspace_size(int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv, int sinks,
                                  int is_backward);
 jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const int64_t* q_offsets,
@@ -232,7 +234,8 @@ jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_str
  * L = lengths[b] (the newest token, at position L - 1, already appended), key j is visible iff
  * j < L and (j >= L - window or j < sinks); window >= 1, sinks >= 0.  L = 0 gives out = 0 and
  * lse = -inf.  Only pages that hold a visible key are looked up, and what rows hold that show
- * no key does not matter (NaN included).  A length below 0 or above max_pages * page_size is
+ * no key does not matter (NaN included); a NaN among its scores gives a head out = NaN and
+ * lse = NaN.  A length below 0 or above max_pages * page_size is
  * JFA_ERR_BAD_OFFSETS, a visible key on a page outside the cache JFA_ERR_BAD_PAGES. */
 jfa_status jfa_cache_attention(const jfa_cache* cache, const void* q, int H, int window, int sinks, float scale,
                                void* out, float* lse, void* workspace, size_t workspace_bytes, jfa_stream_t stream);

@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
 // 64 columns, 128-byte swizzle); four warps take 16 keys of each tile each, with the running
 // maximum, sum and output rows in registers:  S = Q K^T and O += P V on m16n8k16 products whose
 // 16 rows are the query heads (rows past G are zero); P is rounded to bf16 as an operand (at most
-// 2^-8 relative a term).
+// 2^-8 relative a term).  A NaN among a row's scores is in its sum and so in out and lse; only a sum
+// of 0 means that no key is seen (lse = -inf).
 constexpr int kTileKeys = 64;
 constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = 32 * (kAttnWarps + 1);
@@ -611,9 +612,9 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
             x1 += f * row[c + 1];
           }
           if (whole) {
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l != 0.f ? 1.f / l : 0.f;
             *reinterpret_cast<uint32_t*>(p.out + (int64_t(w.b) * p.H + h0 + r) * D + c0 + c) = pack_bf16x2(x0 * inv, x1 * inv);
-            if (c0 + c == 0) p.lse[int64_t(h0 + r) * p.B + w.b] = l > 0.f ? (u + log2f(l)) * kLn2 : -INFINITY;
+            if (c0 + c == 0) p.lse[int64_t(h0 + r) * p.B + w.b] = l != 0.f ? (u + log2f(l)) * kLn2 : -INFINITY;
           } else {
             *reinterpret_cast<float2*>(part + r * kPitch + c0 + c) = make_float2(x0, x1);
             if (c0 + c == 0) *reinterpret_cast<float2*>(part + r * kPitch + D) = make_float2(m, l);
@@ -649,9 +650,9 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
           x0 = x0 * f + v.x * fx;
           x1 = x1 * f + v.y * fx;
         }
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const float inv = l != 0.f ? 1.f / l : 0.f;
         *reinterpret_cast<uint32_t*>(p.out + (int64_t(w.b) * p.H + h0 + r) * D + c) = pack_bf16x2(x0 * inv, x1 * inv);
-        if (c == 0) p.lse[int64_t(h0 + r) * p.B + w.b] = l > 0.f ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2 : -INFINITY;
+        if (c == 0) p.lse[int64_t(h0 + r) * p.B + w.b] = l != 0.f ? ((m == -INFINITY ? 0.f : m) + log2f(l)) * kLn2 : -INFINITY;
       }
       if (tid == 0) p.arrived[unit] = 0;
     }

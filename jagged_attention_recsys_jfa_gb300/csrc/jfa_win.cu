@@ -423,8 +423,9 @@ __global__ void __launch_bounds__(kWinThreads, 2)
       }
       if (!ok) break;
       v_n += n;
-      // ---- epilogue: O / l -> bf16, lse = ln(sum) = (m + log2 l) * ln 2
-      const bool live = l > 0.f;
+      // ---- epilogue: O / l -> bf16, lse = ln(sum) = (m + log2 l) * ln 2; a NaN among the row's scores is
+      // in l and stays in both (only a sum of 0 is a row without keys)
+      const bool live = l != 0.f;
       const float inv_l = live ? 1.f / l : 0.f;
       if (valid) *lrow = live ? ((m == -INFINITY ? 0.f : m) + __log2f(l)) * kLn2 : -INFINITY;
       if (!warp_wait(&o_full, o_n & 1, abort_flag)) { ok = false; break; }
