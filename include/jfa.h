@@ -18,6 +18,7 @@
  * Causal: key j is visible to query i iff j <= i + (Lk_b - Lq_b) (bottom-right
  * alignment; equal lengths give the usual j <= i).  A query row with no visible key
  * (Lk_b = 0, or causal with Lq_b > Lk_b) gets out = 0 and lse = -inf, and no gradient.
+ * A row one of whose scores is NaN gets out = NaN and lse = NaN.
  *
  * Layout.  q, out, dout, dq: bf16 [total_q, H, d] row-major (token-major, heads
  * contiguous); k, v, dk, dv: bf16 [total_kv, H, d]; lse: fp32 [H, total_q];

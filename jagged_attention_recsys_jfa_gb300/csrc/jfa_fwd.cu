@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
       ++o_n;
       tc_fence_after();
       if (leader) trace_event(p.trace, kTraceCompute0 + s, tn, 22);
-      const bool live = l > 0.f;
+      const bool live = !(l <= 0.f);  // a NaN among the row's scores stays in out and lse
       const float inv_l = live ? 1.f / l : 0.f;
       const float m_use = (m == -INFINITY) ? 0.f : m;
       // all of the row's O columns in flight before one wait
