@@ -714,7 +714,7 @@ cudaError_t launch_cache_append(const jfa_cache& c, const CacheAppend& a, void* 
   p.rot = a.rot;
   p.interleaved = a.interleaved;
   p.status = &static_cast<WsHeader*>(ws)->status;
-  p.done = reinterpret_cast<unsigned*>(&static_cast<WsHeader*>(ws)->claim_fwd);
+  p.done = &static_cast<WsHeader*>(ws)->append_done;
   for (int i = 0; i < a.rot / 2; ++i) p.turn[i] = a.turn[i];
   for (int i = a.rot / 2; i < 64; ++i) p.turn[i] = 0;
   // few tokens: several warps for each, until the warps fill the card about twice over; then one

@@ -137,7 +137,8 @@ struct WsHeader {
   uint64_t wait_ns[5];
   int n_nsp;       // number of non-sequence-parallel backward items
   int planned;     // 1: the last plan found the offsets well formed
-  int pad[40];
+  unsigned append_done;  // cache append: CTAs that have read the lengths (written by no other call, left at 0)
+  int pad[39];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
 
