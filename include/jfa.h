@@ -224,7 +224,10 @@ size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
  * may be `lengths` itself.  Each cache row must be written by one token only.
  *
  * Errors on the device: malformed offsets or a negative length (JFA_ERR_BAD_OFFSETS); a token
- * whose page is missing (JFA_ERR_BAD_PAGES; that token is not stored). */
+ * whose page is missing (JFA_ERR_BAD_PAGES; that token is not stored).  After an error
+ * lengths_out[b] is lengths[b] for a sequence with a negative length or a token that was not stored
+ * (the call may be repeated for it), and for all sequences when the offsets are malformed; the
+ * others advance. */
 jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                             const void* q, int64_t q_stride, int H, const int64_t* offsets, int64_t total,
                             const double* frequencies, int rot_dim, int interleaved, void* q_out, void* k_out,

@@ -77,6 +77,16 @@ __device__ __forceinline__ uint32_t rot_pair(uint32_t a, const float2& c) {
   return pack_bf16x2(bf16lo(a) * c.x - bf16hi(a) * c.y, bf16hi(a) * c.x + bf16lo(a) * c.y);
 }
 
+// Whether `n` new tokens of sequence b behind its `len` cached ones all have a page.
+__device__ __forceinline__ bool stores_all(const AppendParams& p, int b, int len, int64_t n) {
+  if (len < 0 || len + n > int64_t(p.max_pages) * p.page_size) return n == 0 && len >= 0;
+  for (int64_t pos = len; pos < len + n; pos += p.page_size - pos % p.page_size) {
+    const int page = p.page_table[int64_t(b) * p.max_pages + pos / p.page_size];
+    if (page < 0 || page >= p.num_pages) return false;
+  }
+  return true;
+}
+
 // A token is one warp's (or, when there are few tokens, split over warps_per_token warps of a
 // CTA): D / 16 lanes share a row, and a lane moves two 16-byte chunks of it, chunks c and c + r/16
 // where they are a half-split pair's halves, else neighbours, so that both elements of every pair
@@ -203,11 +213,25 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
     if (tid == 0) {
       __threadfence();
       last_cta = atomicAdd(p.done, 1u) == gridDim.x - 1;
+      __threadfence();
     }
     __syncthreads();
     if (last_cta) {
-      for (int b = tid; b < p.B; b += kAppendThreads)
-        p.lengths_out[b] = p.lengths[b] + int32_t(p.offsets[b + 1] - p.offsets[b]);
+      // an error of this call (or an earlier one that nobody has asked for) is in *status by now:
+      // then each sequence is looked at for tokens that were not stored
+      const bool errors = *static_cast<volatile const int*>(p.status) != 0;
+      bool bad = false;
+      if (errors) {
+        for (int b = tid; b < p.B; b += kAppendThreads) bad |= p.offsets[b + 1] < p.offsets[b];
+        bad |= p.offsets[0] != 0 || p.offsets[p.B] > p.total;
+        bad = __syncthreads_or(bad);
+      }
+      for (int b = tid; b < p.B; b += kAppendThreads) {
+        const int len = p.lengths[b];
+        const int64_t n = p.offsets[b + 1] - p.offsets[b];
+        const bool grows = !errors || (!bad && stores_all(p, b, len, n));
+        p.lengths_out[b] = grows ? int32_t(len + n) : len;
+      }
       if (tid == 0) *p.done = 0;
     }
   }

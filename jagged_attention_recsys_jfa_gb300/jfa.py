@@ -570,7 +570,8 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
     position (rotary_frequencies), or None for no rotation.  Writes the caches; returns the
     rotated q (None without q), k_out (the rotated keys where a tensor was given for them) and
     the lengths after the call (lengths_out may be `lengths` itself).  Asynchronous; device-side
-    errors are reported by jfa_check_status(workspace).
+    errors are reported by jfa_check_status(workspace), and a sequence that they keep from being
+    stored whole keeps its length.
     """
     lib = load_library()
     cache = _cache_struct(k_cache, v_cache, page_table, lengths)

@@ -33,3 +33,44 @@ def test_append_on_a_workspace_that_served_other_calls(windowed):
         jfa.jfa_cache_append(rows, rows, off, k, v, table, n, lengths_out=n, workspace=ws)
         assert jfa.jfa_check_status(ws) == 0
         assert n.tolist() == [3 + 2 * (step + 1), 20 + 3 * (step + 1)]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_lengths_after_an_error(in_place):
+    """A sequence keeps its length when a token of it was not stored; malformed offsets change none."""
+    g = gen(62)
+    kc, vc, table = make_cache(g, [40, 40, 40], 1, 64, 16, spare_cols=0)  # three pages each
+    k = normal(g, 90, 1, 64)
+    ws = jfa.new_cache_workspace(3, 1, 1, 64, DEV)
+
+    def run(lens, offs, table=table):
+        n = int32(lens)
+        out = n if in_place else torch.full((3,), 77, dtype=torch.int32, device=DEV)
+        jfa.jfa_cache_append(k, k, torch.tensor(offs, device=DEV), kc, vc, table, n, lengths_out=out, workspace=ws)
+        return jfa.jfa_check_status(ws), out.tolist()
+
+    def with_page(b, i, page):
+        t = table.clone()
+        t[b, i] = page
+        return t
+
+    assert run((30, 0, 7), (0, 2, 4, 4)) == (0, [32, 2, 7])
+    assert run((47, 0, 7), (0, 2, 4, 9)) == (7, [47, 2, 12])              # position 48 lies past the table
+    assert run((46, 48, 7), (0, 2, 3, 9)) == (7, [48, 48, 13])
+    assert run((2 ** 31 - 1, 0, 0), (0, 2, 4, 9)) == (7, [2 ** 31 - 1, 2, 5])
+    for bad in (-1, kc.shape[0], 1 << 30):
+        assert run((14, 0, 7), (0, 2, 4, 4), with_page(0, 1, bad)) == (0, [16, 2, 7])       # not needed
+        assert run((15, 0, 7), (0, 2, 4, 4), with_page(0, 1, bad)) == (7, [15, 2, 7])
+        assert run((0, 40, 0), (0, 40, 42, 90), with_page(0, 2, bad)) == (7, [0, 42, 48])   # its last page
+        assert run((0, 40, 0), (0, 40, 42, 82), with_page(2, 0, bad)) == (7, [40, 42, 0])   # its first
+    assert run((-3, 30, 5), (0, 2, 4, 4)) == (5, [-3, 32, 5])
+    assert run((5, 6, 7), (0, 2, 4, 4), with_page(2, 0, -1)) == (0, [7, 8, 7])              # nothing for it to store
+    for offs in ([0, 3, 2, 4], [0, 3, 5, 91], [1, 3, 4, 5], [0, -1, 3, 5], [0, 2, 4, 1 << 40]):
+        status, after = run((5, 6, 7), offs)  # such offsets also put tokens past the table: either error may be the first
+        assert status in (5, 7) and after == [5, 6, 7]
+    assert run((5, 6, 7), (0, 2, 4, 4)) == (0, [7, 8, 7])
+    # a status that nobody has read yet does not hold later calls back
+    n = int32([47, 0, 7])
+    jfa.jfa_cache_append(k, k, torch.tensor([0, 2, 4, 9], device=DEV), kc, vc, table, n, lengths_out=n, workspace=ws)
+    jfa.jfa_cache_append(k, k, torch.tensor([0, 0, 4, 9], device=DEV), kc, vc, table, n, lengths_out=n, workspace=ws)
+    assert n.tolist() == [47, 6, 17] and jfa.jfa_check_status(ws) == 7
