@@ -57,7 +57,8 @@ typedef enum {
   JFA_OK = 0,
   JFA_ERR_INVALID_ARG = 1, /* null pointer, bad size, misaligned pointer */
   JFA_ERR_UNSUPPORTED = 2, /* head_dim not in {64,128}, unsupported bias kind or bias gradient */
-  JFA_ERR_WORKSPACE = 3,   /* workspace missing, too small or misaligned */
+  JFA_ERR_WORKSPACE = 3,   /* workspace missing, too small or misaligned; device: one that the cache attention
+                              cannot use until it is zeroed */
   JFA_ERR_CUDA = 4,        /* a CUDA runtime/driver call failed (launch, tensor-map encode) */
   JFA_ERR_BAD_OFFSETS = 5, /* device: offsets not 0-based, not monotone, or last != total (also kind-2 bias block offsets) */
   JFA_ERR_TIMEOUT = 6,     /* device: a bounded pipeline wait ran out; outputs unspecified */
@@ -198,8 +199,10 @@ typedef struct {
 /* Bytes of workspace jfa_cache_attention needs (jfa_cache_append needs the first 256 of them);
  * 256-byte aligned, zero before its first use, every call leaves what it needs zero, zero again.
  * One workspace serves both calls, at any sizes that it is large enough for, but only one call
- * at a time.  Zero it again after a JFA_ERR_TIMEOUT, and before it serves these calls when other
- * calls of this library have used it.  Returns 0 on invalid sizes. */
+ * at a time.  When forward or backward calls of this library have used it, or after a
+ * JFA_ERR_TIMEOUT, zero it again: as long as its counters may not be zero, jfa_cache_attention
+ * computes nothing and reports JFA_ERR_WORKSPACE.  (jfa_cache_append needs no zeroing.)  Returns 0
+ * on invalid sizes. */
 size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
 
 /* Append new tokens, keys rotated by their position on the way.  Sequence b's new tokens are

@@ -567,7 +567,7 @@ const char* jfa_status_string(jfa_status s) {
     case JFA_OK: return "ok";
     case JFA_ERR_INVALID_ARG: return "invalid argument";
     case JFA_ERR_UNSUPPORTED: return "unsupported configuration (head_dim must be 64 or 128; bias kind 0 or 1)";
-    case JFA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
+    case JFA_ERR_WORKSPACE: return "workspace missing, misaligned, too small, or to be zeroed first (cache attention)";
     case JFA_ERR_CUDA: return "CUDA runtime or driver call failed";
     case JFA_ERR_BAD_OFFSETS: return "offsets must start at 0, be non-decreasing and end at the row count";
     case JFA_ERR_TIMEOUT: return "a bounded pipeline wait ran out on the device; outputs are unspecified";

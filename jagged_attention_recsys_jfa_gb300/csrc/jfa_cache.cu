@@ -273,6 +273,7 @@ struct CacheAttnParams {
   float scale_log2;
   int rows;                     // query heads of a block that are real at most: min(G, 16)
   int* status;
+  int* counters_used;           // nonzero: `arrived` may not be at 0
   unsigned* arrived;            // [units] partial sums written (left at 0)
   float* partial;               // [2 * grid][rows][d + 2]
 };
@@ -344,6 +345,7 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
   __shared__ uint64_t full[C::kStages], empty[C::kStages];
   __shared__ long long run_end[kAttnThreads];  // tiles of all units before the end of each thread's run of sequences
   __shared__ int abort_sh;
+  __shared__ int refused;
   __shared__ int is_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -358,6 +360,8 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
   grid_launch_dependents();
   volatile int* abort_flag = &abort_sh;
 
+  // (one thread reads the word: another CTA whose wait has run out may be writing it)
+  if (tid == 0) refused = *static_cast<volatile const int*>(p.counters_used);
   // ---- tiles per run of consecutive sequences, then their running sums
   const int run = (p.B + kAttnThreads - 1) / kAttnThreads;
   {
@@ -384,6 +388,10 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
     }
   }
   __syncthreads();
+  if (refused) {  // uniform over the CTA, nothing in flight
+    if (tid == 0) raise_status(p.status, JFA_ERR_WORKSPACE);
+    return;
+  }
   const int64_t total = run_end[kAttnThreads - 1];
 
   // ---- sequences that show no key: out 0, lse -inf
@@ -474,7 +482,10 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
         off = off_next;
       }
     }
-    if (!ok && lane == 0) raise_status(p.status, JFA_ERR_TIMEOUT);
+    if (!ok && lane == 0) {
+      raise_status(p.status, JFA_ERR_TIMEOUT);
+      *p.counters_used = 1;  // units that this CTA leaves undone keep their counts
+    }
     // every copy this warp started has landed before the CTA can exit
     const uint32_t first = n > uint32_t(C::kStages) ? n - C::kStages : 0;
     for (uint32_t m = first; m < n; ++m) {
@@ -680,18 +691,12 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
       }
       if (tid == 0) p.arrived[unit] = 0;
     }
-    if (!ok && lane == 0) raise_status(p.status, JFA_ERR_TIMEOUT);
+    if (!ok && lane == 0) {
+      raise_status(p.status, JFA_ERR_TIMEOUT);
+      *p.counters_used = 1;  // units that this CTA leaves undone keep their counts
+    }
   }
 }
-
-constexpr int kMaxAttnCtas = 512;  // bounds the partial rows in the workspace
-
-// The workspace behind its header: the partial rows, then the units' counters.  The counters start
-// at the same place for every call, behind the most partial rows that any call writes: calls of
-// different sizes may share a workspace, and one call's partial rows must not be found where
-// another expects its counters at zero.
-constexpr size_t kPartialAt = sizeof(WsHeader);
-constexpr size_t kArrivedAt = kPartialAt + size_t(2) * kMaxAttnCtas * 16 * (128 + 2) * sizeof(float);
 
 template <int D>
 cudaError_t launch_attn_t(const CUtensorMap& km, const CUtensorMap& vm, const CacheAttnParams& p, int num_sms,
@@ -774,6 +779,7 @@ cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& km, co
   p.sinks = sinks;
   p.scale_log2 = scale * kLog2e;
   p.status = &reinterpret_cast<WsHeader*>(w)->status;
+  p.counters_used = &reinterpret_cast<WsHeader*>(w)->counters_used;
   p.arrived = reinterpret_cast<unsigned*>(w + kArrivedAt);
   p.partial = reinterpret_cast<float*>(w + kPartialAt);
   return c.d == 128 ? launch_attn_t<128>(km, vm, p, num_sms, stream) : launch_attn_t<64>(km, vm, p, num_sms, stream);

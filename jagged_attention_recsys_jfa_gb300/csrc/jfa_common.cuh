@@ -138,9 +138,19 @@ struct WsHeader {
   int n_nsp;       // number of non-sequence-parallel backward items
   int planned;     // 1: the last plan found the offsets well formed
   unsigned append_done;  // cache append: CTAs that have read the lengths (written by no other call, left at 0)
-  int pad[39];
+  int counters_used;     // 1: the cache attention's counters (kArrivedAt) may hold anything: another call's
+                         // layout has reached them, or a wait of that call ran out
+  int pad[38];
 };
 static_assert(sizeof(WsHeader) == 256, "header is 256 bytes");
+
+// The cache attention's workspace behind the header: the partial rows, then the units' counters.  The
+// counters start at the same place for every call, behind the most partial rows that any call writes:
+// calls of different sizes may share a workspace, and one call's partial rows must not be found where
+// another expects its counters at zero.
+constexpr int kMaxAttnCtas = 512;  // bounds the partial rows
+constexpr size_t kPartialAt = sizeof(WsHeader);
+constexpr size_t kArrivedAt = kPartialAt + size_t(2) * kMaxAttnCtas * 16 * (128 + 2) * sizeof(float);
 
 struct WsLayout {
   size_t maps = 0;       // CUtensorMap[B][kNumMapSlots], then CUtensorMap[kNumMapSlots][kTailMaps]

@@ -255,7 +255,10 @@ __global__ void __launch_bounds__(1024, 1) plan_kernel(const __grid_constant__ P
       bad = 1;
     if (p.jb_off && (p.jb_off[0] != 0 || p.jb_off[p.B] != p.jb_plane)) bad = 1;
   }
-  if (blockIdx.x == 0 && tid == 0) hdr->claim_fwd = hdr->claim_dq = hdr->claim_dkv = hdr->claim_fused = hdr->claim_nsp = 0;
+  if (blockIdx.x == 0 && tid == 0) {
+    hdr->claim_fwd = hdr->claim_dq = hdr->claim_dkv = hdr->claim_fused = hdr->claim_nsp = 0;
+    if (p.L.total > kArrivedAt) hdr->counters_used = 1;
+  }
   bad = __syncthreads_or(bad);
   if (bad) {
     if (tid == 0) {

@@ -204,7 +204,10 @@ __global__ void __launch_bounds__(1024, 1) win_plan_kernel(const __grid_constant
     if (p.q_off[0] != 0 || p.kv_off[0] != 0 || p.q_off[p.B] != p.total_q || p.kv_off[p.B] != p.total_kv)
       bad = 1;
   }
-  if (blockIdx.x == 0 && tid == 0) hdr->claim_fwd = hdr->claim_dq = hdr->claim_dkv = hdr->claim_fused = hdr->claim_nsp = 0;
+  if (blockIdx.x == 0 && tid == 0) {
+    hdr->claim_fwd = hdr->claim_dq = hdr->claim_dkv = hdr->claim_fused = hdr->claim_nsp = 0;
+    if (p.L.total > kArrivedAt) hdr->counters_used = 1;
+  }
   bad = __syncthreads_or(bad);
   if (bad) {
     if (tid == 0) {

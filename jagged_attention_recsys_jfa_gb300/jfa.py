@@ -544,7 +544,9 @@ def cache_workspace_size(B, H, H_kv, d) -> int:
 
 
 def new_cache_workspace(B, H, H_kv, d, device) -> torch.Tensor:
-    """A zero-initialised workspace for jfa_cache_append and jfa_cache_attention."""
+    """A zero-initialised workspace for jfa_cache_append and jfa_cache_attention, one call at a time.
+    Zero it again after a timeout, or when forward or backward calls have used it: as long as its
+    counters may not be zero, jfa_cache_attention reports JFA_ERR_WORKSPACE."""
     nbytes = cache_workspace_size(B, H, H_kv, d)
     if nbytes == 0:
         raise ValueError(f"no cache workspace for B={B}, H={H}, H_kv={H_kv}, d={d}")

@@ -74,3 +74,24 @@ def test_lengths_after_an_error(in_place):
     jfa.jfa_cache_append(k, k, torch.tensor([0, 2, 4, 9], device=DEV), kc, vc, table, n, lengths_out=n, workspace=ws)
     jfa.jfa_cache_append(k, k, torch.tensor([0, 0, 4, 9], device=DEV), kc, vc, table, n, lengths_out=n, workspace=ws)
     assert n.tolist() == [47, 6, 17] and jfa.jfa_check_status(ws) == 7
+
+
+def test_attention_refuses_a_workspace_that_served_other_calls():
+    """Where another call's data may have reached its counters: an error instead of wrong sums, until
+    the workspace is zeroed.  A call that did not reach them changes nothing."""
+    g = gen(65)
+    k, v, table, n = filled(g, [9000, 700, 3], 2, 64, 64)
+    q = normal(g, 3, 2, 64)
+    ws = torch.zeros(64 << 20, dtype=torch.uint8, device=DEV)
+    check_attention(q, k, v, table, n, None, 0, workspace=ws)
+    for lens, refused in (([1] * 20000, True), ([2000], False)):
+        x, _ = make(lens, lens, 2, 2, 64, 64)
+        for call in (lambda: jfa.jfa_window_forward(**x, window=90, sinks=2, workspace=ws),
+                     lambda: jfa.jfa_forward(**x, workspace=ws)):
+            call()
+            if refused:
+                for _ in range(2):
+                    jfa.jfa_cache_attention(q, k, v, table, n, workspace=ws)
+                    assert jfa.jfa_check_status(ws) == 3
+                ws.zero_()
+            check_attention(q, k, v, table, n, None, 0, workspace=ws)
