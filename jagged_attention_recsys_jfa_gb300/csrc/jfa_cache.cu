@@ -311,8 +311,11 @@ struct Walk {
   SeqTiles s;
 };
 
+// Plain loads of `lengths` and of q: the kernel in front, which may still be running when this grid
+// becomes resident, may be the append that writes both, and the read-only path is for data that stays
+// as it is for the grid's whole life.  (Page tables and offsets are written by no kernel of the library.)
 __device__ __forceinline__ int checked_len(const CacheAttnParams& p, int b) {
-  const int len = __ldg(p.lengths + b);
+  const int len = p.lengths[b];
   return len < 0 || len > int64_t(p.max_pages) * p.page_size ? 0 : len;
 }
 
@@ -368,7 +371,7 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
     long long sum = 0;
     for (int b = tid * run; b < min(p.B, (tid + 1) * run); ++b) {
       const int len = checked_len(p, b);
-      if (len != __ldg(p.lengths + b) && blockIdx.x == 0) raise_status(p.status, JFA_ERR_BAD_OFFSETS);
+      if (len != p.lengths[b] && blockIdx.x == 0) raise_status(p.status, JFA_ERR_BAD_OFFSETS);
       sum += seq_tiles(len, p.window, p.sinks).n;
     }
     run_end[tid] = sum * p.Hkv * p.RB;
@@ -508,10 +511,10 @@ __global__ void __launch_bounds__(kAttnThreads, CacheCfg<D>::kCtasPerSm)
         const uint32_t* q1 = q0 + 8 * D / 2;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          qa[kk][0] = g < rows ? __ldg(q0 + kk * 8) : 0u;
-          qa[kk][1] = g + 8 < rows ? __ldg(q1 + kk * 8) : 0u;
-          qa[kk][2] = g < rows ? __ldg(q0 + kk * 8 + 4) : 0u;
-          qa[kk][3] = g + 8 < rows ? __ldg(q1 + kk * 8 + 4) : 0u;
+          qa[kk][0] = g < rows ? q0[kk * 8] : 0u;
+          qa[kk][1] = g + 8 < rows ? q1[kk * 8] : 0u;
+          qa[kk][2] = g < rows ? q0[kk * 8 + 4] : 0u;
+          qa[kk][3] = g + 8 < rows ? q1[kk * 8 + 4] : 0u;
         }
       }
       float o[D / 8][4];

@@ -76,6 +76,39 @@ def test_lengths_after_an_error(in_place):
     assert n.tolist() == [47, 6, 17] and jfa.jfa_check_status(ws) == 7
 
 
+def test_decoding_without_a_pause():
+    """Steps enqueued one behind the other give what synchronised steps give, bit for bit."""
+    B, H, G, d, page, steps = 48, 8, 2, 64, 16, 300
+    g = gen(63)
+    start = [int(x) for x in np.random.RandomState(2).randint(0, 200, B)]
+    k0, v0, table = make_cache(g, [n + steps for n in start], G, d, page)
+    k0.zero_(), v0.zero_()
+    x = normal(g, steps, B, H + 2 * G, d)
+    off, f = torch.arange(B + 1, device=DEV), jfa.rotary_frequencies(d)
+
+    def run(wait):
+        kc, vc, n = k0.clone(), v0.clone(), int32(start)
+        ws = jfa.new_cache_workspace(B, H, G, d, DEV)
+        q_rot = torch.empty(B, H, d, dtype=BF16, device=DEV)
+        outs = torch.empty(steps, B, H, d, dtype=BF16, device=DEV)
+        lses = torch.empty(steps, H, B, device=DEV)
+        torch.cuda.synchronize()
+        for t in range(steps):
+            jfa.jfa_cache_append(x[t][:, H:H + G], x[t][:, H + G:], off, kc, vc, table, n, q=x[t][:, :H], frequencies=f,
+                                 q_out=q_rot, lengths_out=n, workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+            jfa.jfa_cache_attention(q_rot, kc, vc, table, n, 150, 3, out=outs[t], lse=lses[t], workspace=ws)
+            if wait:
+                torch.cuda.synchronize()
+        assert jfa.jfa_check_status(ws) == 0 and n.tolist() == [a + steps for a in start]
+        return outs, lses, kc, vc
+
+    want = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(run(False), want))
+
+
 def test_attention_refuses_a_workspace_that_served_other_calls():
     """Where another call's data may have reached its counters: an error instead of wrong sums, until
     the workspace is zeroed.  A call that did not reach them changes nothing."""
