@@ -147,10 +147,10 @@ __global__ void __launch_bounds__(256, 4) preprocess_kernel(const PreParams p) {
     int lo = 0, hi = p.B;  // the last b with qpad[b] <= pr (qpad[0] = 0 <= pr < qpad[B])
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(p.qpad + mid) <= pr) lo = mid; else hi = mid;
+      if (p.qpad[mid] <= pr) lo = mid; else hi = mid;
     }
     const int64_t qo = __ldg(p.q_off + lo);
-    const int64_t i = pr - __ldg(p.qpad + lo);
+    const int64_t i = pr - p.qpad[lo];  // (qpad: plain loads, the planner in front writes it)
     if (i >= __ldg(p.q_off + lo + 1) - qo) {  // padding row
       for (int h = lane; h < p.H; h += 32) {
         p.delta[int64_t(h) * p.qpad_cap + pr] = 0.f;

@@ -501,18 +501,19 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_kernel(const FwdParams p) {
         const int kv0 = j * kBN;
         const bool last = (j == nkv - 1);
         // relative-position bias * log2(e) of this tile's columns, loaded before the wait so the
-        // loads overlap the MMAs (0 on padded key columns, which then score exactly 0)
+        // loads overlap the MMAs (0 on padded key columns, which then score exactly 0).  Plain loads:
+        // the table is written by the planner, which may still run when this grid becomes resident
         float bw[kBias ? 128 : 1];
         if (kBias) {
           const int n_real = min(kBN, it.Lk - kv0);
           const int idx0 = kv0 - i + p.center;  // bucket of column c: idx0 + c
           if (idx0 >= 0 && idx0 + kBN - 1 < p.num_buckets && n_real == kBN) {
 #pragma unroll
-            for (int c = 0; c < 128; ++c) bw[c] = __ldg(brow + idx0 + c);
+            for (int c = 0; c < 128; ++c) bw[c] = brow[idx0 + c];
           } else {
 #pragma unroll
             for (int c = 0; c < 128; ++c)
-              bw[c] = c < n_real ? __ldg(brow + min(max(idx0 + c, 0), p.num_buckets - 1)) : 0.f;
+              bw[c] = c < n_real ? brow[min(max(idx0 + c, 0), p.num_buckets - 1)] : 0.f;
           }
         }
         if (!mbar_wait(&s_full[s], s_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }

@@ -11,9 +11,19 @@ import pytest
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "jagged_attention_recsys_jfa_gb300", "csrc")
 
-# what may be read so, by file: arrays that only callers write
+# what may be read so, by file: arrays that only callers write, and what comes from a kernel at least two in front
 ALLOWED = {
     "jfa_cache.cu": {"p.offsets", "offsets", "p.page_table", "table"},
+    "jfa_fwd.cu": set(),
+    # dout, out and lse: from callers, or the forward, behind which the planner runs; brow: the bias table, from
+    # the planner, behind which the preprocess runs; lse2, delta: from the preprocess, read by the dQ pass behind dK/dV
+    "jfa_bwd.cu": {"p.dout", "p.out", "drow", "orow", "p.lse", "p.q_off", "brow", "p.lse2", "p.delta"},
+    "jfa_win.cu": set(),
+    "jfa_win_bwd.cu": {"p.lse2", "p.delta", "part", "pv"},  # part, pv: from dK/dV, read by the join behind dQ
+    "jfa_win_dkdv.cu": set(),
+    "jfa_win_dq.cu": {"p.lse2", "p.delta"},
+    "jfa_plan.cu": set(),
+    "jfa_win_plan.cu": set(),
 }
 
 
