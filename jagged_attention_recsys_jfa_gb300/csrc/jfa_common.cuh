@@ -14,15 +14,19 @@ constexpr int kBN = 128;  // key rows per tile
 constexpr int kMaxBuckets = 8192;
 constexpr int kCostBuckets = 2048;  // planner's counting-sort buckets (cost clamped)
 // Bounded pipeline waits.  A wait that outlasts its limit ends the CTA with
-// JFA_ERR_TIMEOUT, so the limit must exceed any wait a correct launch can have.  Waits
-// inside an item's tile pipeline last at most a few units' time (a unit visits at most
-// 2 x 128 tile pairs, well under a millisecond) and keep the fixed kWaitTimeoutNs.  The
-// waits that scale with the launch are the item hand-offs of the scheduler ring: a CTA's
-// scheduler waits for item k - 2 to be released, and its roles for item k to be
-// published, i.e. for up to about a CTA's whole share of the launch.  The planner
-// therefore sizes each list's hand-off limit from the work it planned: a 2 s floor plus a
-// generous time per tile pair (kWaitNsPerTilePair, ~30x the measured ~1 us per 128x128
-// tile pair on one SM) for one CTA's share of the pairs and the costliest single item.
+// JFA_ERR_TIMEOUT, so the limit must exceed any wait a correct launch can have.  Waits for
+// one step of an item's tile pipeline (a load, a product, a few tile pairs ahead) keep the
+// fixed kWaitTimeoutNs.  The others scale with the launch: the item hand-offs of the
+// scheduler ring (a CTA's scheduler waits for item k - 2 to be released, and its roles for
+// item k to be published, i.e. for up to about a CTA's whole share of the launch), and the
+// waits of the roles that meet an item only at its ends, the loader of its resident tiles
+// and the epilogue, which last a whole unit: a windowed key tile meets every query tile that
+// its keys' windows reach, of every query head of its group, which nothing bounds (a million
+// tile pairs, 64 heads of 2M queries on one key head, are over 2 s).  The planner
+// therefore sizes each list's limit from the work it planned: a 2 s floor plus a
+// generous time per tile pair (kWaitNsPerTilePair, 10 to 30 times the 1 to 3.2 us that a
+// 128x128 tile pair takes in the kernels) for one CTA's share of the pairs and the costliest
+// single item.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;   // floor: 2 s
 constexpr uint64_t kWaitNsPerTilePair = 32000ull;    // 32 us per planned tile pair
 constexpr uint64_t kWaitLimitCapNs = 3600ull * 1000000000ull;  // an hour: no overflow

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
           const int skip = !sink ? meta_win(wi).skip : 0;
           const TileMap mk = win_tile_map(maps, kMapK, wi.b, sink ? 0 : kt, kBN, skip);
           const TileMap mv = win_tile_map(maps, kMapV, wi.b, sink ? 0 : kt, kBN, skip);
-          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
           mbar_arrive_expect_tx(&kv_full, sink ? uint32_t(p.sink_rows) * D * 4 : 2u * C::kTileBytes);
           load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
@@ -433,10 +433,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
         const int64_t slot = sink_slot0(it.qp / kBM, it.b, p.group) * p.win.H_kv +
                              int64_t(it.h) * win_sink_chunks(Lq, ws, p.group) + ku.chunk;
         float* part = p.spart + (slot * 2 * p.win.sinks + row) * int64_t(D);
-        if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
         tc_fence_after();
         drain_row_f32<D>(tmem + lane_addr + C::kColA1, part + p.win.sinks * int64_t(D), row < ws.ns, &dv_empty);
-        if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
         ++acc_n;
         tc_fence_after();
         drain_row_f32<D>(tmem + lane_addr + C::kColA0, part, row < ws.ns, &dk_empty);
@@ -450,10 +450,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dkdv_kernel(const BwdPara
         }
         continue;
       }
-      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA1, 1.f, dv_row, valid, &dv_empty);
-      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA0, p.scale, dk_row, valid, &dk_empty);
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
         if (query_unit(p, wi, qt).nkv == 0) continue;
         const TileMap mq = win_tile_map(p.maps, kMapQ, wi.b, qt, kBM, 0);
         const TileMap mdo = win_tile_map(p.maps, kMapDO, wi.b, qt, kBM, 0);
-        if (!mbar_wait(&qdo_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&qdo_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
         trace_event(p.trace, kTraceLoader, tn, 1);
         mbar_arrive_expect_tx(&qdo_full, 2 * C::kTileBytes);
         load_tile<D>(sQ, mq.map, &qdo_full, wi.h * D, mq.y);
@@ -866,7 +866,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) win_dq_kernel(const BwdParams
         for (int c0 = 0; c0 < D; c0 += 32) store_acc_row<32>(0, 0.f, dq_row + c0, valid, true);
         continue;
       }
-      if (!mbar_wait(&acc_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&acc_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColDQ, p.scale, dq_row, valid, &acc_empty);

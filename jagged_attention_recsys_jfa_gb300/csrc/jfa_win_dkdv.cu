@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kWinThreads, 2)
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
           }
-          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
           mbar_arrive_expect_tx(&kv_full, half ? uint32_t(p.sink_rows) * kD * 4 : 2u * kTileBytes);
           const int col = wi.h * kD;
           tma_load_2d(sK, mk.map, &kv_full, col, mk.y);
