@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
           }
-          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
           mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
           load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
@@ -704,10 +704,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dkdv_kernel(const BwdParams p
         }
         continue;
       }
-      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA1, 1.f, dv_row, valid, &dv_empty);
-      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA0, p.scale, dk_row, valid, &dk_empty);
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
           tmap_acquire(mq.map);
           tmap_acquire(mdo.map);
         }
-        if (!mbar_wait(&qdo_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&qdo_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
         trace_event(p.trace, kTraceLoader, tn, 1);
         mbar_arrive_expect_tx(&qdo_full, 2 * C::kTileBytes);
         load_tile<D>(sQ, mq.map, &qdo_full, wi.h * D, mq.y);
@@ -1174,7 +1174,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) dq_kernel(const BwdParams p) 
         for (int c0 = 0; c0 < D; c0 += 32) store_acc_row<32>(0, 0.f, dq_row + c0, valid, true);
         continue;
       }
-      if (!mbar_wait(&acc_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&acc_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColDQ, p.scale, dq_row, valid, &acc_empty);
@@ -1292,7 +1292,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) fused_kernel(const BwdParams 
           }
           const float* l2src = p.lse2 + int64_t(wi.h) * p.qpad_cap + wi.qp;
           const float* dsrc = p.delta + int64_t(wi.h) * p.qpad_cap + wi.qp;
-          if (!mbar_wait(&q_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+          if (!mbar_wait(&q_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
           trace_event(p.trace, kTraceLoader, tn, 1);
           mbar_arrive_expect_tx(&q_full, 2 * C::kTileBytes + 2 * kBM * 4);
           load_tile<D>(sQ, mq.map, &q_full, wi.h * D, mq.y);
@@ -1653,10 +1653,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) fused_kernel(const BwdParams 
         store_acc_row_own<D>(0, 0.f, dv_row, valid, true);
         continue;
       }
-      if (!mbar_wait(&dv_full, g & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dv_full, g & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       tc_fence_after();
       drain_row_own<D>(tmem + lane_addr + C::kColFdV, 1.f, dv_row, valid, &dv_empty);
-      if (!mbar_wait(&dk_full, g & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dk_full, g & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       tc_fence_after();
       drain_row_own<D>(tmem + lane_addr + C::kColP, p.scale, dk_row, valid, &dk_empty);
       ++g;
@@ -1665,7 +1665,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) fused_kernel(const BwdParams 
      const bool qvalid = row < Lq;
      __nv_bfloat16* dq_row = p.g2 + ((it.qo + row) * p.H + it.h) * int64_t(D);
      if (live) {
-       if (!mbar_wait(&dq_full, item_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+       if (!mbar_wait(&dq_full, item_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
        ++item_n;
        tc_fence_after();
        drain_row_own<D>(tmem + lane_addr + C::kColFdQ, p.scale, dq_row, qvalid, &dq_empty);
@@ -1782,7 +1782,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) nsp_kernel(const BwdParams p)
             tmap_acquire(mk.map);
             tmap_acquire(mv.map);
           }
-          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+          if (!mbar_wait(&kv_empty, (item_n & 1) ^ 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
           mbar_arrive_expect_tx(&kv_full, 2 * C::kTileBytes);
           load_tile<D>(sK, mk.map, &kv_full, wi.h * D, mk.y);
           load_tile<D>(sV, mv.map, &kv_full, wi.h * D, mv.y);
@@ -2168,7 +2168,7 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) nsp_kernel(const BwdParams p)
         const int jl = kv_tiles_for_q_tile(qt, Lq, Lk, causal) - 1;  // last key tile that sees qt
         float* acc = p.dqacc + ((qo + qi) * p.H + it.h) * int64_t(D);
         __nv_bfloat16* dq_row = p.g2 + ((qo + qi) * p.H + it.h) * int64_t(D);
-        if (!mbar_wait(&dq_full, g & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+        if (!mbar_wait(&dq_full, g & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
         ++g;
         tc_fence_after();
         if (leader) trace_event(p.trace, kTraceLoader, tn, 30);
@@ -2206,10 +2206,10 @@ __global__ void __launch_bounds__(kThreadsDkdv, 1) nsp_kernel(const BwdParams p)
       }
       if (!ok) break;
       if (leader) trace_event(p.trace, kTraceLoader, tn, 32);
-      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dv_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA1, 1.f, dv_row, valid, &dv_empty);
-      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, kWaitTimeoutNs)) { ok = false; break; }
+      if (!mbar_wait(&dk_full, acc_n & 1, abort_flag, meta.wait_ns, kWaitTimeoutNs)) { ok = false; break; }
       ++acc_n;
       tc_fence_after();
       drain_acc_rows<D>(tmem + lane_addr + C::kColA0, p.scale, dk_row, valid, &dk_empty);

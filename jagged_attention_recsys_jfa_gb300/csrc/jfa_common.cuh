@@ -20,9 +20,10 @@ constexpr int kCostBuckets = 2048;  // planner's counting-sort buckets (cost cla
 // scheduler ring (a CTA's scheduler waits for item k - 2 to be released, and its roles for
 // item k to be published, i.e. for up to about a CTA's whole share of the launch), and the
 // waits of the roles that meet an item only at its ends, the loader of its resident tiles
-// and the epilogue, which last a whole unit: a windowed key tile meets every query tile that
-// its keys' windows reach, of every query head of its group, which nothing bounds (a million
-// tile pairs, 64 heads of 2M queries on one key head, are over 2 s).  The planner
+// and the epilogue, which last a whole unit: a key tile meets every query tile of its
+// sequence (a windowed one those that its keys' windows reach, of every query head of its
+// group), a query tile every key tile, which nothing bounds (a million tile pairs, 64 heads
+// of 2M queries on one key head, are over 2 s).  The planner
 // therefore sizes each list's limit from the work it planned: a 2 s floor plus a
 // generous time per tile pair (kWaitNsPerTilePair, 10 to 30 times the 1 to 3.2 us that a
 // 128x128 tile pair takes in the kernels) for one CTA's share of the pairs and the costliest

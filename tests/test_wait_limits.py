@@ -11,6 +11,8 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 
 # barriers that a role meets only at an item's ends
 ITEM_LONG = {
+    "jfa_fwd.cu": {"q_empty": 1},
+    "jfa_bwd.cu": {"kv_empty": 2, "dv_full": 3, "dk_full": 3, "qdo_empty": 1, "acc_full": 1, "q_empty": 1, "dq_full": 2},
     "jfa_win_bwd.cu": {"kv_empty": 1, "dv_full": 2, "dk_full": 2, "qdo_empty": 1, "acc_full": 1},
     "jfa_win_dkdv.cu": {"kv_empty": 1},
 }
