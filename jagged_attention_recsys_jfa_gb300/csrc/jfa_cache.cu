@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
     if (tid == 0) {
       __threadfence();
       last_cta = atomicAdd(p.done, 1u) == gridDim.x - 1;
-      __threadfence();
+      if (last_cta) __threadfence();
     }
     __syncthreads();
     if (last_cta) {
