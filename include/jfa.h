@@ -216,8 +216,9 @@ size_t jfa_cache_workspace_size(int B, int H, int H_kv, int d);
  * form rot_dim / 2 pairs, pair i = (x_i, x_{i + rot_dim/2}), or (x_2i, x_2i+1) when
  * `interleaved`, and (a, b) becomes (a cos t - b sin t, b cos t + a sin t) with
  * t = position * frequencies[i]; `frequencies` is a HOST array of rot_dim / 2 doubles
- * (radians per position), read during the call.  Angles are exact to 2^-32 of a turn at any
- * position when the frequencies are.  Results are rounded to bf16 once.
+ * (radians per position), read during the call.  At any position sines and cosines are good to
+ * 2^-22 of their value and 2^-32 of a turn, frequencies up to 2^20 taken as exact.  Results are rounded
+ * to bf16 once.
  *
  * q (may be NULL) is rotated into q_out, contiguous [total][H][d]; with k_out non-NULL the
  * rotated keys are also written there, contiguous [total][H_kv][d] (for the prompt's own

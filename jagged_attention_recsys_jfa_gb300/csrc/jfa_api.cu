@@ -247,6 +247,20 @@ jfa_status window_maps(WinPlanMaps* maps, const Problem& pr, const void* q, cons
   return JFA_OK;
 }
 
+// x modulo one in units of 2^-64, to the nearest.
+uint64_t fraction64(double x) {
+  x -= std::rint(x);  // exact, in [-1/2, 1/2]
+  return x < 0.5 ? uint64_t(std::llrint(std::ldexp(x, 64))) : uint64_t(1) << 63;
+}
+// An angle in radians as a fraction of a turn in units of 2^-64.  1 / 2 pi = kHi + kLo to 2^-110, and
+// the product's rounding error is taken along: a quotient in double alone is off by 2^-26 of a turn
+// after 2^30 steps of one radian.
+uint64_t turn_of(double radians) {
+  constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+  const double hi = radians * kHi;
+  return fraction64(hi) + fraction64(std::fma(radians, kHi, -hi) + radians * kLo);
+}
+
 jfa_status check_workspace_bytes(void* ws, size_t bytes, size_t need) {
   return !ws || (reinterpret_cast<uintptr_t>(ws) & 255u) != 0 || bytes < need ? JFA_ERR_WORKSPACE : JFA_OK;
 }
@@ -511,9 +525,7 @@ jfa_status jfa_cache_append(const jfa_cache* cache, const void* k, int64_t k_str
                    interleaved ? 1 : 0, {}};
   for (int i = 0; i < rot_dim / 2; ++i) {
     if (!std::isfinite(frequencies[i])) return JFA_ERR_INVALID_ARG;
-    const double turns = frequencies[i] / 6.283185307179586476925;
-    const double frac = std::ldexp(turns - std::floor(turns), 64);  // of one turn per position, in 2^-64
-    a.turn[i] = frac < 18446744073709551616.0 ? uint64_t(frac) : 0;
+    a.turn[i] = turn_of(frequencies[i]);
   }
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;

@@ -22,9 +22,12 @@ __device__ __forceinline__ void raise_status(int* status, int code) { atomicCAS(
 //   half split   (x_i, x_{i + r/2})  ->  (x_i cos - x_{i+r/2} sin, x_{i+r/2} cos + x_i sin)
 //   interleaved  (x_2i, x_2i+1) likewise
 // The angle is kept as a fraction of a turn in 64-bit fixed point, turn_i = f_i / 2 pi mod 1
-// in units of 2^-64: p * turn_i wraps modulo one turn exactly, at any position, and its top
-// 32 bits give the angle to 2^-32 of a turn.  (In fp32 the product p * f_i alone is off by
-// 0.06 rad at p = 10^6.)  Memory bound: every row is read once and written once.
+// in units of 2^-64 (on the host, in twice double precision, to one unit for |f_i| up to 2^20):
+// p * turn_i wraps modulo one turn exactly and is off by 2^-33 of a turn at p = 2^31.  Its
+// distance to the nearest quarter turn is what becomes fp32, so that a sine or cosine next to
+// zero keeps its relative precision: both are good to 2^-22 of their value and 2^-32 of a turn.
+// (In fp32 the product p * f_i alone is off by 0.06 rad at p = 10^6.)  Memory bound: every row
+// is read once and written once.
 struct AppendParams {
   const __nv_bfloat16 *k, *v, *q;              // new rows; q may be nullptr
   int64_t k_stride, v_stride, q_stride;        // elements between tokens
@@ -149,10 +152,14 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
     float2* cs = cs_all[warp];
     for (int i = lane; i < p.rot / 2; i += 32) {
       const uint64_t turns = uint64_t(pos) * p.turn[i];
+      const uint32_t units = uint32_t((turns + (1ull << 31)) >> 32);  // of 2^-32 turns
+      const uint32_t quarter = (units + (1u << 29)) >> 30;             // the nearest quarter turn, 4 being 0
+      const int32_t rest = int32_t(units - (quarter << 30));           // behind it, at most an eighth
       float sn, cn;
-      // top 32 bits as a signed fraction of a turn: [-1/2, 1/2)
-      sincospif(float(int32_t(turns >> 32)) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31
-      cs[i] = make_float2(cn, sn);
+      sincospif(float(rest) * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: half turns
+      const float2 at_0 = make_float2(cn, sn), at_1 = make_float2(-sn, cn);
+      const float2 w1 = quarter & 1 ? at_1 : at_0;
+      cs[i] = quarter & 2 ? make_float2(-w1.x, -w1.y) : w1;
     }
     __syncwarp();
     float2 w[8];  // this lane's pairs: 8 of a split pair of chunks, 4 + 4 of two interleaved ones
