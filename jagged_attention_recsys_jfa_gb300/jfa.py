@@ -767,20 +767,22 @@ def _check_capture(*inputs):
     this graph was made on.  Made on the default stream, that is work which a capture cannot hold,
     and a backward pass captured then ends the process.  So an eager call there marks its leaves'
     accumulators, and a captured call refuses a marked one.  (A graph made on a side stream joins
-    the capture, and a mark is gone with its graph.)"""
-    leaves = [t for t in inputs if t.requires_grad and t.is_leaf]
+    the capture, and a mark is gone with its graph.)  Returns the accumulators, for the caller to
+    hold until its own graph does."""
+    leaves = [t for t in inputs if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad and t.is_leaf]
     if not leaves:
-        return
+        return ()
     capturing = torch.cuda.is_current_stream_capturing()
     if not capturing and torch.cuda.current_stream(leaves[0].device).cuda_stream != 0:
-        return
-    for t in leaves:
-        node = torch.autograd.graph.get_gradient_edge(t).node
+        return ()
+    nodes = [torch.autograd.graph.get_gradient_edge(t).node for t in leaves]
+    for node in nodes:
         if not capturing:
             node.metadata["jfa_default_stream"] = True
         elif node.metadata.get("jfa_default_stream"):
             raise RuntimeError("cannot capture this call: an eager graph of the same leaf tensors, made on the default "
                                "stream, is alive; drop its outputs first, or run eager steps on a side stream")
+    return nodes
 
 
 class WindowAttention(torch.autograd.Function):
@@ -788,9 +790,16 @@ class WindowAttention(torch.autograd.Function):
     kv_offsets, window, sinks, scale).  lse is saved for the backward, which cannot be
     differentiated again.  A step may be captured in a CUDA graph (see _check_capture)."""
 
+    @classmethod
+    def apply(cls, q, k, v, *args):
+        # no graph is made where no gradient is recorded (in inference mode neither): nothing to check
+        marked = _check_capture(q, k, v) if torch.is_grad_enabled() else ()
+        out = super().apply(q, k, v, *args)
+        del marked  # the graph holds them now
+        return out
+
     @staticmethod
     def forward(ctx, q, k, v, q_offsets, kv_offsets, window=None, sinks=0, scale=None):
-        _check_capture(q, k, v)
         out, lse, _ = jfa_window_forward(q, k, v, q_offsets, kv_offsets, window, sinks, scale)
         ctx.save_for_backward(q, k, v, out, lse, q_offsets, kv_offsets)
         ctx.cfg = (window, sinks, scale)

@@ -1,0 +1,56 @@
+"""Calls of the windowed attention that need no gradient, and malformed ones."""
+import pytest
+import torch
+
+import jagged_attention_recsys_jfa_gb300 as jfa
+from test_gpu_window import make
+
+pytestmark = pytest.mark.gpu
+
+
+def leaves(seed):
+    x, dout = make([140, 33], [140, 33], 2, 2, 64, seed)
+    want = jfa.jfa_window_forward(**x, window=20, sinks=2)[0]
+    for n in ("q", "k", "v"):
+        x[n].requires_grad_()
+    return x, dout, want
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_without_gradients(mode):
+    """Leaves that require a gradient may be given where none is recorded."""
+    x, _, want = leaves(70)
+    with mode():
+        out = jfa.window_attention(*x.values(), 20, 2)
+    assert torch.equal(out, want) and not out.requires_grad
+
+
+@pytest.mark.parametrize("mode", [torch.no_grad, torch.inference_mode])
+def test_captured_without_gradients(mode):
+    """Such a call accumulates nothing, so it is captured whatever eager graphs live; and it does not
+    keep a training step of the same leaves from being captured."""
+    x, dout, want = leaves(71)
+    eager = jfa.window_attention(*x.values(), 20, 2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph), mode():  # (a capture begun in inference mode leaves torch unable to begin another outside)
+        out = jfa.window_attention(*x.values(), 20, 2)
+    graph.replay()
+    assert torch.equal(out, want)
+    del eager
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        kept = jfa.window_attention(*x.values(), 20, 2)
+        kept.backward(dout, retain_graph=True)
+    torch.cuda.current_stream().wait_stream(side)
+    with mode():
+        jfa.window_attention(*x.values(), 20, 2)  # on the default stream, `kept` alive
+    first = [x[n].grad.clone() for n in ("q", "k", "v")]
+    for n in ("q", "k", "v"):
+        x[n].grad = None
+    step = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(step):
+        jfa.window_attention(*x.values(), 20, 2).backward(dout)
+    step.replay()
+    assert all(torch.equal(x[n].grad, g) for n, g in zip(("q", "k", "v"), first))
+    del kept
