@@ -361,6 +361,16 @@ def _require_rows(name, t, shape, device):
     raise ValueError(f"{name} is on {t.device}, the other tensors on {device}")
 
 
+def _require_offsets(name, t, n, device):
+    try:
+        if t.dtype is _I64 and t.shape == (n,) and n > 1 and t.is_contiguous() and t.device == device:
+            return
+    except AttributeError:
+        pass
+    _check_offsets(name, t)
+    raise ValueError(f"{name} must hold {n} offsets on {device}")
+
+
 def _require_lse(t, H, rows, device):
     _check_lse(t, H, rows)
     if t.device != device:
@@ -399,11 +409,11 @@ def _check_windowed(q, k, v, q_offsets, kv_offsets):
     device, (Tk, G, _) = q.device, k.shape
     _require_rows("k", k, (Tk, G, d), device)
     _require_rows("v", v, (Tk, G, d), device)
+    if not isinstance(q_offsets, torch.Tensor):
+        _check_offsets("q_offsets", q_offsets)
     n = q_offsets.numel()
-    for name, t in (("q_offsets", q_offsets), ("kv_offsets", kv_offsets)):
-        if not (t.dtype is _I64 and t.shape == (n,) and n > 1 and t.is_contiguous() and t.device == device):
-            _check_offsets(name, t)
-            raise ValueError(f"{name} must hold as many offsets as q_offsets, on {device}")
+    _require_offsets("q_offsets", q_offsets, n, device)
+    _require_offsets("kv_offsets", kv_offsets, n, device)
     return n - 1, Tq, H, G, d, Tk
 
 
@@ -580,9 +590,7 @@ def jfa_cache_append(k, v, offsets, k_cache, v_cache, page_table, lengths, q=Non
     device, G, d, B = k_cache.device, cache.H_kv, cache.d, cache.B
     T, k_ptr, k_step = _check_tokens("k", k, None, G, d, device)
     _, v_ptr, v_step = _check_tokens("v", v, T, G, d, device)
-    if not (offsets.dtype is _I64 and offsets.shape == (B + 1,) and offsets.is_contiguous() and offsets.device == device):
-        _check_offsets("offsets", offsets)
-        raise ValueError(f"offsets must have {B + 1} entries on {device}")
+    _require_offsets("offsets", offsets, B + 1, device)
     H, q_ptr, q_step = 0, None, 0
     if q is not None:
         _, q_ptr, q_step = _check_tokens("q", q, T, None, d, device)

@@ -54,3 +54,20 @@ def test_captured_without_gradients(mode):
     step.replay()
     assert all(torch.equal(x[n].grad, g) for n, g in zip(("q", "k", "v"), first))
     del kept
+
+
+def test_missing_offsets_are_refused():
+    x, dout, _ = leaves(72)
+    out, lse, _ = jfa.jfa_window_forward(**x, window=20)
+    for name in ("q_offsets", "kv_offsets"):
+        for bad in (None, [0, 140, 173]):
+            y = {**x, name: bad}
+            with pytest.raises(ValueError, match="offsets"):
+                jfa.jfa_window_forward(**y, window=20)
+            with pytest.raises(ValueError, match="offsets"):
+                jfa.jfa_window_backward(dout, y["q"], y["k"], y["v"], out, lse, y["q_offsets"], y["kv_offsets"], 20)
+    c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16, device="cuda:0")
+    t, n = torch.zeros(1, 4, dtype=torch.int32, device="cuda:0"), torch.zeros(1, dtype=torch.int32, device="cuda:0")
+    for bad in (None, [0, 173]):
+        with pytest.raises(ValueError, match="offsets"):
+            jfa.jfa_cache_append(x["k"].detach(), x["v"].detach(), bad, c, c.clone(), t, n)
