@@ -671,8 +671,10 @@ def jfa_cache_attention(q, k_cache, v_cache, page_table, lengths, window=None, s
 
 
 def jfa_check_status(workspace, stream=None) -> int:
-    """Synchronise the stream and return (and clear) the device status of the last call."""
-    return int(load_library().jfa_check_status(workspace.data_ptr(), _stream_handle(stream)))
+    """Synchronise `stream` (the workspace's device's current one) and return (and clear) the device
+    status of the last call on that workspace."""
+    lib = load_library()
+    return _call(workspace.device, stream, lambda handle: int(lib.jfa_check_status(workspace.data_ptr(), handle)))
 
 
 def jfa_set_nsp_max_tiles(max_tiles: int) -> int:

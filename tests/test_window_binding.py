@@ -1,4 +1,7 @@
 """The windowed call's autograd binding on the CPU: what it does before the library is called."""
+import contextlib
+import types
+
 import pytest
 import torch
 
@@ -28,3 +31,33 @@ def test_no_graph_no_check(mode, monkeypatch):
         out = jfa.window_attention(*x, off, off)
     assert not seen and not out.requires_grad
     assert jfa.window_attention(*x, off, off).requires_grad and len(seen) == 1
+
+
+def test_status_is_read_on_the_workspaces_device(monkeypatch):
+    """The stream that is waited for is one of the device that the workspace, and so the call, is on."""
+    current, calls = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    @contextlib.contextmanager
+    def stream(s):
+        with device(s.device):
+            yield
+
+    lib = types.SimpleNamespace(jfa_check_status=lambda ptr, handle: calls.append((ptr, handle, current[0])) or 0)
+    monkeypatch.setattr(jfa.jfa, "load_library", lambda *a: lib)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: types.SimpleNamespace(cuda_stream=1000 + current[0]))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 1000 + i, raising=False)
+    ws = types.SimpleNamespace(device=torch.device("cuda", 1), data_ptr=lambda: 4096)
+    assert jfa.jfa_check_status(ws) == 0 and calls == [(4096, 1001, 1)]
+    side = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=77)
+    assert jfa.jfa_check_status(ws, side) == 0 and calls[1] == (4096, 77, 1) and current == [0]
+    with pytest.raises(ValueError, match="stream"):
+        jfa.jfa_check_status(ws, types.SimpleNamespace(device=torch.device("cuda", 0), cuda_stream=5))
