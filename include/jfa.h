@@ -139,10 +139,11 @@ jfa_status jfa_backward(const void* dout, const void* q, const void* k, const vo
  * with the visible key tiles, not with the sequence length squared.  Keys that no query of their
  * sequence sees (when queries follow a longer history) are not read: they may hold anything,
  * NaN included, and get zero gradients.  A non-finite value in a key or value that some query
- * sees may reach every row of that sequence and head, in out and in the gradients.  A row one of
- * whose scores is NaN (or +inf) gets out = NaN and lse = NaN; lse = -inf means that it sees no key
- * (or that all its scores are -inf).  dk and dv sum over the group's query heads in fp32, in a fixed
- * order (results are bit-reproducible). */
+ * sees, or in dout, may reach every row of that sequence and head, in out and in the gradients.  A
+ * row one of whose scores is NaN (or +inf) gets out = NaN and lse = NaN; lse = -inf means that it
+ * sees no key (or that all its scores are -inf).  Outputs must not overlap inputs or one another
+ * (equal pointers are refused), but out may be q, and dq may be q, dout or out.  dk and dv sum over
+ * the group's query heads in fp32, in a fixed order (results are bit-reproducible). */
 size_t jfa_window_workspace_size(int B, int H, int H_kv, int d, int64_t total_q, int64_t total_kv, int sinks,
                                  int is_backward);
 jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const int64_t* q_offsets,

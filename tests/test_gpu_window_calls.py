@@ -71,3 +71,19 @@ def test_missing_offsets_are_refused():
     for bad in (None, [0, 173]):
         with pytest.raises(ValueError, match="offsets"):
             jfa.jfa_cache_append(x["k"].detach(), x["v"].detach(), bad, c, c.clone(), t, n)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_outputs_in_the_place_of_queries(d):
+    """out may be q, and dq may be q, dout or out."""
+    x, dout = make([300, 0, 5, 129], [300, 7, 5, 200], 4, 2, d, 73)
+    want, wl, _ = jfa.jfa_window_forward(**x, window=40, sinks=3)
+    q = x["q"].clone()
+    out, lse, ws = jfa.jfa_window_forward(**{**x, "q": q}, window=40, sinks=3, out=q)
+    assert jfa.jfa_check_status(ws) == 0 and torch.equal(out, want) and torch.equal(lse, wl)
+    rest = (wl, x["q_offsets"], x["kv_offsets"], 40, 3)
+    ref = jfa.jfa_window_backward(dout, x["q"], x["k"], x["v"], want, *rest)[:3]
+    for i in range(3):
+        a = [dout.clone(), x["q"].clone(), want.clone()]
+        got = jfa.jfa_window_backward(a[0], a[1], x["k"], x["v"], a[2], *rest, dq=a[i])[:3]
+        assert all(torch.equal(s, t) for s, t in zip(got, ref))
