@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
   constexpr int kLanes = D / 16, kSlots = 32 / kLanes;  // lanes per row, rows a warp takes at a time
   constexpr int kWarps = kAppendThreads / 32;
   __shared__ __align__(16) float2 cs_all[kWarps][D / 2];  // cos, sin of each warp's token
-  __shared__ bool last_cta;
+  __shared__ bool last_cta, errors;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -220,13 +220,16 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
     if (tid == 0) {
       __threadfence();
       last_cta = atomicAdd(p.done, 1u) == gridDim.x - 1;
-      if (last_cta) __threadfence();
+      if (last_cta) {
+        __threadfence();
+        // an error of this call (or an earlier one that nobody has asked for) is in *status by now:
+        // then each sequence is looked at for tokens that were not stored.  (One thread reads it: the
+        // CTA must agree, whoever clears it meanwhile.)
+        errors = *static_cast<volatile const int*>(p.status) != 0;
+      }
     }
     __syncthreads();
     if (last_cta) {
-      // an error of this call (or an earlier one that nobody has asked for) is in *status by now:
-      // then each sequence is looked at for tokens that were not stored
-      const bool errors = *static_cast<volatile const int*>(p.status) != 0;
       bool bad = false;
       if (errors) {
         for (int b = tid; b < p.B; b += kAppendThreads) bad |= p.offsets[b + 1] < p.offsets[b];
