@@ -418,13 +418,13 @@ jfa_status jfa_window_forward(const void* q, const void* k, const void* v, const
   if (total_q > 0 && (!q || !out || !lse || !aligned16(q) || !aligned16(out) || !aligned16(lse)))
     return JFA_ERR_INVALID_ARG;
   if (total_kv > 0 && (!k || !v || !aligned16(k) || !aligned16(v))) return JFA_ERR_INVALID_ARG;
-  // (out may be q: a query tile is written once it has been read)
-  if (total_q > 0 && total_kv > 0 && (out == k || out == v)) return JFA_ERR_INVALID_ARG;
   if (total_q == 0) return JFA_OK;  // no rows: nothing to enqueue
   Problem pr = make_problem(B, H, d, total_q, total_kv, q_offsets, kv_offsets, nullptr, scale, 1);
   pr.win = WindowSpec{window < kMaxWindow ? window : kMaxWindow, sinks, H_kv};
   const WsLayout L = make_layout(B, H, d, total_q, total_kv, false, false, pr.win);
   if ((st = check_workspace(workspace, workspace_bytes, L)) != JFA_OK) return st;
+  // (out may be q: a query tile is written once it has been read)
+  if (total_q > 0 && total_kv > 0 && (out == k || out == v)) return JFA_ERR_INVALID_ARG;
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -456,16 +456,16 @@ jfa_status jfa_window_backward(const void* dout, const void* q, const void* k, c
     return JFA_ERR_INVALID_ARG;
   if (total_kv > 0 && (!k || !v || !dk || !dv || !aligned16(k) || !aligned16(v) || !aligned16(dk) || !aligned16(dv)))
     return JFA_ERR_INVALID_ARG;
-  // outputs in the place of what a later item or pass still reads, or writes (dq may be q, dout or out)
-  if (total_kv > 0 && (dk == dv || dk == k || dk == v || dv == k || dv == v)) return JFA_ERR_INVALID_ARG;
-  if (total_q > 0 && total_kv > 0 && (dk == q || dk == dout || dv == q || dv == dout || dq == k || dq == v || dq == dk || dq == dv))
-    return JFA_ERR_INVALID_ARG;
   if (total_q == 0 && total_kv == 0) return JFA_OK;  // no rows: nothing to enqueue
   Problem pr = make_problem(B, H, d, total_q, total_kv, q_offsets, kv_offsets, nullptr, scale, 1);
   pr.win = WindowSpec{window < kMaxWindow ? window : kMaxWindow, sinks, H_kv};
   pr.nsp_max_tiles = 0;
   const WsLayout L = make_layout(B, H, d, total_q, total_kv, true, false, pr.win);
   if ((st = check_workspace(workspace, workspace_bytes, L)) != JFA_OK) return st;
+  // outputs in the place of what a later item or pass still reads, or writes (dq may be q, dout or out)
+  if (total_kv > 0 && (dk == dv || dk == k || dk == v || dv == k || dv == v)) return JFA_ERR_INVALID_ARG;
+  if (total_q > 0 && total_kv > 0 && (dk == q || dk == dout || dv == q || dv == dout || dq == k || dq == v || dq == dk || dq == dv))
+    return JFA_ERR_INVALID_ARG;
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

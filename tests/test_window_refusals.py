@@ -31,19 +31,15 @@ def test_arguments(call, over, status):
     assert call(**over) == status
 
 
+ROOM = dict(ws=256, wsb=1 << 30)  # these are looked at last
+
+
 @pytest.mark.parametrize("over", [dict(out=32), dict(out=48)])
 def test_forward_outputs_in_the_place_of_keys(over):
-    assert forward(**over) == INVALID
+    assert forward(**over, **ROOM) == INVALID
 
 
 @pytest.mark.parametrize("over", [dict(dk=32), dict(dk=48), dict(dv=32), dict(dv=48), dict(dk=160), dict(dk=16), dict(dv=16),
                                   dict(dk=112), dict(dv=112), dict(dq=32), dict(dq=48), dict(dq=144), dict(dq=160)])
 def test_backward_outputs_in_the_place_of_inputs(over):
-    assert backward(**over) == INVALID
-
-
-@pytest.mark.parametrize("call,over", [(forward, dict(out=16)), (backward, dict(dq=16)), (backward, dict(dq=112)),
-                                       (backward, dict(dq=80))])
-def test_outputs_in_the_place_of_queries(call, over):
-    """Allowed: only the workspace is missing."""
-    assert call(**over) == WORKSPACE
+    assert backward(**over, **ROOM) == INVALID
