@@ -95,7 +95,7 @@ __device__ __forceinline__ bool stores_all(const AppendParams& p, int b, int len
 // where they are a half-split pair's halves, else neighbours, so that both elements of every pair
 // meet in one lane.  A lane's pairs are the same in every row of the token, so its 8 sines and
 // cosines stay in registers for all heads (read again for every row from shared memory, the call
-// took 166 us on 841 MB instead of 150, 5.6 TB/s).  The first rows' loads are under way while the
+// took 166 us on 841 MB instead of 150; now 147, 5.7 TB/s).  The first rows' loads are under way while the
 // token's sequence, page and angles are found.
 template <int D>
 __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_constant__ AppendParams p) {
@@ -248,10 +248,13 @@ __global__ void __launch_bounds__(kAppendThreads, 5) append_kernel(const __grid_
 }
 
 // ================================================================== attention over the cache
-// One query token per sequence, G = H / H_kv query heads per key/value head.  Memory bound:
-// each visible key and value row is read once, for all G heads (4 d G flops per 4 d bytes).
-// 2.35 GB (128 sequences of up to 16384 tokens, 4 heads of d = 128 read by 16, pages of 64): 349 us,
-// 6.73 TB/s, the rate of a plain copy; 996 MB of two sequences 163 us; 189 MB in pages of 16 41 us.
+// One query token per sequence, G = H / H_kv query heads per key/value head.  Memory bound: each
+// visible key and value row is read once per block of 16 query heads (4 d G flops per 4 d bytes up to
+// G = 16; 537 MB of 128 x 8192 tokens of one head: 101 us for 8 query heads, 109 for 16, 185 for 32,
+// 332 for 64).  2.35 GB (128 sequences of up to 16384 tokens, 4 heads of d = 128 read by 16, pages
+// of 64): 347 us, 6.77 TB/s, the rate of a plain copy; 996 MB of two sequences 162 us; 189 MB in
+// pages of 16 41 us.  Not near that rate: few units of many rows, whose joins one CTA each does
+// (2 x 400000 tokens of one head, 410 MB: 153 us for 1 query head, 307 for 8, 518 for 16).
 //
 // Keys are walked in tiles of 64.  A unit is (sequence, kv head, block of 16 query heads);
 // the tiles of all units, in order, are dealt out evenly: CTA x of n takes tiles

@@ -15,7 +15,8 @@
 // 4 key/value heads, window 512, 16 sinks) and the plain dK/dV pass keeps its 0.699 ms (0.714 with
 // the window's branches in the code it shared).  Of the 773 the dK/dV pass is 298, dQ 235, forward
 // 154, preprocess 50, join 10; the floor of the step's products is 190.
-// P and dS are rounded to bf16 as operands (at most 2^-8 relative a term); sums are fp32.
+// P and dS are rounded to bf16 as operands (at most 2^-8 relative a term), and D = rowsum(dO o out) is
+// formed from the bf16 out that the forward wrote, as in the plain call; sums are fp32.
 // Bound by the tensor pipe with its operands and results in TMEM (4150 cycles per 128 x 128 pair of
 // the dK/dV pass, as in the plain call).
 #include <cuda_bf16.h>

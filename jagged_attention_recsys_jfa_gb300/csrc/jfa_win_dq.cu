@@ -4,7 +4,8 @@
 //
 // Built like the windowed forward (jfa_win.cu), for the same reason: an item is a few short steps
 // whose hand-offs, not their products, set the pace, so two CTAs share an SM, each with half of its
-// shared and tensor memory.  At d = 128 a CTA's tiles would not fit half of the shared memory.
+// shared and tensor memory.  (At d = 128 Q, dO and one stage of K and V take 97 of the 112 KB that a
+// CTA would have: room for no second stage, and not tried.)
 // 62 us (64 sequences of up to 2048 tokens, 4 query and 2 key/value heads, window 256, 4 sinks), with
 // every tile through its sequence's maps 86; one CTA per SM with 128-key steps took 93.  2048
 // sequences of up to 96 tokens: 157 us instead of 282.

@@ -8,9 +8,9 @@ pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
 
 
-@pytest.mark.parametrize("d,tiles", [(64, 208), (128, 288)])
+@pytest.mark.parametrize("d,tiles", [(64, 256), (128, 288)])
 def test_key_tiles_of_a_large_group(d, tiles):
-    """The first key tile sums over 4096 x `tiles` query tiles, 2 s and more.  Keys are zeros, so P_ij =
+    """The first key tile sums over 4096 x `tiles` query tiles, 2.5 and 3.6 s.  Keys are zeros, so P_ij =
     1 / (i + 1) for j <= i; values ones, so out = 1, dS = 0, and with dout = 1 in a few heads dv_j =
     sum over i >= j of (number of those heads) / (i + 1).  Everything that is zero or one is exact; P
     is off by half a bf16 step (and by the roundings of lse, below 16, and its product with log2 e: 2^-19),
