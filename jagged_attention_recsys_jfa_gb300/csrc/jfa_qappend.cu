@@ -94,7 +94,8 @@ __global__ void __launch_bounds__(kQAppendThreads, D == 64 ? 3 : 2) qappend_kern
     const int e = p.interleaved ? chunk / kLanes * 2 + (pair >> 1 & 1) : pair >> 1 & 3;
     pair_cs = reinterpret_cast<float*>(cs + e * kLanes + in_lane) + (pair & 1);
   }
-  int turn = 0, in_stage = 0, out_stage = 0;  // the ring's next stage to read, to copy into
+  // which of the two buffers of maxima a team uses next; the ring's next stage to read, to copy into
+  int turn, in_stage = 0, out_stage = 0;
 
   auto number = [&](int s) { return (__ldg(p.offsets + s) >> lb) + 2 * int64_t(s); };
   const int64_t numbers = (p.total >> lb) + 2 * int64_t(p.B);
@@ -192,6 +193,7 @@ __global__ void __launch_bounds__(kQAppendThreads, D == 64 ? 3 : 2) qappend_kern
       if (pg < p.max_pages) page = __ldg(p.page_table + int64_t(b) * p.max_pages + pg);
       copy_ahead();
       __syncthreads();  // the block in front is done with its angles and maxima
+      turn = 0;         // (its teams may have been others, whose warps took different numbers of heads)
       if (pair < pairs) {
         uint64_t turns = uint64_t(start + 16 * v.g0 + tid / kPairs) * pair_turn;
         float* to = pair_cs + (tid / kPairs) * 16 * kLanes;
