@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kQAppendThreads, D == 64 ? 3 : 2) qappend_kern
             m = __reduce_max_sync(0xffffffffu, team_max[turn][(warp & ~(team_size - 1)) + (lane & (team_size - 1))]);
           }
           scale = scale_for<kInt8>(m, is_k && p.rot > 0);
-          if (old && !(fabsf(s_old) <= scale)) scale = s_old;  // larger, or NaN
+          if (old && (fabsf(s_old) > scale || s_old != s_old)) scale = s_old;  // (a new scale that is NaN stays)
           if (stored) {
             if (old && scale != s_old && scale == scale) {  // earlier rows' codes at the new scale
               const float f = s_old / scale;

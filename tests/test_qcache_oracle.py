@@ -115,6 +115,23 @@ def test_append_by_hand(kind):
     assert np.all(lo[0] == 0) and np.all(lo[1, 0, 3:] == 0)
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_append_not_finite_by_hand(kind, value):
+    """A value that is not finite makes its block's scale NaN, behind earlier tokens too; so does an earlier scale."""
+    codes, scales = np.full((2, 2, 16, 64), 5.0), np.full((2, 2, 1), 2.0 ** -3)
+    x = np.ones((2, 2, 64))
+    x[1, 0, 7] = value
+    lo, hi, s = qo.append(codes, scales, np.array([[1]]), [3], [2], x, kind)
+    assert np.isnan(s[1, 0, 0]) and s[1, 1, 0] == 2.0 ** -3 and np.all(s[0] == 2.0 ** -3)
+    assert np.all(np.isneginf(lo[1, 0, 3:5])) and np.all(np.isposinf(hi[1, 0, 3:5])) and np.all(lo[1, 0, :3] == 5.0)
+    assert np.all(lo[1, 1, 3:5] == 8.0) and np.array_equal(lo[1, 1], hi[1, 1])
+    lo, hi, s = qo.append(codes, s, np.array([[1]]), [5], [1], np.ones((1, 2, 64)), kind)
+    assert np.isnan(s[1, 0, 0]) and s[1, 1, 0] == 2.0 ** -3
+    lo, hi, s = qo.append(codes, s, np.array([[1]]), [0], [1], np.ones((1, 2, 64)), kind)
+    assert s[1, 0, 0] == s[1, 1, 0] == qo.needed_scale(1.0, kind, False) and np.array_equal(lo, hi)
+
+
 def test_pages_by_hand():
     table = np.full((3, 4), -1)
     table[0, :2], table[2, 0] = [7, 8], 9
