@@ -261,7 +261,9 @@ __global__ void __launch_bounds__(kQAppendThreads, D == 64 ? 3 : 2) qappend_kern
                 uint32_t lo, hi;
                 codes_f16<kInt8>(*at, lo, hi);
                 const float2 a = f16x2_floats(lo), z = f16x2_floats(hi);
-                *at = to_codes<kInt8>(a.x * f, a.y * f, z.x * f, z.y * f);
+                // (a code of -128, of another origin, by a factor of -1: 127 is the nearest)
+                auto top = [](float x) { return kInt8 ? fminf(x, 127.f) : x; };
+                *at = to_codes<kInt8>(top(a.x * f), top(a.y * f), top(z.x * f), top(z.y * f));
               }
             }
             if (in_team == 0 && lane == 0) *scale_at = scale;

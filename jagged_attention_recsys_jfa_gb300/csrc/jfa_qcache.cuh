@@ -19,7 +19,7 @@ __device__ __forceinline__ void codes_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     hi = e4m3_hi_f16x2(w);
   }
 }
-// Four values as codes, to the nearest, ties to even (int8: |x| <= 127, added to 1.5 * 2^23, whose last bit is 1).
+// Four values as codes, to the nearest, ties to even (int8: -128 <= x <= 127, added to 1.5 * 2^23).
 template <bool kInt8>
 __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
   if (kInt8) {

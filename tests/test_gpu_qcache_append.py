@@ -80,3 +80,18 @@ def test_append_not_finite_behind_earlier_tokens(kind, value, rot, page, block, 
     assert bool(torch.isnan(ks[at[0], 1, at[1]])) and bool(torch.isnan(vs[at[0], 0, at[1]]))
     assert int(torch.isnan(ks).sum()) == int(torch.isnan(vs).sum()) == 1
     assert jfa.jfa_check_status(ws) == 0
+
+
+@pytest.mark.parametrize("old", [-2.0 ** -5, 2.0 ** -5, -2.0 ** -6, -0.999 * 2.0 ** -5, 0.999 * 2.0 ** -5])
+def test_append_behind_the_lowest_int8_code(old):
+    """Earlier codes of -128, of another origin, become the nearest ones at a scale that is exactly minus theirs, or next
+    to it.  (The new rows need 2^-5: their largest element lies between 127 / 64 and 127 / 32.)"""
+    start = filled(gen(33), [40, 40], 2, 64, 32, 32, "int8")
+    for codes, scales in (start[:1] + start[2:3], start[1:2] + start[3:4]):
+        codes[:, :, ::2] = -128
+        scales.fill_(old)
+    check_append([5, 37], [3, 2], 2, 1, 64, 32, 32, "int8", 0, start=start)
+    first, second = start[4][0, 0].long(), start[4][1, 1].long()
+    for codes, scales in (start[:1] + start[2:3], start[1:2] + start[3:4]):
+        assert bool((scales[first] == 2.0 ** -5).all()) and bool((scales[second] == 2.0 ** -5).all())
+        assert bool((codes[first, :, 0:5:2] == {-2.0 ** -5: 127, -2.0 ** -6: 64, -0.999 * 2.0 ** -5: 127}.get(old, -128)).all())

@@ -132,6 +132,15 @@ def test_append_not_finite_by_hand(kind, value):
     assert s[1, 0, 0] == s[1, 1, 0] == qo.needed_scale(1.0, kind, False) and np.array_equal(lo, hi)
 
 
+def test_append_behind_the_lowest_int8_code():
+    """-128 stays where its scale does, and becomes the nearest code where that changes: 127 by a factor of -1."""
+    for old, want in ((2.0 ** -5, -128), (-2.0 ** -5, 127), (-2.0 ** -6, 64), (2.0 ** -6, -64), (0.996 * 2.0 ** -5, -127),
+                      (0.999 * 2.0 ** -5, -128), (-0.999 * 2.0 ** -5, 127)):
+        codes, scales = np.full((1, 1, 16, 64), -128.0), np.full((1, 1, 1), old)
+        lo, hi, s = qo.append(codes, scales, np.array([[0]]), [3], [1], np.full((1, 1, 64), 3.0), "int8")
+        assert s[0, 0, 0] == 2.0 ** -5 and np.all(lo[0, 0, :3] == want) and np.array_equal(lo, hi)
+
+
 def test_pages_by_hand():
     table = np.full((3, 4), -1)
     table[0, :2], table[2, 0] = [7, 8], 9
