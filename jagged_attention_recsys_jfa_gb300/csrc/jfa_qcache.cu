@@ -655,11 +655,14 @@ __global__ void __launch_bounds__(QCfg<D, NT>::kThreads, QCfg<D, NT>::kCtasPerSm
         }
       }
       named_bar_sync(1, kThreads);
+      // (O^T holds sums of up to 2^15 n codes, so that next to the smallest ref its factor is too small for a float: there
+      // the factor is 2^60 times as large until it has been applied)
+      const float up = ref < 8.6736174e-19f ? 1.1529215e18f : 1.f, down = ref < 8.6736174e-19f ? 8.6736174e-19f : 1.f;
       float out_f[NT][2];
 #pragma unroll
       for (int t8 = 0; t8 < NT; ++t8)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) out_f[t8][k] = weights[warp * C::kHeads + t8 * 8 + 2 * c + k].x * ref * (1.f / 128.f);
+        for (int k = 0; k < 2; ++k) out_f[t8][k] = weights[warp * C::kHeads + t8 * 8 + 2 * c + k].x * up * ref * (1.f / 128.f);
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += 32) {
         named_bar_sync(1, kThreads);  // the weights, or the previous columns, have been read
@@ -671,7 +674,7 @@ __global__ void __launch_bounds__(QCfg<D, NT>::kThreads, QCfg<D, NT>::kCtasPerSm
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float* v = o[c0 / 16 + j][t8];
-              *reinterpret_cast<float2*>(row + 16 * j + 2 * g) = make_float2(v[k] * out_f[t8][k], v[2 + k] * out_f[t8][k]);
+              *reinterpret_cast<float2*>(row + 16 * j + 2 * g) = make_float2(v[k] * out_f[t8][k] * down, v[2 + k] * out_f[t8][k] * down);
             }
           }
         named_bar_sync(1, kThreads);
