@@ -269,11 +269,13 @@ typedef struct {
  * Keys are rotated in fp32 and rounded to codes once (k_out: to bf16 once).  A block's scale is the smallest
  * power of two, 2^-126 at least, with which the largest code (448, 127) holds the block's new values, or sqrt(2)
  * times the largest element of the block's new keys where keys are rotated; or the scale it has, where tokens
- * of the block that came before these have a larger one (one of another origin may be negative: its magnitude counts).  When it grows, the codes of those are rounded
- * again: a block is one sequence's to append to, only whole blocks may be shared.  Codes are to the nearest
+ * of the block that came before these have a larger one (one of another origin may be negative: its magnitude
+ * counts).  When it grows, the codes of those are rounded again (int8 codes may be -128): a block is one sequence's
+ * to append to, only whole blocks may be shared.  Codes are to the nearest
  * of value / scale, ties to even (by a scale of another origin that is no power of two: of value times 1 / scale
  * in fp32).  Where a new value of a block and head is not finite, the block's scale
- * becomes NaN, and stays so until its first token is written again.  Workspace: 256 bytes, as there. */
+ * becomes NaN, and stays so until its first token is written again.  (Powers of two cost e4m3 nothing but range;
+ * of int8 a code's step is up to 2, with rotated keys 2 sqrt(2), times the block's largest |x| / 127.)  Workspace: 256 bytes, as there. */
 jfa_status jfa_qcache_append(const jfa_qcache* cache, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                              const void* q, int64_t q_stride, int H, const int64_t* offsets, int64_t total,
                              const double* frequencies, int rot_dim, int interleaved, void* q_out, void* k_out,
@@ -282,7 +284,7 @@ jfa_status jfa_qcache_append(const jfa_qcache* cache, const void* k, int64_t k_s
 /* jfa_cache_attention over such a cache, with scales of any origin and value: the same arguments, mask, results
  * and errors, and the same workspace (jfa_cache_workspace_size).  What codes and scales hold that show no key
  * does not matter.  Products and sums run on the codes as they are; the weights of the values are rounded to
- * f16 (2^-11 relative; those that are below 2^-21 of the largest with their scales, to 2^-32 of that).  A NaN in
+ * f16 (2^-11 relative; those that are below 2^-21 of the largest, or of 2^-126, with their scales, to 2^-32 of that).  A NaN in
  * a visible key's codes or scale gives its head out = NaN and lse = NaN, one in a value's out = NaN.  out may be q. */
 jfa_status jfa_qcache_attention(const jfa_qcache* cache, const void* q, int H, int window, int sinks, float scale,
                                 void* out, float* lse, void* workspace, size_t workspace_bytes, jfa_stream_t stream);

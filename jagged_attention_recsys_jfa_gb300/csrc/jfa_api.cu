@@ -645,7 +645,7 @@ jfa_status jfa_qcache_append(const jfa_qcache* cache, const void* k, int64_t k_s
   if ((st = check_append_args(cache->cache, k, k_stride, v, v_stride, q, q_stride, H, offsets, total, frequencies, rot_dim, interleaved,
                               q_out, k_out, lengths_out, workspace, workspace_bytes, &a)) != JFA_OK)
     return st;
-  // the grid's first axis numbers the blocks (jfa_qcache.cu)
+  // the grid's first axis has at most as many CTAs as there are numbers of blocks (jfa_qappend.cu)
   if (total / cache->block + 2 * int64_t(cache->cache.B) >= (int64_t(1) << 31)) return JFA_ERR_INVALID_ARG;
   const int nsm = sm_count();
   if (nsm <= 0) return JFA_ERR_CUDA;

@@ -142,7 +142,8 @@ struct WsHeader {
   uint64_t wait_ns[5];
   int n_nsp;       // number of non-sequence-parallel backward items
   int planned;     // 1: the last plan found the offsets well formed
-  unsigned append_done;  // cache append: CTAs that have read the lengths (written by no other call, left at 0)
+  unsigned append_done;  // appends and page calls: CTAs that have read what the last one writes (written by no other
+                         // call, one call at a time, left at 0)
   int counters_used;     // 1: the cache attentions' counters (kGroupAt on) may hold anything: another call's
                          // layout has reached them, or a wait of that call ran out
   int pad[38];

@@ -150,7 +150,7 @@ cudaError_t launch_cache_attention(const jfa_cache& c, const CUtensorMap& k_map,
                                    int H, int window, int sinks, float scale, void* out, float* lse, void* ws,
                                    int num_sms, cudaStream_t stream);
 
-// ---- the same held in 8 bits (jfa_qcache.cu); maps of 128-byte lines, boxes of qcache_box_rows rows
+// ---- the same held in 8 bits (jfa_qappend.cu, jfa_qcache.cu); maps of 128-byte lines, boxes of qcache_box_rows rows
 int qcache_box_rows(int page_size);
 cudaError_t launch_qcache_append(const jfa_qcache& c, const CacheAppend& a, void* ws, int num_sms, cudaStream_t stream);
 cudaError_t launch_qcache_attention(const jfa_qcache& c, const CUtensorMap& k_map, const CUtensorMap& v_map, const void* q,

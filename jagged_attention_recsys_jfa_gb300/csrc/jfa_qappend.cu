@@ -12,6 +12,10 @@ namespace {
 // codes, so that all roundings of a value together stay below one step of the block's last scale.  A new
 // value that is not finite makes the block's scale NaN.  Scales of another origin may have any value.
 //
+// What a power of two costs: of e4m3 nothing but range.  Of int8 a code's step is up to 2, with rotated keys 2 sqrt(2),
+// times max |x| / 127, the smallest with which the block's new values fit: the largest of them is 64 steps at least, of
+// rotated keys 45 before they are turned.
+//
 // With bits m of max |x| as bf16 (exponent E = m >> 7, fraction f = m & 127): M s >= c max |x| for
 // s = 2^(E - 127 - kBase + (f > kLimit)), M / c = (1 + x) 2^kBase, kLimit = floor(128 x):
 //   448 = 1.75 * 2^8, 448 / sqrt(2) = 1.2374 * 2^8, 127 = 1.984375 * 2^6, 127 / sqrt(2) = 1.4031 * 2^6.
@@ -57,8 +61,8 @@ __device__ __forceinline__ float2 turned(uint64_t turns) {
 //
 // Measured: 740 MB of rotated prompts, 4 + 4 + 16 heads of 128, blocks of 32: 139 us, 5300 GB/s, a quarter more
 // than the floor: reads and writes together, and the warps' latency (47% of the issue slots are taken).  102 MB of 64-dim
-// heads without queries, blocks of 128: 39 us: the latency of a head (5300 clk a warp, eight heads one behind the
-// other) and 640 blocks over 456 CTAs.  64 decoding tokens of 8 heads: 8 us in a replayed graph.
+// heads without queries, blocks of 128: 39 us: what bounds it is this form, rows that go through shared memory (5300 clk
+// for a warp's head, eight heads one behind the other, 24 warps an SM) and whole blocks to a CTA (640 over 456 CTAs).  64 decoding tokens of 8 heads: 8 us in a replayed graph.
 //
 // Blocks are numbered without a sum over the sequences: sequence b's are offsets[b] / block + 2 b + i, which leaves
 // each at least the (n - 2) / block + 2 that n tokens can touch; other numbers stay empty.

@@ -7,7 +7,9 @@
 // Measured (e4m3, d = 128 unless stated; GB/s of codes, scales and rows): 936 MB of 128 sequences, 4 heads to a
 // key, 144 us, 6500 GB/s: memory; 451 MB of two sequences, 77 us, 5830: some 10 us are the way to the first tile and
 // the join of 152 partials at the end; 210 MB with 32 heads to a key, 71 us: its warps' latency, 2100 clk for a
-// tile of 128 keys with two warps to a scheduler; 95 MB in windows, 33 us: the same ends.
+// tile of 128 keys with two warps to a scheduler; 95 MB in windows, 33 us: the first tile is there after 5 (a CTA's
+// sum of the lengths, the page, the copy), a CTA's tiles take 20 in the median (4800 GB/s; the first CTA is done with
+// them at 21, the last at 28), and its joins another 4.
 //
 // Codes are exact in f16, and so the products run in f16 with fp32 sums, m16n8k16, keys (or output columns)
 // as the 16 rows and 8 query heads as the columns, so that a code is converted once for all heads of a block:
@@ -16,14 +18,14 @@
 // P = exp2(s - base), base being a maximum that is raised only where a score exceeds it by more than 8 (then O^T
 // and the sums are rescaled): P <= 2^8.  P is rounded to f16 as an operand, at most 2^-11 relative a term.  A
 // 16-key group has one value scale vs, which multiplies its P before that: P' = 2^7 P vs / r, r being the
-// largest |vs| met so far.  P' keeps f16's 11 bits down to 2^-14, so terms lose relative precision only where
+// largest |vs| met so far (2^-126 at least).  P' keeps f16's 11 bits down to 2^-14, so terms lose relative precision only where
 // P vs is below 2^-21 of the largest scale, and are then off by 2^-32 of that.
 //
 // Work is dealt as in the bf16 kernel (jfa_cache.cuh), in tiles of 128 keys, a unit counting kExtra tiles more for
 // its query and its join.  Up to 16 heads, four warps take 32 keys of each tile, two CTAs to an SM; above, eight
-// warps take 16 keys (at d = 64 of two tiles at a time), one CTA to an SM, with q in shared memory.  A unit whose tiles lie in several CTAs is
-// joined from their partial rows, in a fixed order: by the CTA that finishes last, and where there are many, by
-// the last of each 16 first.
+// warps take 16 keys (at d = 64 of two tiles at a time), one CTA to an SM, with q in shared memory.  A unit whose tiles
+// lie in several CTAs is joined from their partial rows, in a fixed order: by the CTA that finishes last, and where
+// there are many, by the last of each 16 first.
 #include "jfa_qcache.cuh"
 
 namespace jfa {

@@ -750,7 +750,9 @@ def jfa_qcache_append(k, v, offsets, k_cache, v_cache, k_scale, v_scale, page_ta
     float32 [num_pages, H_kv, page_size / block], one scale for each aligned block of 16, 32, 64 or 128 tokens of a
     page and head; a value is code * scale.  Scales are powers of two that hold the block's values; where a
     later token needs a larger one, the block's earlier codes are rounded again (so a block that is not full
-    belongs to one sequence).  A value that is not finite makes its block's scale NaN.  Everything else is as for
+    belongs to one sequence).  A value that is not finite makes its block's scale NaN.  (Powers of two cost e4m3
+    nothing but range; of int8 a code's step is up to 2, with rotated keys 2 sqrt(2), times the block's largest |x| / 127.
+    Codes with other scales, made elsewhere, serve as well.)  Everything else is as for
     jfa_cache_append: k, v and q bf16, the rotation, the other outputs, lengths, errors.
     """
     qc = _qcache_struct(k_cache, v_cache, k_scale, v_scale, page_table, lengths)
