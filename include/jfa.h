@@ -284,8 +284,10 @@ jfa_status jfa_qcache_append(const jfa_qcache* cache, const void* k, int64_t k_s
 /* jfa_cache_attention over such a cache, with scales of any origin and value: the same arguments, mask, results
  * and errors, and the same workspace (jfa_cache_workspace_size).  What codes and scales hold that show no key
  * does not matter.  Products and sums run on the codes as they are; the weights of the values are rounded to
- * f16 (2^-11 relative; those that are below 2^-21 of the largest, or of 2^-126, with their scales, to 2^-32 of that).  A NaN in
- * a visible key's codes or scale gives its head out = NaN and lse = NaN, one in a value's out = NaN.  out may be q. */
+ * f16 (2^-11 relative; those that are below 2^-21 of the largest, or of 2^-126, with their scales, to 2^-32 of that).
+ * Scores are fp32 products of a head's factor, its largest |q| to a power of two times scale, and the key's scale: a
+ * factor below 2^-112 has fewer bits, which counts where key scales are above 2^90.  A NaN in a visible key's codes
+ * or scale gives its head out = NaN and lse = NaN, one in a value's out = NaN.  out may be q. */
 jfa_status jfa_qcache_attention(const jfa_qcache* cache, const void* q, int H, int window, int sinks, float scale,
                                 void* out, float* lse, void* workspace, size_t workspace_bytes, jfa_stream_t stream);
 
